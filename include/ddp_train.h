@@ -1,0 +1,110 @@
+/*
+ * ddp_train.h -- C ABI of the operators around the gradient sync of
+ * ddp_ring.h, on the same MI355X (gfx950): what makes the gradients where the
+ * sync reads them, and what reads them after it (the global gradient norm,
+ * clipping, an AdamW step).
+ *
+ * In the step of "DDP 与 Ring All-Reduce" (blog.vllbc.top), section 05, the
+ * optimizer is what step 5 hands the reduced gradients to. The operators
+ * themselves are written from the formulas given with each.
+ *
+ * Conventions: those of ddp_ring.h (status codes, ddp_last_error, device
+ * pointers checked against their allocations before anything is launched,
+ * host arrays of device pointers, work enqueued on `stream` without waiting,
+ * DDP_FP32 / DDP_BF16). In addition:
+ *   - All sums are held in fp32 or wider; a bf16 result is rounded once, to
+ *     nearest, ties to even.
+ *   - Results do not depend on the order in which blocks run: no floating
+ *     point atomics are used, so a call repeated on the same inputs gives the
+ *     same bits.
+ *   - Every call except the create and free functions can be captured in a
+ *     graph.
+ */
+#ifndef DDP_TRAIN_H
+#define DDP_TRAIN_H
+
+#include <stdint.h>
+
+#include "ddp_ring.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* ---------------------------------------------------------------- gradient norm, clipping
+ * A ddp_grads is a set of gradient tensors (one rank's, or any others on one
+ * device) whose places stay the same from step to step, as those of a
+ * gradient arena (ddp_plan_grad_arena) do.
+ *
+ * ddp_grads_create: grads[n] are device pointers (host array, copied), each
+ *   aligned to its element size and numels[i] >= 0 contiguous elements of
+ *   `dtype`, pairwise disjoint; an empty tensor's pointer may be NULL. n >= 0.
+ *   The set belongs to the current device: a table of 16 bytes per 8192
+ *   elements (one entry at least per tensor that is not empty) and 16 KiB of scratch are
+ *   allocated there. The tensors must stay allocated while the set exists.
+ *   Calls on one set share its scratch: they must be ordered (one stream, or
+ *   streams that wait for each other). */
+typedef struct ddp_grads ddp_grads;
+int ddp_grads_create(void* const* grads, const int64_t* numels, int32_t n, int32_t dtype, ddp_grads** out);
+
+/* Releases a set (NULL is accepted); no work that uses it, and no ddp_adamw
+ * made from it, may be left. */
+void ddp_grads_free(ddp_grads* grads);
+
+/* ddp_grads_norm: *norm_dev (a device float, overwritten) receives
+ *   DDP_NORM_L2:  sqrt(sum g^2) over every element of every tensor;
+ *   DDP_NORM_MAX: max |g|.
+ * The squares are summed in fp64, so no finite fp32 gradient overflows or
+ * vanishes on the way. A NaN element makes the norm NaN, an infinite one (without NaN)
+ * infinite; an empty set's norm is 0. One launch. */
+#define DDP_NORM_L2 0
+#define DDP_NORM_MAX 1
+int ddp_grads_norm(ddp_grads* grads, int32_t kind, float* norm_dev, void* stream);
+
+/* ddp_grads_clip: into = rnd(g * f), f = min(1, max_norm / (*norm_dev + 1e-6)),
+ * element by element. `into` is a set of the same element counts (of either
+ * dtype), none of whose tensors overlaps one of `grads`, or NULL to scale
+ * `grads` in place, where a factor of 1 leaves the gradients untouched. *norm_dev is
+ * read when the launch runs: the value of ddp_grads_norm on the same stream, or one
+ * combined from several sets' by the caller. A NaN norm gives NaN gradients;
+ * an infinite one gives f = 0. max_norm >= 0 (infinity: never clip a finite norm). */
+int ddp_grads_clip(const ddp_grads* grads, const ddp_grads* into, float max_norm, const float* norm_dev,
+                   void* stream);
+
+/* ---------------------------------------------------------------- AdamW
+ * ddp_adamw_create: an optimizer over the set's tensors. For tensor i of n
+ *   (the set's n), params[i], exp_avg[i] and exp_avg_sq[i] are fp32 device
+ *   arrays of the gradient's element count; params_bf16 (NULL for none) gives
+ *   bf16 arrays that receive the rounded new weights; decay (NULL: all 1)
+ *   holds 1 for tensors that weight decay applies to, else 0. *step_dev is a
+ *   device int64, the number of steps done (0 at first). Everything but the
+ *   gradients is written, so none of it may overlap anything else. The pointers
+ *   are copied into a device table; the set must outlive the optimizer. */
+typedef struct ddp_adamw ddp_adamw;
+int ddp_adamw_create(const ddp_grads* grads, void* const* params, void* const* exp_avg, void* const* exp_avg_sq,
+                     void* const* params_bf16, const uint8_t* decay, int64_t* step_dev, ddp_adamw** out);
+
+/* Releases an optimizer (NULL is accepted); no work that uses it may be left. */
+void ddp_adamw_free(ddp_adamw* opt);
+
+/* ddp_adamw_step: one AdamW step in one launch. With t = *step_dev + 1 and
+ * f = 1 if norm_dev is NULL, else min(1, max_norm / (*norm_dev + 1e-6)):
+ *   g = f * grad
+ *   m = beta1 m + (1 - beta1) g
+ *   v = beta2 v + (1 - beta2) g^2
+ *   p = (1 - lr * weight_decay [if the tensor decays]) p
+ *       - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps)
+ *   params_bf16 = rnd(p); *step_dev = t.
+ * The gradients are left as they are: clipping costs no pass of its own. If
+ * norm_dev is given and *norm_dev is not finite, the step is skipped: nothing
+ * is written. lr, eps, weight_decay and max_norm >= 0; beta1 and beta2 in
+ * [0, 1). max_norm is not looked at without norm_dev. Calls on one optimizer
+ * must be ordered. */
+int ddp_adamw_step(ddp_adamw* opt, double lr, double beta1, double beta2, double eps, double weight_decay,
+                   double max_norm, const float* norm_dev, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* DDP_TRAIN_H */

@@ -1,7 +1,8 @@
 """Python binding of libddp_ring.so: the bucketed ring all-reduce of DDP
 gradients over N virtual ranks on one MI355X.
 
-The functions have the names of the C entry points in include/ddp_ring.h and
+The functions have the names of the C entry points in include/ddp_ring.h (the
+operators around the sync, of include/ddp_train.h, drop the ddp_ prefix) and
 only marshal arguments: torch tensors become device pointers, dtypes become
 DDP_FP32 / DDP_BF16, and the stream defaults to torch's current stream. Every
 step of the computation runs in the library's HIP kernels; there is no other
@@ -53,6 +54,7 @@ def _load():
                           "`python -m ring_all_reduce_ddp_amd.build` (hipcc, gfx950)")
     lib = ctypes.CDLL(LIB_PATH)
     vp, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+    f64 = ctypes.c_double
     pp = ctypes.POINTER(ctypes.c_void_p)
     sig = {
         "ddp_last_error": (ctypes.c_char_p, []),
@@ -91,6 +93,14 @@ def _load():
         "ddp_copy_probe": (ctypes.c_int, [vp, vp, i64, vp]),
         "ddp_device_alloc": (ctypes.c_int, [i64, i32, ctypes.POINTER(vp)]),
         "ddp_device_free": (ctypes.c_int, [vp]),
+        "ddp_grads_create": (ctypes.c_int, [pp, ctypes.POINTER(i64), i32, i32, ctypes.POINTER(vp)]),
+        "ddp_grads_free": (None, [vp]),
+        "ddp_grads_norm": (ctypes.c_int, [vp, i32, vp, vp]),
+        "ddp_grads_clip": (ctypes.c_int, [vp, vp, f32, vp, vp]),
+        "ddp_adamw_create": (ctypes.c_int, [vp, pp, pp, pp, pp, ctypes.POINTER(ctypes.c_uint8), vp,
+                                            ctypes.POINTER(vp)]),
+        "ddp_adamw_free": (None, [vp]),
+        "ddp_adamw_step": (ctypes.c_int, [vp, f64, f64, f64, f64, f64, f64, vp, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -495,3 +505,130 @@ def ddp_copy_probe(dst, src, nbytes=None, stream=None):
         nbytes = src.numel() * src.element_size()
     _check(_get_lib().ddp_copy_probe(ctypes.c_void_p(_ptr(dst)), ctypes.c_void_p(_ptr(src)), int(nbytes),
                               _stream(stream)))
+
+
+# ---------------------------------------------------------------- around the sync (ddp_train.h)
+
+NORMS = {"l2": 0, "max": 1}
+
+
+def _stream_context(stream):
+    """Allocations made under it belong to `stream` (None: the current one)."""
+    if stream is None:
+        return torch.cuda.stream(None)
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+
+
+def _device_tensors(tensors, dtype, numels, what):
+    tensors = list(tensors)
+    if numels is not None and len(tensors) != len(numels):
+        raise ValueError(f"{what}: {len(tensors)} tensors for {len(numels)} gradients")
+    for i, t in enumerate(tensors):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous() or t.dtype != dtype:
+            raise ValueError(f"{what}[{i}] must be a contiguous {dtype} tensor on the GPU")
+        if numels is not None and t.numel() != numels[i]:
+            raise ValueError(f"{what}[{i}] has {t.numel()} elements, its gradient {numels[i]}")
+    return tensors
+
+
+class GradSet:
+    """A set of gradient tensors at fixed places (views of a gradient arena,
+    or any others of one dtype on one device): their global norm, and clipping
+    (see ddp_grads_* in include/ddp_train.h). Keeps the tensors alive."""
+
+    def __init__(self, tensors):
+        tensors = list(tensors)
+        dtype = tensors[0].dtype if tensors else torch.float32
+        self.dtype = dtype_code(dtype)
+        self.tensors = _device_tensors(tensors, dtype, None, "grads")
+        self.numels = [t.numel() for t in self.tensors]
+        n = len(self.tensors)
+        numels = (ctypes.c_int64 * max(n, 1))(*self.numels)
+        h = ctypes.c_void_p()
+        _check(_get_lib().ddp_grads_create(_ptr_array(self.tensors), numels, n, self.dtype, ctypes.byref(h)))
+        self._h = h.value
+
+    def norm(self, kind="l2", out=None, stream=None):
+        """The norm, as a float32 device tensor of one element (`out` if given)."""
+        if out is None:
+            with _stream_context(stream):
+                out = torch.empty((), dtype=torch.float32, device="cuda")
+        elif out.dtype != torch.float32 or out.numel() != 1:
+            raise ValueError("out must hold one float32")
+        _check(_get_lib().ddp_grads_norm(self._h, NORMS[kind], out.data_ptr(), _stream(stream)))
+        return out
+
+    def clip(self, max_norm, norm, into=None, stream=None):
+        """Scales the gradients by min(1, max_norm / (norm + 1e-6)), in place
+        or into another GradSet; `norm` is a float32 device tensor."""
+        if norm.dtype != torch.float32 or norm.numel() != 1:
+            raise ValueError("norm must hold one float32")
+        _check(_get_lib().ddp_grads_clip(self._h, None if into is None else into._h, float(max_norm),
+                                         norm.data_ptr(), _stream(stream)))
+
+    def free(self):
+        if self._h:
+            _get_lib().ddp_grads_free(self._h)
+            self._h = None
+
+    def __del__(self, _finalizing=sys.is_finalizing):
+        if _finalizing():   # as for Plan: no HIP calls during shutdown
+            return
+        try:
+            self.free()
+        except Exception:
+            pass
+
+
+class AdamW:
+    """AdamW on fp32 parameters whose gradients are the GradSet `grads` (see
+    ddp_adamw_* in include/ddp_train.h). params, exp_avg, exp_avg_sq: float32
+    tensors, one per gradient; steps: an int64 device tensor of one element,
+    the steps done; params_bf16: tensors that receive the rounded weights;
+    decay: per tensor, whether weight decay applies (None: to all). The
+    tensors are updated in place and kept alive."""
+
+    def __init__(self, grads, params, exp_avg, exp_avg_sq, steps, params_bf16=None, decay=None):
+        if steps.dtype != torch.int64 or steps.numel() != 1:
+            raise ValueError("steps must hold one int64")
+        n = len(grads.numels)
+        if decay is not None and len(decay) != n:
+            raise ValueError(f"decay: {len(decay)} entries for {n} gradients")
+        self.grads = grads   # the set must outlive the optimizer
+        self.params = _device_tensors(params, torch.float32, grads.numels, "params")
+        self.exp_avg = _device_tensors(exp_avg, torch.float32, grads.numels, "exp_avg")
+        self.exp_avg_sq = _device_tensors(exp_avg_sq, torch.float32, grads.numels, "exp_avg_sq")
+        self.params_bf16 = None if params_bf16 is None else \
+            _device_tensors(params_bf16, torch.bfloat16, grads.numels, "params_bf16")
+        self.steps = steps
+        flags = None if decay is None else (ctypes.c_uint8 * max(n, 1))(*[1 if d else 0 for d in decay])
+        h = ctypes.c_void_p()
+        _check(_get_lib().ddp_adamw_create(grads._h, _ptr_array(self.params), _ptr_array(self.exp_avg),
+                                           _ptr_array(self.exp_avg_sq),
+                                           None if params_bf16 is None else _ptr_array(self.params_bf16), flags,
+                                           steps.data_ptr(), ctypes.byref(h)))
+        self._h = h.value
+
+    def step(self, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, max_norm=None, norm=None, stream=None):
+        """One step. With `norm` (a float32 device tensor) and max_norm the
+        gradients count as clipped, and a norm that is not finite skips it."""
+        if (norm is None) != (max_norm is None):
+            raise ValueError("norm and max_norm go together")
+        if norm is not None and (norm.dtype != torch.float32 or norm.numel() != 1):
+            raise ValueError("norm must hold one float32")
+        _check(_get_lib().ddp_adamw_step(self._h, float(lr), float(betas[0]), float(betas[1]), float(eps),
+                                         float(weight_decay), 0.0 if max_norm is None else float(max_norm),
+                                         None if norm is None else norm.data_ptr(), _stream(stream)))
+
+    def free(self):
+        if self._h:
+            _get_lib().ddp_adamw_free(self._h)
+            self._h = None
+
+    def __del__(self, _finalizing=sys.is_finalizing):
+        if _finalizing():   # as for Plan: no HIP calls during shutdown
+            return
+        try:
+            self.free()
+        except Exception:
+            pass

@@ -1,0 +1,370 @@
+// The global norm of a set of gradient tensors, and clipping by it.
+//
+//   norm = sqrt(sum over all tensors and elements of g^2)   (or max |g|)
+//   clip: g <- rnd(g * min(1, max_norm / (norm + 1e-6)))
+//
+// Both stream the gradients: two flops a byte at most, so the bound is memory.
+// The set's tile table maps a block to a run of one tensor with one scalar
+// load (no search over tensors, no launch per tensor).
+#include <algorithm>
+#include <cmath>
+#include <new>
+
+#include "train_internal.h"
+
+namespace ddp {
+
+bool spans_overlap(const void* a, int64_t abytes, const void* b, int64_t bbytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return abytes > 0 && bbytes > 0 && x < y + uint64_t(bbytes) && y < x + uint64_t(abytes);
+}
+
+namespace {
+
+std::string span_name(const Span& s) {
+  return s.index < 0 ? std::string(s.what) : std::string(s.what) + "[" + std::to_string(s.index) + "]";
+}
+
+template <int DT>
+struct Elem;
+template <>
+struct Elem<DDP_FP32> {
+  static constexpr int V = 4;
+  static __device__ __forceinline__ u32x4 load(const void* p, int64_t e) {
+    return *reinterpret_cast<const u32x4_at4*>(static_cast<const float*>(p) + e);
+  }
+};
+template <>
+struct Elem<DDP_BF16> {
+  static constexpr int V = 8;
+  static __device__ __forceinline__ u32x4 load(const void* p, int64_t e) {
+    return *reinterpret_cast<const u32x4_at2*>(static_cast<const uint16_t*>(p) + e);
+  }
+};
+
+// Running sum of squares, or largest magnitude, of one thread.
+//
+// The squares are added in fp64: an fp32 square overflows from 1.8e19 and
+// vanishes below 1e-23, and a sum of 1e9 of them loses digits. fp64 runs at
+// half the fp32 rate here, far from the bound of a stream.
+template <int KIND>
+struct Norm;
+template <>
+struct Norm<DDP_NORM_L2> {
+  double s[2] = {0.0, 0.0};
+  __device__ __forceinline__ void add(float x, int k) { s[k & 1] = fma(double(x), double(x), s[k & 1]); }
+  __device__ __forceinline__ double value() const { return s[0] + s[1]; }
+  static __device__ __forceinline__ double join(double a, double b) { return a + b; }
+  static __device__ __forceinline__ float finish(double s) { return float(sqrt(s)); }
+};
+// Magnitudes compare as the integers of their bits, NaN above infinity, so a
+// NaN survives every comparison. The partial travels as the double of that
+// integer, which is exact.
+template <>
+struct Norm<DDP_NORM_MAX> {
+  uint32_t m[2] = {0u, 0u};
+  __device__ __forceinline__ void add(float x, int k) {
+    const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
+    m[k & 1] = b > m[k & 1] ? b : m[k & 1];
+  }
+  __device__ __forceinline__ double value() const { return double(m[0] > m[1] ? m[0] : m[1]); }
+  static __device__ __forceinline__ double join(double a, double b) { return a > b ? a : b; }
+  static __device__ __forceinline__ float finish(double s) { return __uint_as_float(uint32_t(s)); }
+};
+
+// The block's 256 values joined in a fixed order; valid in thread 0.
+template <int KIND>
+__device__ __forceinline__ double block_join(double v) {
+  __shared__ double wave[kThreads / 64];
+  for (int d = 32; d > 0; d >>= 1) v = Norm<KIND>::join(v, __shfl_down(v, d));
+  if ((threadIdx.x & 63) == 0) wave[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = wave[0];
+  for (int w = 1; w < kThreads / 64; ++w) v = Norm<KIND>::join(v, wave[w]);
+  __syncthreads();
+  return v;
+}
+
+// One launch: every block leaves one fp64 partial, and the block whose ticket
+// is the last joins them, in index order whichever block that is, so the
+// result does not depend on the order of arrival.
+template <int DT, int KIND>
+__global__ __launch_bounds__(kThreads) void k_grads_norm(const GradTile* tiles, int64_t n_tiles, double* partials,
+                                                         unsigned int* ticket, float* norm) {
+  using E = Elem<DT>;
+  constexpr int V = E::V;
+  constexpr int U = kGradTile / (kThreads * V);
+  Norm<KIND> acc;
+  for (int64_t t = blockIdx.x; t < n_tiles; t += gridDim.x) {
+    const GradTile tile = tiles[t];
+    if (tile.count == kGradTile) {
+      u32x4 x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) x[u] = E::load(tile.p, (u * kThreads + int(threadIdx.x)) * V);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const typename Ops<DT>::Acc a = Ops<DT>::from(x[u]);
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc.add(a.v[i], i);
+      }
+    } else {
+      const int vecs = tile.count / V;
+      for (int i = threadIdx.x; i < vecs; i += kThreads) {
+        const typename Ops<DT>::Acc a = Ops<DT>::from(E::load(tile.p, i * V));
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc.add(a.v[j], j);
+      }
+      const int e = vecs * V + int(threadIdx.x);
+      if (e < tile.count) acc.add(Ops<DT>::load1(tile.p, e), 0);
+    }
+  }
+  const double mine = block_join<KIND>(acc.value());
+  if (gridDim.x == 1) {
+    if (threadIdx.x == 0) *norm = Norm<KIND>::finish(mine);
+    return;
+  }
+  __shared__ bool last;
+  if (threadIdx.x == 0) {
+    __hip_atomic_store(&partials[blockIdx.x], mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const unsigned int k = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    last = k == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  double s = 0.0;
+  for (unsigned int i = threadIdx.x; i < gridDim.x; i += kThreads)
+    s = Norm<KIND>::join(s, __hip_atomic_load(&partials[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+  s = block_join<KIND>(s);
+  if (threadIdx.x == 0) {
+    *norm = Norm<KIND>::finish(s);
+    __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next launch
+  }
+}
+
+template <int SRC, int DST>
+__global__ __launch_bounds__(kThreads) void k_grads_clip(const GradTile* src, const GradTile* dst, int64_t n_tiles,
+                                                         float max_norm, const float* norm) {
+  const float q = max_norm / (*norm + 1e-6f);
+  const float f = q >= 1.0f ? 1.0f : q;  // a NaN stays
+  if (src == dst && f == 1.0f) return;   // in place, nothing to do
+  constexpr int E = 4;
+  for (int64_t t = blockIdx.x; t < n_tiles; t += gridDim.x) {
+    const GradTile a = src[t];
+    void* const to = dst[t].p;
+    const int vecs = a.count / E;
+    for (int i = threadIdx.x; i < vecs; i += kThreads) {
+      float x[E];
+      if constexpr (SRC == DDP_FP32) {
+        const u32x4 w = reinterpret_cast<const u32x4_at4*>(a.p)[i];
+        for (int j = 0; j < E; ++j) x[j] = __uint_as_float(w[j]) * f;
+      } else {
+        const u32x2 w = reinterpret_cast<const u32x2_at2*>(a.p)[i];
+        x[0] = bf16_lo(w.x) * f, x[1] = bf16_hi(w.x) * f, x[2] = bf16_lo(w.y) * f, x[3] = bf16_hi(w.y) * f;
+      }
+      if constexpr (DST == DDP_FP32)
+        reinterpret_cast<u32x4_at4*>(to)[i] =
+            u32x4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
+      else
+        reinterpret_cast<u32x2_at2*>(to)[i] = u32x2{round_bf16x2(x[0], x[1]), round_bf16x2(x[2], x[3])};
+    }
+    const int e = vecs * E + int(threadIdx.x);
+    if (e < a.count) {
+      const float x = Ops<SRC>::load1(a.p, e) * f;
+      Ops<DST>::store1(to, e, DST == DDP_BF16 ? round_bf16(x) : x);
+    }
+  }
+}
+
+// The sets' tensors against each other: at once if the sets lie apart as
+// wholes (two arenas), else tensor by tensor.
+int check_sets_disjoint(const ddp_grads& a, const ddp_grads& b, const char* fn) {
+  if (a.hi <= b.lo || b.hi <= a.lo) return DDP_OK;
+  try {
+    std::vector<Span> spans;
+    for (size_t i = 0; i < a.ptrs.size(); ++i) {
+      spans.push_back({a.ptrs[i], a.numels[i] * elem_bytes(a.dtype), "grads", int32_t(i)});
+      spans.push_back({b.ptrs[i], b.numels[i] * elem_bytes(b.dtype), "into", int32_t(i)});
+    }
+    return check_disjoint(spans, fn);
+  } catch (const std::bad_alloc&) {
+    return fail(DDP_ENOMEM, std::string(fn) + ": out of host memory");
+  }
+}
+
+unsigned stream_grid(int64_t tiles, int64_t most) { return unsigned(std::max<int64_t>(1, std::min(tiles, most))); }
+
+}  // namespace
+
+int check_disjoint(std::vector<Span>& spans, const char* fn) {
+  spans.erase(std::remove_if(spans.begin(), spans.end(), [](const Span& s) { return s.bytes == 0; }), spans.end());
+  std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) {
+    return reinterpret_cast<uintptr_t>(a.p) < reinterpret_cast<uintptr_t>(b.p);
+  });
+  for (size_t i = 1; i < spans.size(); ++i)
+    if (spans_overlap(spans[i - 1].p, spans[i - 1].bytes, spans[i].p, spans[i].bytes))
+      return fail(DDP_EINVAL, std::string(fn) + ": " + span_name(spans[i - 1]) + " and " + span_name(spans[i]) + " overlap");
+  return DDP_OK;
+}
+
+int check_scalar(const void* p, int64_t bytes, const char* fn, const char* what) {
+  int st = check_range(p, bytes, fn, what);
+  if (st != DDP_OK) return st;
+  if (reinterpret_cast<uintptr_t>(p) % uintptr_t(bytes) != 0)
+    return fail(DDP_EINVAL, std::string(fn) + ": " + what + " is not " + std::to_string(bytes) + "-byte aligned");
+  return DDP_OK;
+}
+
+int check_device(int dev, const char* fn) {
+  int now = 0;
+  DDP_HIP_TRY(hipGetDevice(&now), fn);
+  if (now != dev) return fail(DDP_EINVAL, std::string(fn) + ": the current device is not the one it was created on");
+  return DDP_OK;
+}
+
+}  // namespace ddp
+
+using namespace ddp;
+
+extern "C" int ddp_grads_create(void* const* grads, const int64_t* numels, int32_t n, int32_t dtype, ddp_grads** out) {
+  const char* fn = "ddp_grads_create";
+  if (out == nullptr) return fail(DDP_EINVAL, std::string(fn) + ": out is NULL");
+  *out = nullptr;
+  if (!valid_dtype(dtype)) return fail(DDP_EINVAL, std::string(fn) + ": unknown dtype");
+  if (n < 0) return fail(DDP_EINVAL, std::string(fn) + ": n is negative");
+  if (n > 0 && (grads == nullptr || numels == nullptr)) return fail(DDP_EINVAL, std::string(fn) + ": an array is NULL");
+  const int eb = elem_bytes(dtype);
+  ddp_grads* g = nullptr;
+  try {
+    std::vector<Span> spans;
+    for (int32_t i = 0; i < n; ++i) {
+      if (numels[i] < 0 || numels[i] > (int64_t(1) << 48))
+        return fail(DDP_EINVAL, std::string(fn) + ": numels[" + std::to_string(i) + "] out of range");
+      const std::string what = "grads[" + std::to_string(i) + "]";
+      if (reinterpret_cast<uintptr_t>(grads[i]) % uintptr_t(eb) != 0 && numels[i] > 0)
+        return fail(DDP_EINVAL, std::string(fn) + ": " + what + " is not aligned to its element");
+      int st = check_range(grads[i], numels[i] * eb, fn, what.c_str());
+      if (st != DDP_OK) return st;
+      spans.push_back({grads[i], numels[i] * eb, "grads", i});
+    }
+    int st = check_disjoint(spans, fn);
+    if (st != DDP_OK) return st;
+    std::vector<GradTile> tiles;
+    int64_t total = 0;
+    uintptr_t lo = UINTPTR_MAX, hi = 0;
+    for (int32_t i = 0; i < n; ++i) {
+      if (numels[i] == 0) continue;
+      total += numels[i];
+      lo = std::min(lo, reinterpret_cast<uintptr_t>(grads[i]));
+      hi = std::max(hi, reinterpret_cast<uintptr_t>(grads[i]) + uintptr_t(numels[i] * eb));
+      for (int64_t e = 0; e < numels[i]; e += kGradTile)
+        tiles.push_back({static_cast<char*>(grads[i]) + e * eb, int32_t(std::min<int64_t>(kGradTile, numels[i] - e)), i});
+    }
+    g = new ddp_grads;
+    g->dtype = dtype;
+    if (n > 0) {
+      g->ptrs.assign(grads, grads + n);
+      g->numels.assign(numels, numels + n);
+    }
+    g->total = total;
+    g->lo = lo;
+    g->hi = hi;
+    g->n_tiles = int64_t(tiles.size());
+    const size_t table = size_t(round_up(int64_t(sizeof(GradTile) * tiles.size()), 256));
+    const size_t scratch = sizeof(double) * kNormBlocks + 256;
+    hipError_t e = hipGetDevice(&g->dev);
+    if (e == hipSuccess) {
+      e = hipMalloc(&g->memory, table + scratch);
+      if (e != hipSuccess) {
+        (void)hipGetLastError();
+        delete g;
+        return fail(DDP_ENOMEM, std::string(fn) + ": hipMalloc: " + hipGetErrorString(e));
+      }
+    }
+    char* base = static_cast<char*>(g->memory);
+    if (e == hipSuccess && !tiles.empty())
+      e = hipMemcpy(base, tiles.data(), sizeof(GradTile) * tiles.size(), hipMemcpyHostToDevice);
+    if (e == hipSuccess) {
+      const std::vector<char> zeros(scratch, 0);
+      e = hipMemcpy(base + table, zeros.data(), scratch, hipMemcpyHostToDevice);
+    }
+    if (e != hipSuccess) {
+      if (g->memory != nullptr) (void)hipFree(g->memory);
+      delete g;
+      return hip_fail(e, "ddp_grads_create: tables");
+    }
+    g->tiles = reinterpret_cast<GradTile*>(base);
+    g->partials = reinterpret_cast<double*>(base + table);
+    g->ticket = reinterpret_cast<unsigned int*>(base + table + sizeof(double) * kNormBlocks);
+    *out = g;
+    return DDP_OK;
+  } catch (const std::bad_alloc&) {
+    if (g != nullptr && g->memory != nullptr) (void)hipFree(g->memory);
+    delete g;
+    return fail(DDP_ENOMEM, std::string(fn) + ": out of host memory");
+  }
+}
+
+extern "C" void ddp_grads_free(ddp_grads* g) {
+  if (g == nullptr) return;
+  (void)hipFree(g->memory);
+  delete g;
+}
+
+extern "C" int ddp_grads_norm(ddp_grads* g, int32_t kind, float* norm_dev, void* stream) {
+  const char* fn = "ddp_grads_norm";
+  if (g == nullptr) return fail(DDP_EINVAL, std::string(fn) + ": grads is NULL");
+  if (kind != DDP_NORM_L2 && kind != DDP_NORM_MAX) return fail(DDP_EINVAL, std::string(fn) + ": unknown kind");
+  int st = check_device(g->dev, fn);
+  if (st != DDP_OK) return st;
+  st = check_scalar(norm_dev, 4, fn, "norm_dev");
+  if (st != DDP_OK) return st;
+  const dim3 grid(stream_grid(g->n_tiles, kNormBlocks)), block(kThreads);
+  hipStream_t s = as_stream(stream);
+  if (g->dtype == DDP_FP32) {
+    if (kind == DDP_NORM_L2)
+      hipLaunchKernelGGL((k_grads_norm<DDP_FP32, DDP_NORM_L2>), grid, block, 0, s, g->tiles, g->n_tiles, g->partials, g->ticket, norm_dev);
+    else
+      hipLaunchKernelGGL((k_grads_norm<DDP_FP32, DDP_NORM_MAX>), grid, block, 0, s, g->tiles, g->n_tiles, g->partials, g->ticket, norm_dev);
+  } else {
+    if (kind == DDP_NORM_L2)
+      hipLaunchKernelGGL((k_grads_norm<DDP_BF16, DDP_NORM_L2>), grid, block, 0, s, g->tiles, g->n_tiles, g->partials, g->ticket, norm_dev);
+    else
+      hipLaunchKernelGGL((k_grads_norm<DDP_BF16, DDP_NORM_MAX>), grid, block, 0, s, g->tiles, g->n_tiles, g->partials, g->ticket, norm_dev);
+  }
+  DDP_HIP_TRY(hipGetLastError(), "ddp_grads_norm: launch");
+  return DDP_OK;
+}
+
+extern "C" int ddp_grads_clip(const ddp_grads* g, const ddp_grads* into, float max_norm, const float* norm_dev,
+                              void* stream) {
+  const char* fn = "ddp_grads_clip";
+  if (g == nullptr) return fail(DDP_EINVAL, std::string(fn) + ": grads is NULL");
+  if (!(max_norm >= 0.0f)) return fail(DDP_EINVAL, std::string(fn) + ": max_norm is negative or not a number");
+  int st = check_device(g->dev, fn);
+  if (st != DDP_OK) return st;
+  if (into == nullptr) into = g;
+  if (into != g) {
+    if (into->dev != g->dev) return fail(DDP_EINVAL, std::string(fn) + ": the sets are on different devices");
+    if (into->numels != g->numels) return fail(DDP_EINVAL, std::string(fn) + ": the sets' element counts differ");
+    st = check_sets_disjoint(*g, *into, fn);
+    if (st != DDP_OK) return st;
+  }
+  st = check_scalar(norm_dev, 4, fn, "norm_dev");
+  if (st != DDP_OK) return st;
+  if (g->n_tiles == 0) return DDP_OK;
+  const dim3 grid(stream_grid(g->n_tiles, 1 << 16)), block(kThreads);
+  hipStream_t s = as_stream(stream);
+  if (g->dtype == DDP_FP32) {
+    if (into->dtype == DDP_FP32)
+      hipLaunchKernelGGL((k_grads_clip<DDP_FP32, DDP_FP32>), grid, block, 0, s, g->tiles, into->tiles, g->n_tiles, max_norm, norm_dev);
+    else
+      hipLaunchKernelGGL((k_grads_clip<DDP_FP32, DDP_BF16>), grid, block, 0, s, g->tiles, into->tiles, g->n_tiles, max_norm, norm_dev);
+  } else {
+    if (into->dtype == DDP_FP32)
+      hipLaunchKernelGGL((k_grads_clip<DDP_BF16, DDP_FP32>), grid, block, 0, s, g->tiles, into->tiles, g->n_tiles, max_norm, norm_dev);
+    else
+      hipLaunchKernelGGL((k_grads_clip<DDP_BF16, DDP_BF16>), grid, block, 0, s, g->tiles, into->tiles, g->n_tiles, max_norm, norm_dev);
+  }
+  DDP_HIP_TRY(hipGetLastError(), "ddp_grads_clip: launch");
+  return DDP_OK;
+}
