@@ -40,7 +40,7 @@ extern "C" {
  *   aligned to its element size and numels[i] >= 0 contiguous elements of
  *   `dtype`, pairwise disjoint; an empty tensor's pointer may be NULL. n >= 0.
  *   The set belongs to the current device: a table of 16 bytes per 8192
- *   elements (one entry at least per tensor that is not empty) and 16 KiB of scratch are
+ *   elements (one entry at least per tensor that is not empty) and 17 KiB of scratch are
  *   allocated there. The tensors must stay allocated while the set exists.
  *   Calls on one set share its scratch: they must be ordered (one stream, or
  *   streams that wait for each other). */

@@ -25,7 +25,11 @@ struct AdamTile {
   int32_t count;   // elements, kAdamTile but for a tensor's last tile
   int32_t decays;
 };
-constexpr int kAdamTile = 2048;
+// 512 elements: with 256 M elements and more, the 1 to 2 KB runs of each array
+// that a block of this size touches kept HBM busier than longer ones (300M
+// elements, bf16 gradients and weights: 1.46 ms at 512, 1.54 at 1024, 1.72 at
+// 256).
+constexpr int kAdamTile = 512;
 
 // Step constants; those near 1 or 0 are taken from fp64 (1 - 0.999 in fp32 is
 // off by 1e-5).
@@ -34,22 +38,18 @@ struct AdamArgs {
   float b2, c2;
   float keep;        // 1 - lr * weight_decay
   float eps;
-  double lr, beta1, beta2;
+  float lr;
+  double log_b1, log_b2;
   float max_norm;
   const float* norm;   // NULL: no clipping
   long long* step;
-  unsigned int* ticket;
+  unsigned int* tickets;
 };
 
-// b^t in fp64 by squaring: at most 2 log2(t) products.
-__device__ __forceinline__ double power(double b, long long t) {
-  double r = 1.0;
-  for (; t > 0; t >>= 1) {
-    if (t & 1) r *= b;
-    b *= b;
-  }
-  return r;
-}
+// 1 - b^t = -expm1(t ln b). The product is made in fp64 and rounded once, and
+// expm1 keeps the relative precision of a small one, so fp32 is enough from
+// there; b^t by itself would need fp64 (1 - 0.999 in fp32 is off by 1e-5).
+__device__ __forceinline__ float correction(double log_b, double t) { return -expm1f(float(log_b * t)); }
 
 struct AdamElem {
   float p, m, v;
@@ -64,24 +64,35 @@ __device__ __forceinline__ AdamElem adam(float g, float p, float m, float v, con
   return {p, m, v};
 }
 
-template <int DT>
-__device__ __forceinline__ void load4(const void* p, int64_t i, float x[4]) {
-  if constexpr (DT == DDP_FP32) {
-    const u32x4 w = reinterpret_cast<const u32x4_at4*>(p)[i];
-    for (int j = 0; j < 4; ++j) x[j] = __uint_as_float(w[j]);
-  } else {
-    const u32x2 w = reinterpret_cast<const u32x2_at2*>(p)[i];
-    x[0] = bf16_lo(w.x), x[1] = bf16_hi(w.x), x[2] = bf16_lo(w.y), x[3] = bf16_hi(w.y);
-  }
-}
-
-__device__ __forceinline__ void store4(float* p, int64_t i, const float x[4]) {
-  reinterpret_cast<u32x4_at4*>(p)[i] =
-      u32x4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
-}
-
-template <int DT>
+// One block per tile and one wave per array: wave 0 streams the gradient (and
+// the bf16 weights), waves 1 to 3 p, m and v; they meet in LDS, where each
+// thread updates two elements. A wave that reads and writes one array keeps
+// each array's accesses together; threads that each took 4 elements of every
+// array ran the 300M-element step in 1.62 ms against 1.54. Blocks go to the 8
+// XCDs in turn, so block b takes tile b / 8 of the part b % 8 of the tiles:
+// each XCD walks a run of memory of its own (1.46 against 1.54 ms, 5.8 TB/s).
+//
+// NT: accesses stream past the caches, for tensors that exceed the Infinity
+// Cache together (1.46 against 1.84 ms with cached loads).
+template <int DT, bool NT>
 __global__ __launch_bounds__(kThreads) void k_adamw(const AdamTile* tiles, int64_t n_tiles, AdamArgs a) {
+  constexpr int U = kAdamTile / 256;   // vectors of four per lane
+  __shared__ float st[4][kAdamTile];
+  AdamTile tile{};
+  const unsigned int at = blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;  // the grid is a multiple of 8
+  if (at < n_tiles) tile = table_entry(tiles, at);  // else an empty one
+  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / 64), lane = int(threadIdx.x) % 64;
+  float x[U][4];
+  if (tile.count == kAdamTile) {
+    if (wave == 0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) load4<DT, NT>(tile.g, u * 64 + lane, x[u]);
+    } else {
+      const float* p = wave == 1 ? tile.p : wave == 2 ? tile.m : tile.v;
+#pragma unroll
+      for (int u = 0; u < U; ++u) load4<DDP_FP32, NT>(p, u * 64 + lane, x[u]);
+    }
+  }
   float f = 1.0f;
   if (a.norm != nullptr) {
     const float norm = *a.norm;
@@ -90,48 +101,52 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const AdamTile* tiles, int64
     f = q >= 1.0f ? 1.0f : q;
   }
   const long long t = *a.step + 1;
-  const float rate = float(a.lr / (1.0 - power(a.beta1, t)));
-  const float root = float(sqrt(1.0 / (1.0 - power(a.beta2, t))));  // sqrt(v / (1 - b2^t)) = root * sqrt(v)
-  for (int64_t i = blockIdx.x; i < n_tiles; i += gridDim.x) {
-    const AdamTile tile = tiles[i];
-    const float keep = tile.decays ? a.keep : 1.0f;
-    const int vecs = tile.count / 4;
-    for (int k = threadIdx.x; k < vecs; k += kThreads) {
-      float g[4], p[4], m[4], v[4];
-      load4<DT>(tile.g, k, g);
-      load4<DDP_FP32>(tile.p, k, p);
-      load4<DDP_FP32>(tile.m, k, m);
-      load4<DDP_FP32>(tile.v, k, v);
+  const float rate = a.lr / correction(a.log_b1, double(t));
+  const float root = 1.0f / sqrtf(correction(a.log_b2, double(t)));  // sqrt(v / (1 - b2^t)) = root * sqrt(v)
+  const float keep = tile.decays ? a.keep : 1.0f;
+  if (tile.count == kAdamTile) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const AdamElem e = adam(f * g[j], p[j], m[j], v[j], a, keep, rate, root);
-        p[j] = e.p, m[j] = e.m, v[j] = e.v;
-      }
-      store4(tile.p, k, p);
-      store4(tile.m, k, m);
-      store4(tile.v, k, v);
+    for (int u = 0; u < U; ++u)
+      *reinterpret_cast<float4*>(&st[wave][(u * 64 + lane) * 4]) = make_float4(x[u][0], x[u][1], x[u][2], x[u][3]);
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int e = u * kThreads + int(threadIdx.x);
+      const AdamElem y = adam(f * st[0][e], st[1][e], st[2][e], st[3][e], a, keep, rate, root);
+      st[1][e] = y.p, st[2][e] = y.m, st[3][e] = y.v;
+    }
+    __syncthreads();
+    if (wave == 0) {
       if (tile.c != nullptr)
-        reinterpret_cast<u32x2_at2*>(tile.c)[k] = u32x2{round_bf16x2(p[0], p[1]), round_bf16x2(p[2], p[3])};
+#pragma unroll
+        for (int u = 0; u < U; ++u) store4<DDP_BF16, NT>(tile.c, u * 64 + lane, &st[1][(u * 64 + lane) * 4]);
+    } else {
+      float* p = wave == 1 ? tile.p : wave == 2 ? tile.m : tile.v;
+#pragma unroll
+      for (int u = 0; u < U; ++u) store4<DDP_FP32, NT>(p, u * 64 + lane, &st[wave][(u * 64 + lane) * 4]);
     }
-    const int e = vecs * 4 + int(threadIdx.x);
-    if (e < tile.count) {
-      const AdamElem x = adam(f * Ops<DT>::load1(tile.g, e), tile.p[e], tile.m[e], tile.v[e], a, keep, rate, root);
-      tile.p[e] = x.p;
-      tile.m[e] = x.m;
-      tile.v[e] = x.v;
-      if (tile.c != nullptr) Ops<DDP_BF16>::store1(tile.c, e, round_bf16(x.p));
+  } else {
+    for (int e = threadIdx.x; e < tile.count; e += kThreads) {
+      const AdamElem y = adam(f * Ops<DT>::load1(tile.g, e), tile.p[e], tile.m[e], tile.v[e], a, keep, rate, root);
+      tile.p[e] = y.p;
+      tile.m[e] = y.m;
+      tile.v[e] = y.v;
+      if (tile.c != nullptr) Ops<DDP_BF16>::store1(tile.c, e, round_bf16(y.p));
     }
   }
-  // The step count moves on when every block has read it: the block with the
-  // last ticket writes it, and clears the ticket for the next launch.
+  // The step count moves on when every block has read it: the last block to
+  // finish writes it.
   __syncthreads();
-  if (threadIdx.x == 0) {
-    const unsigned int k = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (k == gridDim.x - 1) {
-      __hip_atomic_store(a.ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      *a.step = t;
-    }
-  }
+  if (threadIdx.x == 0 && is_last_block(a.tickets)) *a.step = t;
+}
+
+template <int DT>
+void launch_adamw(const AdamTile* tiles, int64_t n_tiles, int64_t bytes, const AdamArgs& a, hipStream_t s) {
+  const dim3 grid(unsigned(std::max<int64_t>(8, (n_tiles + 7) / 8 * 8))), block(kThreads);
+  if (bytes > kInfinityCacheBytes)
+    hipLaunchKernelGGL((k_adamw<DT, true>), grid, block, 0, s, tiles, n_tiles, a);
+  else
+    hipLaunchKernelGGL((k_adamw<DT, false>), grid, block, 0, s, tiles, n_tiles, a);
 }
 
 }  // namespace
@@ -141,9 +156,10 @@ struct ddp_adamw {
   int32_t dtype = DDP_FP32;  // the gradients'
   int dev = 0;
   int64_t n_tiles = 0;
-  void* memory = nullptr;  // tiles, then the ticket
+  int64_t bytes = 0;       // of all the tensors
+  void* memory = nullptr;  // tiles, then the tickets
   ddp::AdamTile* tiles = nullptr;
-  unsigned int* ticket = nullptr;
+  unsigned int* tickets = nullptr;
   int64_t* step = nullptr;
 };
 
@@ -196,29 +212,31 @@ extern "C" int ddp_adamw_create(const ddp_grads* grads, void* const* params, voi
     }
     st = check_disjoint(spans, fn);
     if (st != DDP_OK) return st;
+    if (tiles.size() >= (size_t(1) << 31)) return fail(DDP_EINVAL, std::string(fn) + ": too many elements for one launch");
     o = new ddp_adamw;
     o->dtype = grads->dtype;
     o->dev = grads->dev;
     o->n_tiles = int64_t(tiles.size());
+    o->bytes = grads->total * (elem_bytes(grads->dtype) + 12 + (params_bf16 == nullptr ? 0 : 2));
     o->step = step_dev;
     const size_t table = size_t(round_up(int64_t(sizeof(AdamTile) * tiles.size()), 256));
-    hipError_t e = hipMalloc(&o->memory, table + 256);
+    hipError_t e = hipMalloc(&o->memory, table + kTicketBytes);
     if (e != hipSuccess) {
       (void)hipGetLastError();
       delete o;
       return fail(DDP_ENOMEM, std::string(fn) + ": hipMalloc: " + hipGetErrorString(e));
     }
     char* base = static_cast<char*>(o->memory);
-    const char zeros[256] = {};
+    const std::vector<char> zeros(kTicketBytes, 0);
     if (!tiles.empty()) e = hipMemcpy(base, tiles.data(), sizeof(AdamTile) * tiles.size(), hipMemcpyHostToDevice);
-    if (e == hipSuccess) e = hipMemcpy(base + table, zeros, sizeof(zeros), hipMemcpyHostToDevice);
+    if (e == hipSuccess) e = hipMemcpy(base + table, zeros.data(), zeros.size(), hipMemcpyHostToDevice);
     if (e != hipSuccess) {
       (void)hipFree(o->memory);
       delete o;
       return hip_fail(e, "ddp_adamw_create: tables");
     }
     o->tiles = reinterpret_cast<AdamTile*>(base);
-    o->ticket = reinterpret_cast<unsigned int*>(base + table);
+    o->tickets = reinterpret_cast<unsigned int*>(base + table);
     *out = o;
     return DDP_OK;
   } catch (const std::bad_alloc&) {
@@ -255,16 +273,16 @@ extern "C" int ddp_adamw_step(ddp_adamw* o, double lr, double beta1, double beta
   a.b2 = float(beta2), a.c2 = float(1.0 - beta2);
   a.keep = float(1.0 - lr * weight_decay);
   a.eps = float(eps);
-  a.lr = lr, a.beta1 = beta1, a.beta2 = beta2;
+  a.lr = float(lr);
+  a.log_b1 = std::log(beta1), a.log_b2 = std::log(beta2);  // -inf for 0: b^t = 0
   a.max_norm = float(max_norm);
   a.norm = norm_dev;
   a.step = reinterpret_cast<long long*>(o->step);
-  a.ticket = o->ticket;
-  const dim3 grid(unsigned(std::max<int64_t>(1, std::min<int64_t>(o->n_tiles, 4096)))), block(kThreads);
+  a.tickets = o->tickets;
   if (o->dtype == DDP_FP32)
-    hipLaunchKernelGGL(k_adamw<DDP_FP32>, grid, block, 0, as_stream(stream), o->tiles, o->n_tiles, a);
+    launch_adamw<DDP_FP32>(o->tiles, o->n_tiles, o->bytes, a, as_stream(stream));
   else
-    hipLaunchKernelGGL(k_adamw<DDP_BF16>, grid, block, 0, as_stream(stream), o->tiles, o->n_tiles, a);
+    launch_adamw<DDP_BF16>(o->tiles, o->n_tiles, o->bytes, a, as_stream(stream));
   DDP_HIP_TRY(hipGetLastError(), "ddp_adamw_step: launch");
   return DDP_OK;
 }
