@@ -1,12 +1,13 @@
 /*
  * ddp_train.h -- C ABI of the operators around the gradient sync of
  * ddp_ring.h, on the same MI355X (gfx950): what makes the gradients where the
- * sync reads them, and what reads them after it (the global gradient norm,
- * clipping, an AdamW step).
+ * sync reads them (a linear layer and its gradients), and what reads them
+ * after it (the global gradient norm, clipping, an AdamW step).
  *
  * In the step of "DDP 与 Ring All-Reduce" (blog.vllbc.top), section 05, the
- * optimizer is what step 5 hands the reduced gradients to. The operators
- * themselves are written from the formulas given with each.
+ * layer is step 2 (backward produces the gradients, whose hooks mark them
+ * ready) and the optimizer is what step 5 hands the reduced gradients to. The
+ * operators themselves are written from the formulas given with each.
  *
  * Conventions: those of ddp_ring.h (status codes, ddp_last_error, device
  * pointers checked against their allocations before anything is launched,
@@ -102,6 +103,70 @@ void ddp_adamw_free(ddp_adamw* opt);
  * must be ordered. */
 int ddp_adamw_step(ddp_adamw* opt, double lr, double beta1, double beta2, double eps, double weight_decay,
                    double max_norm, const float* norm_dev, void* stream);
+
+/* ---------------------------------------------------------------- linear layer
+ * Matrices are row-major: element (i, j) of a matrix with leading dimension
+ * ld lies at i * ld + j; ld >= its number of columns. Pointers are aligned to
+ * the element; no other alignment is needed. M, N, K >= 0: M rows (tokens),
+ * K input and N output features; weights are w[N][K].
+ * `dtype` is the type of x, w, bias, residual, y, z, dz, dx and add. Products
+ * are summed in fp32: bf16 on the bf16 matrix instructions, fp32 on the fp32
+ * ones.
+ * Activations and their slopes:
+ *   DDP_ACT_NONE       z
+ *   DDP_ACT_RELU       max(z, 0), slope 0 at 0
+ *   DDP_ACT_GELU       z/2 (1 + erf(z / sqrt 2))
+ *   DDP_ACT_GELU_TANH  z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))
+ *   DDP_ACT_SILU       z / (1 + exp(-z))
+ * Workspace: with few output tiles the long sum is cut into parts, which need
+ * scratch on the device: ddp_linear_workspace gives the bytes (0 if none) for
+ * a direction and shape on the current device. A call with less (NULL, 0) is refused. The
+ * contents need not be kept between calls; calls that may overlap need their own. 16-byte aligned. */
+#define DDP_ACT_NONE 0
+#define DDP_ACT_RELU 1
+#define DDP_ACT_GELU 2
+#define DDP_ACT_GELU_TANH 3
+#define DDP_ACT_SILU 4
+
+#define DDP_LINEAR_FORWARD 0
+#define DDP_LINEAR_BACKWARD_INPUT 1
+#define DDP_LINEAR_BACKWARD_WEIGHT 2
+int ddp_linear_workspace(int32_t direction, int64_t M, int64_t N, int64_t K, int32_t dtype, int64_t* bytes);
+
+/* y = act(x w^T + bias) + residual; z (NULL: not kept) receives
+ * rnd(x w^T + bias), which the backward pass takes. bias[N] and
+ * residual may be NULL. The activation is applied to the unrounded sum.
+ * y and z must not overlap the inputs, except that y may be the residual. */
+int ddp_linear_forward(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias,
+                       const void* residual, int64_t ldr, void* y, int64_t ldy, void* z, int64_t ldz,
+                       int64_t M, int64_t N, int64_t K, int32_t dtype, int32_t act,
+                       void* workspace, int64_t workspace_bytes, void* stream);
+
+/* dx = (dz w) * act'(z) + add: the gradient of the layer's input, carried on
+ * through the activation of the layer before it, whose kept z[M][K] is given
+ * (NULL: no activation, `act` must be DDP_ACT_NONE), and joined with `add`
+ * (NULL: none), the gradient that reaches the same place along a residual. dz
+ * is the gradient of this layer's z, [M][N]. dx must not overlap the inputs,
+ * except that it may be `add`. */
+int ddp_linear_backward_input(const void* dz, int64_t lddz, const void* w, int64_t ldw, const void* z, int64_t ldz,
+                              const void* add, int64_t ldadd, void* dx, int64_t lddx,
+                              int64_t M, int64_t N, int64_t K, int32_t dtype, int32_t act,
+                              void* workspace, int64_t workspace_bytes, void* stream);
+
+/* dw = dz^T x and db = sum of dz's rows (NULL: not wanted), of grad_dtype:
+ * `dtype`, or fp32 gradients of bf16 data. accumulate = 0 overwrites; 1 adds
+ * to what is there (one rounding of old + new), as over the micro-batches of
+ * a step. dw[N][K] and db[N] may lie in a gradient arena, where the sync
+ * reduces them in place. With M = 0 the sums are zero. */
+int ddp_linear_backward_weight(const void* dz, int64_t lddz, const void* x, int64_t ldx, void* dw, int64_t lddw,
+                               void* db, int64_t M, int64_t N, int64_t K, int32_t dtype, int32_t grad_dtype,
+                               int32_t accumulate, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* dz = dy * act'(z), element by element over [M][N]: the gradient of a
+ * layer's z where that of its output comes from something other than
+ * ddp_linear_backward_input. dz may be dy. */
+int ddp_act_backward(const void* dy, int64_t lddy, const void* z, int64_t ldz, void* dz, int64_t lddz,
+                     int64_t M, int64_t N, int32_t dtype, int32_t act, void* stream);
 
 #ifdef __cplusplus
 }

@@ -101,6 +101,14 @@ def _load():
                                             ctypes.POINTER(vp)]),
         "ddp_adamw_free": (None, [vp]),
         "ddp_adamw_step": (ctypes.c_int, [vp, f64, f64, f64, f64, f64, f64, vp, vp]),
+        "ddp_linear_workspace": (ctypes.c_int, [i32, i64, i64, i64, i32, ctypes.POINTER(i64)]),
+        "ddp_linear_forward": (ctypes.c_int, [vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, i64, i64, i64, i64,
+                                              i32, i32, vp, i64, vp]),
+        "ddp_linear_backward_input": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64,
+                                                     i32, i32, vp, i64, vp]),
+        "ddp_linear_backward_weight": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i32, i32, i32,
+                                                      vp, i64, vp]),
+        "ddp_act_backward": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, i64, i64, i32, i32, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -632,3 +640,115 @@ class AdamW:
             self.free()
         except Exception:
             pass
+
+
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+LINEAR_FORWARD, LINEAR_BACKWARD_INPUT, LINEAR_BACKWARD_WEIGHT = 0, 1, 2
+
+
+def linear_workspace(direction, m, n, k, dtype):
+    """Bytes of scratch that a linear call of these sizes needs."""
+    b = ctypes.c_int64()
+    _check(_get_lib().ddp_linear_workspace(int(direction), int(m), int(n), int(k), dtype_code(dtype), ctypes.byref(b)))
+    return b.value
+
+
+def _matrix(t, rows, cols, dtype, what):
+    """(pointer, leading dimension) of a rows x cols matrix; (None, cols) for None."""
+    if t is None:
+        return None, cols
+    if not t.is_cuda or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or t.dtype != dtype:
+        raise ValueError(f"{what} must be a {rows} x {cols} matrix of {dtype} on the GPU")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {what} must be contiguous")
+    return t.data_ptr(), (t.stride(0) if rows > 1 else max(cols, 1))
+
+
+def _vector(t, n, dtype, what):
+    if t is None:
+        return None
+    if not t.is_cuda or t.numel() != n or t.dim() != 1 or not t.is_contiguous() or t.dtype != dtype:
+        raise ValueError(f"{what} must be a contiguous vector of {n} {dtype} on the GPU")
+    return t.data_ptr()
+
+
+def _scratch(nbytes, workspace, stream):
+    """The caller's workspace, or torch memory that belongs to the stream."""
+    if workspace is None and nbytes:
+        with _stream_context(stream):
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    return workspace, (0, None) if workspace is None else (workspace.numel() * workspace.element_size(), workspace.data_ptr())
+
+
+def _result(out, rows, cols, dtype, stream):
+    if out is None:
+        with _stream_context(stream):
+            out = torch.empty(rows, cols, dtype=dtype, device="cuda")
+    return out
+
+
+def linear_forward(x, w, bias=None, residual=None, act="none", keep=False, out=None, z=None, workspace=None, stream=None):
+    """act(x w^T + bias) + residual; with keep=True (or a matrix z to fill)
+    the pair (y, z), z = x w^T + bias as the backward pass takes it (see
+    ddp_linear_forward in include/ddp_train.h)."""
+    m, k = x.shape
+    n, dt = w.shape[0], x.dtype
+    code = dtype_code(dt)
+    y = _result(out, m, n, dt, stream)
+    if keep and z is None:
+        z = _result(None, m, n, dt, stream)
+    xp, ldx = _matrix(x, m, k, dt, "x")
+    wp, ldw = _matrix(w, n, k, dt, "w")
+    rp, ldr = _matrix(residual, m, n, dt, "residual")
+    yp, ldy = _matrix(y, m, n, dt, "out")
+    zp, ldz = _matrix(z, m, n, dt, "z")
+    ws, (nbytes, p) = _scratch(linear_workspace(LINEAR_FORWARD, m, n, k, code), workspace, stream)
+    _check(_get_lib().ddp_linear_forward(xp, ldx, wp, ldw, _vector(bias, n, dt, "bias"), rp, ldr, yp, ldy, zp, ldz,
+                                         m, n, k, code, ACTIVATIONS[act], p, nbytes, _stream(stream)))
+    return y if z is None else (y, z)
+
+
+def linear_backward_input(dz, w, act="none", z=None, add=None, out=None, workspace=None, stream=None):
+    """(dz w) * act'(z) + add: the gradient of the layer's input, through the
+    activation of the layer before it (see ddp_linear_backward_input)."""
+    m, n = dz.shape
+    k, dt = w.shape[1], dz.dtype
+    code = dtype_code(dt)
+    dx = _result(out, m, k, dt, stream)
+    gp, ldg = _matrix(dz, m, n, dt, "dz")
+    wp, ldw = _matrix(w, n, k, dt, "w")
+    zp, ldz = _matrix(z, m, k, dt, "z")
+    ap, lda = _matrix(add, m, k, dt, "add")
+    op, ldo = _matrix(dx, m, k, dt, "out")
+    ws, (nbytes, p) = _scratch(linear_workspace(LINEAR_BACKWARD_INPUT, m, n, k, code), workspace, stream)
+    _check(_get_lib().ddp_linear_backward_input(gp, ldg, wp, ldw, zp, ldz, ap, lda, op, ldo, m, n, k, code,
+                                                ACTIVATIONS[act], p, nbytes, _stream(stream)))
+    return dx
+
+
+def linear_backward_weight(dz, x, dw, db=None, accumulate=False, workspace=None, stream=None):
+    """dw (+)= dz^T x and db (+)= the sum of dz's rows, into tensors of the
+    data's dtype or float32, e.g. views of a gradient arena (see
+    ddp_linear_backward_weight)."""
+    m, n = dz.shape
+    k, dt, gt = x.shape[1], dz.dtype, dw.dtype
+    code = dtype_code(dt)
+    gp, ldg = _matrix(dz, m, n, dt, "dz")
+    xp, ldx = _matrix(x, m, k, dt, "x")
+    wp, ldw = _matrix(dw, n, k, gt, "dw")
+    bp = _vector(db, n, gt, "db")
+    ws, (nbytes, p) = _scratch(linear_workspace(LINEAR_BACKWARD_WEIGHT, m, n, k, code), workspace, stream)
+    _check(_get_lib().ddp_linear_backward_weight(gp, ldg, xp, ldx, wp, ldw, bp, m, n, k, code, dtype_code(gt),
+                                                 1 if accumulate else 0, p, nbytes, _stream(stream)))
+
+
+def act_backward(dy, z, act, out=None, stream=None):
+    """dy * act'(z), element by element; out may be dy."""
+    m, n = dy.shape
+    dt = dy.dtype
+    dz = _result(out, m, n, dt, stream)
+    yp, ldy = _matrix(dy, m, n, dt, "dy")
+    zp, ldz = _matrix(z, m, n, dt, "z")
+    op, ldo = _matrix(dz, m, n, dt, "out")
+    _check(_get_lib().ddp_act_backward(yp, ldy, zp, ldz, op, ldo, m, n, dtype_code(dt), ACTIVATIONS[act], _stream(stream)))
+    return dz

@@ -1,0 +1,873 @@
+// A linear layer's products on the matrix instructions, each with what
+// follows it in the same pass (ddp_train.h):
+//
+//   forward          z = x w^T + bias,  y = act(z) + residual
+//   input gradient   dx = (dz w) * act'(z) + add
+//   weight gradient  dw (+)= dz^T x,  db (+)= sum of dz's rows
+//
+// All three are C[i][j] = sum_k A(i, k) B(j, k). What differs is how an
+// operand lies in memory: with the sum's index k contiguous ("along": x and w
+// in the forward product), or with k going from row to row ("across": w in
+// the input gradient, both operands of the weight gradient).
+//
+// A block computes a tile of C in steps of 128 bytes of k (64 bf16 or 32 fp32
+// values). Both operands' parts of a step lie in LDS as they lie in memory,
+// in 16-byte chunks, the next step's on their way while this one's are
+// multiplied. A lane of a 32 x 32 matrix instruction needs one row's k values
+// 8h .. 8h+7 (h: its half of the wave): 16 bytes of an "along" row, or, of an
+// "across" operand, eight rows' values of one column, which the transposing
+// LDS read gathers (bf16), or four single reads (fp32).
+#include <algorithm>
+#include <cmath>
+#include <new>
+
+#include "train_internal.h"
+
+namespace ddp {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+#define DDP_LDS __attribute__((address_space(3)))
+
+struct LinearArgs {
+  const void* a;    // operand of the rows of C
+  const void* b;    // operand of the columns of C
+  int64_t lda, ldb; // elements
+  int64_t I, J, K;  // C is I x J, the sum has K terms
+  void* c;          // y, dx or dw
+  int64_t ldc;
+  void* z;          // forward: kept z (NULL: not); input gradient: z (NULL: no activation)
+  int64_t ldz;
+  const void* e;    // forward: residual; input gradient: add (NULL: none)
+  int64_t lde;
+  const void* bias; // forward (NULL: none)
+  int32_t act;
+  int32_t grad32;      // weight gradient: dw is fp32
+  int32_t accumulate;  // weight gradient: add to dw
+  int32_t parts;       // blocks that share a tile's sum
+  int64_t part_k;      // terms of one part (whole steps)
+  float* partial;      // parts > 1: [part][I][round_up(J, 8)]
+  int32_t tiles_i, tiles_j;
+};
+
+constexpr bool a_along(int dir) { return dir != DDP_LINEAR_BACKWARD_WEIGHT; }
+constexpr bool b_along(int dir) { return dir == DDP_LINEAR_FORWARD; }
+
+// ---------------------------------------------------------------- activations
+
+__device__ __forceinline__ float act_value(float z, int act) {
+  switch (act) {
+    case DDP_ACT_RELU:
+      return z > 0.0f ? z : (z != z ? z : 0.0f);
+    case DDP_ACT_GELU:
+      return 0.5f * z * (1.0f + erff(z * 0.70710678f));
+    case DDP_ACT_GELU_TANH: {
+      // 1 + tanh(u) = 2 / (1 + exp(-2u))
+      const float u2 = z * fmaf(0.0713548163f, z * z, 1.59576912f);  // 2 sqrt(2/pi) (z + 0.044715 z^3)
+      return z / (1.0f + __expf(-u2));
+    }
+    case DDP_ACT_SILU:
+      return z / (1.0f + __expf(-z));
+    default:
+      return z;
+  }
+}
+
+// The slopes are flat to the last bit beyond |z| = 16 (silu: 104), where their
+// factors would become infinity times zero. A NaN stays.
+__device__ __forceinline__ float within(float z, float most) { return z > most ? most : z < -most ? -most : z; }
+
+__device__ __forceinline__ float act_slope(float z, int act) {
+  z = within(z, act == DDP_ACT_SILU ? 104.0f : 16.0f);
+  switch (act) {
+    case DDP_ACT_RELU:
+      return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
+    case DDP_ACT_GELU:
+      return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * 0.39894228f * __expf(-0.5f * z * z);
+    case DDP_ACT_GELU_TANH: {
+      const float z2 = z * z;
+      const float s = 1.0f / (1.0f + __expf(-z * fmaf(0.0713548163f, z2, 1.59576912f)));  // (1 + tanh u) / 2
+      // s + z s (1 - s) 2u'
+      return fmaf(z * s * (1.0f - s), fmaf(3.0f * 0.0713548163f, z2, 1.59576912f), s);
+    }
+    case DDP_ACT_SILU: {
+      const float s = 1.0f / (1.0f + __expf(-z));
+      return s * fmaf(z, 1.0f - s, 1.0f);
+    }
+    default:
+      return 1.0f;
+  }
+}
+
+// ---------------------------------------------------------------- eight outputs of a row
+
+// Elements [0, n) of eight at p (element-aligned), the rest zero.
+template <int DT>
+__device__ __forceinline__ void load8(const void* p, int64_t at, int n, float v[8]) {
+  if (n == 8) {
+    if constexpr (DT == DDP_FP32) {
+      const float* q = static_cast<const float*>(p) + at;
+      load4<DDP_FP32, false>(q, 0, v);
+      load4<DDP_FP32, false>(q, 1, v + 4);
+    } else {
+      const u32x4 w = load_at<false, u32x4_at2>(static_cast<const uint16_t*>(p) + at, 0);
+      for (int k = 0; k < 4; ++k) v[2 * k] = bf16_lo(w[k]), v[2 * k + 1] = bf16_hi(w[k]);
+    }
+  } else {
+    for (int k = 0; k < 8; ++k) v[k] = k < n ? Ops<DT>::load1(p, at + k) : 0.0f;
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void store8(void* p, int64_t at, int n, const float v[8]) {
+  if (n == 8) {
+    if constexpr (DT == DDP_FP32) {
+      float* q = static_cast<float*>(p) + at;
+      store4<DDP_FP32, false>(q, 0, v);
+      store4<DDP_FP32, false>(q, 1, v + 4);
+    } else {
+      store_at<false, u32x4_at2>(static_cast<uint16_t*>(p) + at, 0,
+                                 u32x4{round_bf16x2(v[0], v[1]), round_bf16x2(v[2], v[3]), round_bf16x2(v[4], v[5]),
+                                       round_bf16x2(v[6], v[7])});
+    }
+  } else {
+    for (int k = 0; k < 8; ++k)
+      if (k < n) Ops<DT>::store1(p, at + k, DT == DDP_BF16 ? round_bf16(v[k]) : v[k]);
+  }
+}
+
+// What an output needs besides its sum: the residual, add and z, or the old
+// gradient. Loaded ahead of the sums, which arrive later.
+struct Extra {
+  float e[8], z[8];
+};
+
+template <int DT, int DIR>
+__device__ __forceinline__ void load_extra(const LinearArgs& g, int64_t i, int64_t j, int n, Extra& x) {
+  if constexpr (DIR == DDP_LINEAR_BACKWARD_WEIGHT) {
+    if (g.accumulate) {
+      if (g.grad32)
+        load8<DDP_FP32>(g.c, i * g.ldc + j, n, x.e);
+      else
+        load8<DT>(g.c, i * g.ldc + j, n, x.e);
+    }
+  } else {
+    if (g.e != nullptr) load8<DT>(g.e, i * g.lde + j, n, x.e);
+    if (DIR == DDP_LINEAR_BACKWARD_INPUT && g.z != nullptr) load8<DT>(g.z, i * g.ldz + j, n, x.z);
+  }
+}
+
+// Eight sums of row i from column j on (n of them inside C) become outputs.
+template <int DT, int DIR>
+__device__ __forceinline__ void finish(const LinearArgs& g, int64_t i, int64_t j, int n, float v[8], const Extra& x,
+                                       const float bias[8]) {
+  if constexpr (DIR == DDP_LINEAR_FORWARD) {
+    if (g.bias != nullptr)
+      for (int k = 0; k < 8; ++k) v[k] += bias[k];
+    if (g.z != nullptr) store8<DT>(g.z, i * g.ldz + j, n, v);
+    for (int k = 0; k < 8; ++k) v[k] = act_value(v[k], g.act);
+    if (g.e != nullptr)
+      for (int k = 0; k < 8; ++k) v[k] += x.e[k];
+    store8<DT>(g.c, i * g.ldc + j, n, v);
+  } else if constexpr (DIR == DDP_LINEAR_BACKWARD_INPUT) {
+    if (g.z != nullptr)
+      for (int k = 0; k < 8; ++k) v[k] *= act_slope(x.z[k], g.act);
+    if (g.e != nullptr)
+      for (int k = 0; k < 8; ++k) v[k] += x.e[k];
+    store8<DT>(g.c, i * g.ldc + j, n, v);
+  } else {
+    if (g.accumulate)
+      for (int k = 0; k < 8; ++k) v[k] += x.e[k];
+    if (g.grad32)
+      store8<DDP_FP32>(g.c, i * g.ldc + j, n, v);
+    else
+      store8<DT>(g.c, i * g.ldc + j, n, v);
+  }
+}
+
+// ---------------------------------------------------------------- an operand's tile
+
+// T rows of C's side (i or j) by 128 bytes of k, in LDS as 16-byte chunks.
+// "along": T rows of 8 chunks. A read takes the same chunk of 8 neighbouring
+// rows at a time, 128 bytes apart, so chunk c of row r is kept at c ^ (r & 7):
+// the reads then touch all banks.
+// "across": one row of T elements per k. The transposing read takes 4
+// neighbouring rows of 32 bytes at a time, so those are kept apart by
+// exchanging chunks by the row's last two bits.
+// (The exchange is applied to the address that a lane loads from: a direct
+// load to LDS writes the wave's 64 chunks in lane order.)
+template <int DT, bool ALONG, int T, int THREADS>
+struct Tile {
+  static constexpr int ES = DT == DDP_BF16 ? 2 : 4;
+  static constexpr int V = 16 / ES;             // elements per chunk
+  static constexpr int STEP = 128 / ES;         // k per step
+  static constexpr int BYTES = T * 128;
+  static constexpr int ROW = T * ES;            // "across": bytes per row
+  static constexpr int CPR = ALONG ? 8 : ROW / 16;
+  static constexpr int N = T * 8 / THREADS;     // chunks per thread
+  static_assert(T * 8 % THREADS == 0, "whole chunks per thread");
+
+  static __device__ __forceinline__ int swizzle(int row) {
+    if (ALONG) return row & 7;
+    return DT == DDP_BF16 ? (row & 3) << 1 : 0;
+  }
+  // Chunk q of the tile in LDS: its row, and the chunk of memory it holds.
+  static __device__ __forceinline__ int row_of(int q) { return q / CPR; }
+  static __device__ __forceinline__ int col_of(int q) { return (q % CPR) ^ swizzle(q / CPR); }
+
+  // This lane's part of the fragment for rows [32 * t, 32 * t + 32) from
+  // `base` on and the s-th quarter of the step.
+  static __device__ __forceinline__ u32x4 fragment(const char* lds, int base, int t, int s, int lane) {
+    if constexpr (ALONG) {
+      const int row = base + 32 * t + (lane & 31);
+      const int c = (2 * s + (lane >> 5)) ^ (lane & 7);
+      return *reinterpret_cast<const u32x4*>(lds + row * 128 + c * 16);
+    } else if constexpr (DT == DDP_BF16) {
+      const int group = lane >> 4, in = lane & 15;
+      const int k = 16 * s + 8 * (group >> 1) + (in >> 2);
+      const int i = base + 32 * t + 16 * (group & 1) + 4 * (in & 3);
+      const int c = (i >> 3) ^ swizzle(k);
+      const char* p = lds + k * ROW + c * 16 + (i & 7) * 2;
+      const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DDP_LDS i16x4*)p);
+      const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DDP_LDS i16x4*)(p + 4 * ROW));  // rows k+4..k+7: the same exchange
+      const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
+      return u32x4{a.x, a.y, b.x, b.y};
+    } else {
+      const int k = 8 * s + 4 * (lane >> 5);
+      const int i = base + 32 * t + (lane & 31);
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(lds + k * ROW + i * 4);
+      return u32x4{p[0], p[ROW / 4], p[2 * (ROW / 4)], p[3 * (ROW / 4)]};
+    }
+  }
+};
+
+// The 32 x 32 product of two fragments, added to d: lane l holds column l & 31
+// (of `col`'s rows), rows 8 q + 4 (l >> 5) + r in element 4 q + r.
+template <int DT>
+__device__ __forceinline__ f32x16 multiply(u32x4 row, u32x4 col, f32x16 d) {
+  if constexpr (DT == DDP_BF16) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, row), __builtin_bit_cast(bf16x8, col), d, 0, 0, 0);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      d = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(row[k]), __uint_as_float(col[k]), d, 0, 0, 0);
+    return d;
+  }
+}
+
+// ---------------------------------------------------------------- loading a tile
+
+constexpr uint32_t kFar = 0xfffffff0u;      // an offset outside every descriptor's range: reads as zeros
+constexpr uint32_t kMostRange = 0xf0000000u;
+
+// Direct loads to LDS, for operands whose every chunk is 16-byte aligned and
+// whole. The descriptor ends with the operand, so a chunk past it reads as
+// zeros; a row of C's side past the operand repeats the last one (its
+// products are not stored).
+template <class TL, bool ALONG, int THREADS>
+struct DirectLoader {
+  const char* p;           // the tile at the current step
+  int64_t left;            // bytes from p to the operand's end
+  int64_t advance;         // bytes per step
+  int64_t k_left;          // terms left
+  uint32_t off[TL::N];     // of this lane's chunks from p
+  int32_t k_of[TL::N];     // first term of each, within the step
+  int wave;
+
+  __device__ __forceinline__ void init(const void* base, int64_t ld, int64_t side, int64_t K, int64_t s0, int64_t k0, int64_t k1) {
+    const int lane = int(threadIdx.x) & 63;
+    wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+    const int64_t rows = ALONG ? side : K, cols = ALONG ? K : side;
+    const int64_t start = ALONG ? (s0 * ld + k0) * TL::ES : (k0 * ld + s0) * TL::ES;
+    p = static_cast<const char*>(base) + start;
+    left = ((rows - 1) * ld + cols) * TL::ES - start;
+    advance = ALONG ? 128 : TL::STEP * ld * TL::ES;
+    k_left = k1 - k0;
+#pragma unroll
+    for (int n = 0; n < TL::N; ++n) {
+      const int q = (n * (THREADS / 64) + wave) * 64 + lane;
+      const int row = TL::row_of(q), col = TL::col_of(q);
+      if (ALONG) {
+        const int64_t r = s0 + row < side ? row : side - 1 - s0;
+        off[n] = uint32_t(r * ld * TL::ES + col * 16);
+        k_of[n] = col * TL::V;
+      } else {
+        off[n] = uint32_t(int64_t(row) * ld * TL::ES + col * 16);
+        k_of[n] = row;
+      }
+    }
+  }
+  // Starts the loads of the current step into `lds` and moves on.
+  __device__ __forceinline__ void issue(const char* lds) {
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    const uint32_t range = left <= 0 ? 0u : left < int64_t(kMostRange) ? uint32_t(left) : kMostRange;
+    const u32x4 desc = {uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(a))),
+                        uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(a >> 32))),
+                        uint32_t(__builtin_amdgcn_readfirstlane(range)), 0x00020000u};
+    const uint32_t to = uint32_t(reinterpret_cast<uintptr_t>((DDP_LDS const char*)lds));
+#pragma unroll
+    for (int n = 0; n < TL::N; ++n) {
+      const uint32_t o = k_of[n] < k_left ? off[n] : kFar;
+      const uint32_t m = uint32_t(__builtin_amdgcn_readfirstlane(to + (n * (THREADS / 64) + wave) * 1024));
+      // No output register: the load ends in LDS, and every use of it stands
+      // behind a wait for vmcnt(0) and a barrier. (With the builtin, the
+      // compiler waits for all direct loads before any read of LDS.)
+      asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(o), "s"(desc), "s"(m) : "m0");
+    }
+    p += advance;
+    left -= advance;
+    k_left -= TL::STEP;
+  }
+  __device__ __forceinline__ void commit(char*) {}
+};
+
+// Through registers, for operands of any alignment and width: whole chunks as
+// one load at their element's alignment, those over an edge element by
+// element, zeros past the sum's end.
+template <int DT, class TL, bool ALONG, int THREADS>
+struct AnyLoader {
+  const char* base;
+  int64_t ld, side, s0, k, k1;
+  u32x4 x[TL::N];
+
+  __device__ __forceinline__ void init(const void* b, int64_t ld_, int64_t side_, int64_t, int64_t s0_, int64_t k0, int64_t k1_) {
+    base = static_cast<const char*>(b);
+    ld = ld_, side = side_, s0 = s0_, k = k0, k1 = k1_;
+  }
+  __device__ __forceinline__ void issue(const char*) {
+#pragma unroll
+    for (int n = 0; n < TL::N; ++n) {
+      const int q = n * THREADS + int(threadIdx.x);
+      const int row = TL::row_of(q), col = TL::col_of(q) * TL::V;
+      const int64_t r = ALONG ? (s0 + row < side ? s0 + row : side - 1) : k + row;
+      const int64_t e = ALONG ? k + col : s0 + col;    // first element in its row
+      const int64_t end = ALONG ? k1 : side;           // elements of the row that count
+      x[n] = u32x4{0u, 0u, 0u, 0u};
+      if (!ALONG && r >= k1) continue;
+      const char* p = base + (r * ld + e) * TL::ES;
+      if (e + TL::V <= end) {
+        if constexpr (DT == DDP_FP32)
+          x[n] = load_at<false, u32x4_at4>(p, 0);
+        else
+          x[n] = load_at<false, u32x4_at2>(p, 0);
+      } else if (e < end) {
+        if constexpr (DT == DDP_FP32) {
+          for (int j = 0; j < TL::V - 1; ++j)
+            if (e + j < end) x[n][j] = reinterpret_cast<const uint32_t*>(p)[j];
+        } else {
+          for (int j = 0; j < TL::V - 1; ++j)
+            if (e + j < end) x[n][j >> 1] |= uint32_t(reinterpret_cast<const uint16_t*>(p)[j]) << ((j & 1) * 16);
+        }
+      }
+    }
+    k += TL::STEP;
+  }
+  __device__ __forceinline__ void commit(char* lds) {
+#pragma unroll
+    for (int n = 0; n < TL::N; ++n) *reinterpret_cast<u32x4*>(lds + (n * THREADS + int(threadIdx.x)) * 16) = x[n];
+  }
+};
+
+// ---------------------------------------------------------------- the product
+
+// Tile TI x TJ of C by WI x WJ waves.
+template <int DT, int DIR, int TI, int TJ, int WI, int WJ, bool DIRECT>
+__global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
+  constexpr int THREADS = WI * WJ * 64;
+  constexpr int FI = TI / WI / 32, FJ = TJ / WJ / 32;  // 32 x 32 products per wave
+  using TA = Tile<DT, a_along(DIR), TI, THREADS>;
+  using TB = Tile<DT, b_along(DIR), TJ, THREADS>;
+  using LA = std::conditional_t<DIRECT, DirectLoader<TA, a_along(DIR), THREADS>, AnyLoader<DT, TA, a_along(DIR), THREADS>>;
+  using LB = std::conditional_t<DIRECT, DirectLoader<TB, b_along(DIR), THREADS>, AnyLoader<DT, TB, b_along(DIR), THREADS>>;
+  constexpr int STAGE = TA::BYTES + TB::BYTES;
+  constexpr int PITCH = 32 * FJ + 4;  // floats; the outputs' way through LDS
+  static_assert(WI * WJ * 32 * PITCH * 4 <= 2 * STAGE, "the outputs' rows fit");
+  __shared__ __attribute__((aligned(1024))) char lds[2 * STAGE];
+
+  // Blocks go to the 8 XCDs in turn: XCD x takes the tiles of eighth x, in
+  // groups of 8 tile rows, so that blocks that share operands share an L2.
+  const int tiles = g.tiles_i * g.tiles_j;
+  const int at = int(blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8);
+  if (at >= tiles * g.parts) return;
+  const int part = at / tiles, tile = at % tiles;
+  const int group = tile / (8 * g.tiles_j), in_group = tile % (8 * g.tiles_j);
+  const int rows = g.tiles_i - 8 * group < 8 ? g.tiles_i - 8 * group : 8;
+  const int64_t i0 = int64_t(8 * group + in_group % rows) * TI, j0 = int64_t(in_group / rows) * TJ;
+  const int64_t k0 = part * g.part_k, k1 = k0 + g.part_k < g.K ? k0 + g.part_k : g.K;
+  const int steps = int((k1 - k0 + TA::STEP - 1) / TA::STEP);
+
+  const int lane = int(threadIdx.x) & 63, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+  const int wi = wave / WJ * (TI / WI), wj = wave % WJ * (TJ / WJ);
+  f32x16 acc[FI][FJ];
+#pragma unroll
+  for (int a = 0; a < FI; ++a)
+#pragma unroll
+    for (int b = 0; b < FJ; ++b) acc[a][b] = f32x16{};
+
+  if (steps > 0) {
+    LA la;
+    LB lb;
+    la.init(g.a, g.lda, g.I, g.K, i0, k0, k1);
+    lb.init(g.b, g.ldb, g.J, g.K, j0, k0, k1);
+    u32x4 fa[2][FI], fb[2][FJ];
+    const auto read = [&](const char* stage, int s, int to) {
+#pragma unroll
+      for (int a = 0; a < FI; ++a) fa[to][a] = TA::fragment(stage, wi, a, s, lane);
+#pragma unroll
+      for (int b = 0; b < FJ; ++b) fb[to][b] = TB::fragment(stage + TA::BYTES, wj, b, s, lane);
+    };
+    const auto product = [&](int from) {
+#pragma unroll
+      for (int a = 0; a < FI; ++a)
+#pragma unroll
+        for (int b = 0; b < FJ; ++b) acc[a][b] = multiply<DT>(fb[from][b], fa[from][a], acc[a][b]);
+    };
+    // The loads of a step have landed, and every wave is done with the other stage.
+    const auto turn = [&] {
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      __syncthreads();
+    };
+    la.issue(lds);
+    lb.issue(lds + TA::BYTES);
+    la.commit(lds);
+    lb.commit(lds + TA::BYTES);
+    turn();
+    read(lds, 0, 0);
+    for (int t = 0; t < steps; ++t) {
+      const char* stage = lds + (t & 1) * STAGE;
+      char* next = lds + ((t & 1) ^ 1) * STAGE;
+      const bool more = t + 1 < steps;
+      if (more) {
+        la.issue(next);
+        lb.issue(next + TA::BYTES);
+      }
+      read(stage, 1, 1);
+      product(0);
+      read(stage, 2, 0);
+      product(1);
+      read(stage, 3, 1);
+      product(0);
+      if (more) {
+        la.commit(next);
+        lb.commit(next + TA::BYTES);
+        turn();
+        read(next, 0, 0);
+      }
+      product(1);
+    }
+    __syncthreads();  // LDS is free for the outputs
+  }
+
+  // The outputs leave by rows: a wave writes 32 rows of its sums to LDS (a
+  // lane holds four neighbouring columns of one row at a time) and reads them
+  // back eight columns to a lane, so that loads and stores cover whole lines.
+  // Each wave has its own part of LDS.
+  float* const mine = reinterpret_cast<float*>(lds) + wave * 32 * PITCH;
+  constexpr int LPR = 4 * FJ;        // lanes per row
+  constexpr int RPP = 64 / LPR;      // rows per pass
+  constexpr int PASSES = 32 / RPP;
+  const int64_t j = j0 + wj + lane % LPR * 8;
+  const int n = g.J - j >= 8 ? 8 : g.J - j > 0 ? int(g.J - j) : 0;
+  float bias[8] = {};
+  if (DIR == DDP_LINEAR_FORWARD && g.bias != nullptr && n > 0) load8<DT>(g.bias, j, n, bias);
+  const int64_t jp = (g.J + 7) / 8 * 8;
+#pragma unroll
+  for (int a = 0; a < FI; ++a) {
+    const int64_t i_first = i0 + wi + 32 * a + lane / LPR;
+    Extra x[PASSES];
+    if (g.parts == 1 && n > 0) {
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p)
+        if (i_first + p * RPP < g.I) load_extra<DT, DIR>(g, i_first + p * RPP, j, n, x[p]);
+    }
+#pragma unroll
+    for (int b = 0; b < FJ; ++b)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<f32x4*>(mine + (lane & 31) * PITCH + 32 * b + 8 * q + 4 * (lane >> 5)) =
+            f32x4{acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      const float* src = mine + (lane / LPR + p * RPP) * PITCH + lane % LPR * 8;
+      const f32x4 lo = *reinterpret_cast<const f32x4*>(src), hi = *reinterpret_cast<const f32x4*>(src + 4);
+      float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      const int64_t i = i_first + p * RPP;
+      if (i >= g.I || n == 0) continue;
+      if (g.parts > 1)
+        store8<DDP_FP32>(g.partial, (part * g.I + i) * jp + j, 8, v);
+      else
+        finish<DT, DIR>(g, i, j, n, v, x[p], bias);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// Joins the parts of every sum, in their order, and finishes the outputs.
+template <int DT, int DIR>
+__global__ __launch_bounds__(kThreads) void k_linear_join(LinearArgs g) {
+  const int64_t jv = (g.J + 7) / 8;
+  const int64_t at = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+  if (at >= g.I * jv) return;
+  const int64_t i = at / jv, j = at % jv * 8;
+  const int n = g.J - j >= 8 ? 8 : int(g.J - j);
+  Extra x;
+  load_extra<DT, DIR>(g, i, j, n, x);
+  float bias[8] = {};
+  if (DIR == DDP_LINEAR_FORWARD && g.bias != nullptr) load8<DT>(g.bias, j, n, bias);
+  float v[8] = {};
+  for (int p = 0; p < g.parts; ++p) {
+    float w[8];
+    load8<DDP_FP32>(g.partial, (p * g.I + i) * jv * 8 + j, 8, w);
+    for (int k = 0; k < 8; ++k) v[k] += w[k];
+  }
+  finish<DT, DIR>(g, i, j, n, v, x, bias);
+}
+
+// ---------------------------------------------------------------- the bias gradient
+
+// Sums of dz's columns: a block takes kBiasRows rows of 512 columns (8 a
+// lane, each of the 4 waves every fourth row) and leaves one partial row.
+constexpr int kBiasRows = 256;
+
+template <int DT>
+__global__ __launch_bounds__(kThreads) void k_bias_parts(const void* dz, int64_t ld, int64_t M, int64_t N, float* partial) {
+  __shared__ float sums[4][512];
+  const int lane = int(threadIdx.x) & 63, wave = int(threadIdx.x) >> 6;
+  const int64_t j = int64_t(blockIdx.x) * 512 + lane * 8;
+  const int n = N - j >= 8 ? 8 : N - j > 0 ? int(N - j) : 0;
+  const int64_t m1 = std::min<int64_t>(M, int64_t(blockIdx.y + 1) * kBiasRows);
+  float s[8] = {};
+  if (n > 0) {
+#pragma unroll 8
+    for (int64_t m = int64_t(blockIdx.y) * kBiasRows + wave; m < m1; m += 4) {
+      float v[8];
+      load8<DT>(dz, m * ld + j, n, v);
+      for (int k = 0; k < 8; ++k) s[k] += v[k];
+    }
+  }
+  for (int k = 0; k < 8; ++k) sums[wave][lane * 8 + k] = s[k];
+  __syncthreads();
+  for (int c = threadIdx.x; c < 512; c += kThreads) {
+    const int64_t col = int64_t(blockIdx.x) * 512 + c;
+    if (col < N) partial[int64_t(blockIdx.y) * N + col] = (sums[0][c] + sums[1][c]) + (sums[2][c] + sums[3][c]);
+  }
+}
+
+template <int DT>
+__global__ __launch_bounds__(kThreads) void k_bias_join(const float* partial, int64_t parts, int64_t N, void* db, int accumulate) {
+  const int64_t c = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+  if (c >= N) return;
+  float s = 0.0f;
+  for (int64_t p = 0; p < parts; ++p) s += partial[p * N + c];
+  if (accumulate) s += Ops<DT>::load1(db, c);
+  Ops<DT>::store1(db, c, DT == DDP_BF16 ? round_bf16(s) : s);
+}
+
+// ---------------------------------------------------------------- element by element
+
+template <int DT>
+__global__ __launch_bounds__(kThreads) void k_act_backward(const void* dy, int64_t lddy, const void* z, int64_t ldz,
+                                                           void* dz, int64_t lddz, int64_t M, int64_t N, int act) {
+  const int64_t nv = (N + 7) / 8;
+  for (int64_t at = int64_t(blockIdx.x) * kThreads + threadIdx.x; at < M * nv; at += int64_t(gridDim.x) * kThreads) {
+    const int64_t m = at / nv, j = at % nv * 8;
+    const int n = N - j >= 8 ? 8 : int(N - j);
+    float g[8], x[8];
+    load8<DT>(dy, m * lddy + j, n, g);
+    load8<DT>(z, m * ldz + j, n, x);
+    for (int k = 0; k < 8; ++k) g[k] *= act_slope(x[k], act);
+    store8<DT>(dz, m * lddz + j, n, g);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// How a product is cut. The tile is 256 x 256 where there are enough of them
+// to fill the device and the operands can be loaded directly, else 128 x 128,
+// with the sum in parts when those are few. The parts do not depend on
+// alignment, so the workspace is known from the sizes.
+struct Cut {
+  bool big_if_direct;
+  int32_t parts;
+  int64_t part_k;
+};
+Cut cut_of(int64_t I, int64_t J, int64_t K, int dtype) {
+  const int64_t step = 128 / elem_bytes(dtype);
+  Cut c{div_up(I, 256) * div_up(J, 256) >= 192 && dtype == DDP_BF16, 1, std::max<int64_t>(step, round_up(K, step))};
+  const int64_t tiles = div_up(I, 128) * div_up(J, 128), steps = div_up(K, step);
+  if (!c.big_if_direct && tiles < 256 && steps > 4) {
+    const int64_t want = std::min(div_up(512, tiles), steps / 4);
+    if (want > 1) {
+      const int64_t per = div_up(steps, want);
+      c.part_k = per * step;
+      c.parts = int32_t(div_up(steps, per));
+    }
+  }
+  return c;
+}
+
+int64_t partial_bytes(const Cut& c, int64_t I, int64_t J) {
+  return c.parts > 1 ? round_up(int64_t(c.parts) * I * round_up(J, 8) * 4, 256) : 0;
+}
+int64_t bias_bytes(int64_t M, int64_t N) { return round_up(div_up(M, kBiasRows) * N * 4, 256); }
+
+// The sizes of a direction as those of C = A B^T.
+void product_sizes(int dir, int64_t M, int64_t N, int64_t K, int64_t* I, int64_t* J, int64_t* S) {
+  if (dir == DDP_LINEAR_FORWARD)
+    *I = M, *J = N, *S = K;
+  else if (dir == DDP_LINEAR_BACKWARD_INPUT)
+    *I = M, *J = K, *S = N;
+  else
+    *I = N, *J = K, *S = M;
+}
+
+template <int DT, int DIR, int T, int WI, int WJ, bool DIRECT>
+int launch_tiles(LinearArgs& g, hipStream_t s) {
+  const int64_t ti = div_up(g.I, T), tj = div_up(g.J, T);
+  if (ti * tj * g.parts >= (int64_t(1) << 30)) return fail(DDP_EINVAL, "ddp_linear: too many tiles for one launch");
+  g.tiles_i = int32_t(ti);
+  g.tiles_j = int32_t(tj);
+  const dim3 grid(unsigned(round_up(ti * tj * g.parts, 8))), block(WI * WJ * 64);
+  hipLaunchKernelGGL((k_linear<DT, DIR, T, T, WI, WJ, DIRECT>), grid, block, 0, s, g);
+  DDP_HIP_TRY(hipGetLastError(), "ddp_linear: launch");
+  return DDP_OK;
+}
+
+template <int DT, int DIR>
+int launch_product(LinearArgs g, const Cut& c, hipStream_t s) {
+  constexpr int V = 16 / (DT == DDP_BF16 ? 2 : 4);
+  g.parts = c.parts;
+  g.part_k = c.part_k;
+  // Direct loads need whole, aligned chunks: the contiguous index of each
+  // operand a multiple of a chunk, and offsets within a tile below 2^32.
+  const auto direct = [&](const void* p, int64_t ld, int64_t contiguous) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % V == 0 && contiguous % V == 0 && ld <= (int64_t(1) << 21);
+  };
+  const bool d = direct(g.a, g.lda, a_along(DIR) ? g.K : g.I) && direct(g.b, g.ldb, b_along(DIR) ? g.K : g.J);
+  int st;
+  if (!d)
+    st = launch_tiles<DT, DIR, 128, 2, 2, false>(g, s);
+  else if (DT == DDP_BF16 && c.big_if_direct)
+    st = launch_tiles<DT, DIR, DT == DDP_BF16 ? 256 : 128, 2, DT == DDP_BF16 ? 4 : 2, true>(g, s);
+  else
+    st = launch_tiles<DT, DIR, 128, 2, 2, true>(g, s);
+  if (st != DDP_OK || g.parts == 1) return st;
+  const int64_t blocks = div_up(g.I * div_up(g.J, 8), kThreads);
+  hipLaunchKernelGGL((k_linear_join<DT, DIR>), dim3(unsigned(blocks)), dim3(kThreads), 0, s, g);
+  DDP_HIP_TRY(hipGetLastError(), "ddp_linear: join launch");
+  return DDP_OK;
+}
+
+// A matrix argument: rows x cols, leading dimension ld, NULL where allowed.
+struct Matrix {
+  const void* p;
+  int64_t rows, cols, ld;
+  int eb;
+  const char* what;
+  bool written;
+  bool may_be_null;
+  int64_t bytes() const { return rows > 0 && cols > 0 ? ((rows - 1) * ld + cols) * eb : 0; }
+};
+
+// Every matrix lies in its allocation, and what is written overlaps nothing
+// else, except that matrix `in_place` may be matrix `out` (the same place and rows).
+int check_matrices(const char* fn, const Matrix* m, int n, int in_place, int out) {
+  for (int k = 0; k < n; ++k) {
+    const Matrix& x = m[k];
+    if (x.p == nullptr && x.may_be_null) continue;
+    if (x.ld < x.cols) return fail(DDP_EINVAL, std::string(fn) + ": the leading dimension of " + x.what + " is less than its columns");
+    if (x.ld > (int64_t(1) << 31)) return fail(DDP_EINVAL, std::string(fn) + ": the leading dimension of " + x.what + " is too large");
+    if (x.bytes() == 0) continue;
+    if (reinterpret_cast<uintptr_t>(x.p) % uintptr_t(x.eb) != 0)
+      return fail(DDP_EINVAL, std::string(fn) + ": " + x.what + " is not aligned to its element");
+    int st = check_range(x.p, x.bytes(), fn, x.what);
+    if (st != DDP_OK) return st;
+  }
+  for (int k = 0; k < n; ++k) {
+    if (!m[k].written || m[k].p == nullptr) continue;
+    for (int o = 0; o < n; ++o) {
+      if (o == k || m[o].p == nullptr) continue;
+      if (k == out && o == in_place && m[o].p == m[k].p && m[o].ld == m[k].ld) continue;
+      if (spans_overlap(m[k].p, m[k].bytes(), m[o].p, m[o].bytes()))
+        return fail(DDP_EINVAL, std::string(fn) + ": " + m[k].what + " overlaps " + m[o].what);
+    }
+  }
+  return DDP_OK;
+}
+
+int check_common(const char* fn, int64_t M, int64_t N, int64_t K, int32_t dtype, int32_t act) {
+  if (!valid_dtype(dtype)) return fail(DDP_EINVAL, std::string(fn) + ": unknown dtype");
+  if (act < DDP_ACT_NONE || act > DDP_ACT_SILU) return fail(DDP_EINVAL, std::string(fn) + ": unknown activation");
+  const int64_t most = int64_t(1) << 31;
+  if (M < 0 || N < 0 || K < 0 || M >= most || N >= most || K >= most)
+    return fail(DDP_EINVAL, std::string(fn) + ": M, N and K must lie in [0, 2^31)");
+  return DDP_OK;
+}
+
+int check_workspace(const char* fn, const void* p, int64_t have, int64_t need) {
+  if (need == 0) return DDP_OK;
+  if (p == nullptr || have < need)
+    return fail(DDP_EINVAL, std::string(fn) + ": the workspace needs " + std::to_string(need) + " bytes");
+  if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return fail(DDP_EINVAL, std::string(fn) + ": the workspace is not 16-byte aligned");
+  return check_range(p, need, fn, "workspace");
+}
+
+}  // namespace
+}  // namespace ddp
+
+using namespace ddp;
+
+extern "C" int ddp_linear_workspace(int32_t direction, int64_t M, int64_t N, int64_t K, int32_t dtype, int64_t* bytes) {
+  const char* fn = "ddp_linear_workspace";
+  if (bytes == nullptr) return fail(DDP_EINVAL, std::string(fn) + ": bytes is NULL");
+  *bytes = 0;
+  if (direction < DDP_LINEAR_FORWARD || direction > DDP_LINEAR_BACKWARD_WEIGHT)
+    return fail(DDP_EINVAL, std::string(fn) + ": unknown direction");
+  int st = check_common(fn, M, N, K, dtype, DDP_ACT_NONE);
+  if (st != DDP_OK) return st;
+  int64_t I, J, S;
+  product_sizes(direction, M, N, K, &I, &J, &S);
+  *bytes = partial_bytes(cut_of(I, J, S, dtype), I, J) +
+           (direction == DDP_LINEAR_BACKWARD_WEIGHT ? bias_bytes(M, N) : 0);
+  return DDP_OK;
+}
+
+extern "C" int ddp_linear_forward(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias,
+                                  const void* residual, int64_t ldr, void* y, int64_t ldy, void* z, int64_t ldz,
+                                  int64_t M, int64_t N, int64_t K, int32_t dtype, int32_t act, void* workspace,
+                                  int64_t workspace_bytes, void* stream) {
+  const char* fn = "ddp_linear_forward";
+  int st = check_common(fn, M, N, K, dtype, act);
+  if (st != DDP_OK) return st;
+  if (M == 0 || N == 0) return DDP_OK;
+  const int eb = elem_bytes(dtype);
+  const Cut c = cut_of(M, N, K, dtype);
+  const int64_t need = partial_bytes(c, M, N);
+  const Matrix m[] = {{x, M, K, ldx, eb, "x", false, false},       {w, N, K, ldw, eb, "w", false, false},
+                      {bias, 1, N, N, eb, "bias", false, true},    {residual, M, N, ldr, eb, "residual", false, true},
+                      {y, M, N, ldy, eb, "y", true, false},        {z, M, N, ldz, eb, "z", true, true},
+                      {need > 0 ? workspace : nullptr, 1, need, need, 1, "workspace", true, true}};
+  st = check_workspace(fn, workspace, workspace_bytes, need);
+  if (st != DDP_OK) return st;
+  st = check_matrices(fn, m, 7, 3, 4);
+  if (st != DDP_OK) return st;
+  LinearArgs g{};
+  g.a = x, g.lda = ldx, g.b = w, g.ldb = ldw;
+  g.I = M, g.J = N, g.K = K;
+  g.c = y, g.ldc = ldy, g.z = z, g.ldz = ldz, g.e = residual, g.lde = ldr, g.bias = bias;
+  g.act = act;
+  g.partial = static_cast<float*>(workspace);
+  return dtype == DDP_BF16 ? launch_product<DDP_BF16, DDP_LINEAR_FORWARD>(g, c, as_stream(stream))
+                           : launch_product<DDP_FP32, DDP_LINEAR_FORWARD>(g, c, as_stream(stream));
+}
+
+extern "C" int ddp_linear_backward_input(const void* dz, int64_t lddz, const void* w, int64_t ldw, const void* z,
+                                         int64_t ldz, const void* add, int64_t ldadd, void* dx, int64_t lddx,
+                                         int64_t M, int64_t N, int64_t K, int32_t dtype, int32_t act, void* workspace,
+                                         int64_t workspace_bytes, void* stream) {
+  const char* fn = "ddp_linear_backward_input";
+  int st = check_common(fn, M, N, K, dtype, act);
+  if (st != DDP_OK) return st;
+  if (z == nullptr && act != DDP_ACT_NONE) return fail(DDP_EINVAL, std::string(fn) + ": an activation's slope needs z");
+  if (M == 0 || K == 0) return DDP_OK;
+  const int eb = elem_bytes(dtype);
+  const Cut c = cut_of(M, K, N, dtype);
+  const int64_t need = partial_bytes(c, M, K);
+  const Matrix m[] = {{dz, M, N, lddz, eb, "dz", false, false}, {w, N, K, ldw, eb, "w", false, false},
+                      {z, M, K, ldz, eb, "z", false, true},     {add, M, K, ldadd, eb, "add", false, true},
+                      {dx, M, K, lddx, eb, "dx", true, false},
+                      {need > 0 ? workspace : nullptr, 1, need, need, 1, "workspace", true, true}};
+  st = check_workspace(fn, workspace, workspace_bytes, need);
+  if (st != DDP_OK) return st;
+  st = check_matrices(fn, m, 6, 3, 4);
+  if (st != DDP_OK) return st;
+  LinearArgs g{};
+  g.a = dz, g.lda = lddz, g.b = w, g.ldb = ldw;
+  g.I = M, g.J = K, g.K = N;
+  g.c = dx, g.ldc = lddx, g.z = const_cast<void*>(z), g.ldz = ldz, g.e = add, g.lde = ldadd;
+  g.act = act;
+  g.partial = static_cast<float*>(workspace);
+  return dtype == DDP_BF16 ? launch_product<DDP_BF16, DDP_LINEAR_BACKWARD_INPUT>(g, c, as_stream(stream))
+                           : launch_product<DDP_FP32, DDP_LINEAR_BACKWARD_INPUT>(g, c, as_stream(stream));
+}
+
+extern "C" int ddp_linear_backward_weight(const void* dz, int64_t lddz, const void* x, int64_t ldx, void* dw,
+                                          int64_t lddw, void* db, int64_t M, int64_t N, int64_t K, int32_t dtype,
+                                          int32_t grad_dtype, int32_t accumulate, void* workspace,
+                                          int64_t workspace_bytes, void* stream) {
+  const char* fn = "ddp_linear_backward_weight";
+  int st = check_common(fn, M, N, K, dtype, DDP_ACT_NONE);
+  if (st != DDP_OK) return st;
+  if (grad_dtype != dtype && grad_dtype != DDP_FP32)
+    return fail(DDP_EINVAL, std::string(fn) + ": grad_dtype must be the data's or fp32");
+  if (accumulate != 0 && accumulate != 1) return fail(DDP_EINVAL, std::string(fn) + ": accumulate must be 0 or 1");
+  if (N == 0) return DDP_OK;
+  const int eb = elem_bytes(dtype), gb = elem_bytes(grad_dtype);
+  const Cut c = cut_of(N, K, M, dtype);
+  const int64_t parts_need = K > 0 ? partial_bytes(c, N, K) : 0;
+  const int64_t need = parts_need + (db != nullptr ? bias_bytes(M, N) : 0);
+  const Matrix m[] = {{dz, M, N, lddz, eb, "dz", false, false}, {x, M, K, ldx, eb, "x", false, false},
+                      {dw, N, K, lddw, gb, "dw", true, false},  {db, 1, N, N, gb, "db", true, true},
+                      {need > 0 ? workspace : nullptr, 1, need, need, 1, "workspace", true, true}};
+  st = check_workspace(fn, workspace, workspace_bytes, need);
+  if (st != DDP_OK) return st;
+  st = check_matrices(fn, m, 5, -1, -1);
+  if (st != DDP_OK) return st;
+  hipStream_t s = as_stream(stream);
+  if (K > 0) {
+    LinearArgs g{};
+    g.a = dz, g.lda = lddz, g.b = x, g.ldb = ldx;
+    g.I = N, g.J = K, g.K = M;
+    g.c = dw, g.ldc = lddw;
+    g.grad32 = grad_dtype == DDP_FP32, g.accumulate = accumulate;
+    g.partial = static_cast<float*>(workspace);
+    st = dtype == DDP_BF16 ? launch_product<DDP_BF16, DDP_LINEAR_BACKWARD_WEIGHT>(g, c, s)
+                           : launch_product<DDP_FP32, DDP_LINEAR_BACKWARD_WEIGHT>(g, c, s);
+    if (st != DDP_OK) return st;
+  }
+  if (db == nullptr) return DDP_OK;
+  float* partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + parts_need);
+  const int64_t parts = div_up(M, kBiasRows);
+  if (parts > 65535) return fail(DDP_EINVAL, std::string(fn) + ": too many rows for the bias gradient");
+  if (parts > 0) {
+    const dim3 grid(unsigned(div_up(N, 512)), unsigned(parts));
+    if (dtype == DDP_BF16)
+      hipLaunchKernelGGL(k_bias_parts<DDP_BF16>, grid, dim3(kThreads), 0, s, dz, lddz, M, N, partial);
+    else
+      hipLaunchKernelGGL(k_bias_parts<DDP_FP32>, grid, dim3(kThreads), 0, s, dz, lddz, M, N, partial);
+    DDP_HIP_TRY(hipGetLastError(), "ddp_linear_backward_weight: bias launch");
+  }
+  const dim3 grid(unsigned(div_up(N, kThreads)));
+  if (grad_dtype == DDP_BF16)
+    hipLaunchKernelGGL(k_bias_join<DDP_BF16>, grid, dim3(kThreads), 0, s, partial, parts, N, db, accumulate);
+  else
+    hipLaunchKernelGGL(k_bias_join<DDP_FP32>, grid, dim3(kThreads), 0, s, partial, parts, N, db, accumulate);
+  DDP_HIP_TRY(hipGetLastError(), "ddp_linear_backward_weight: bias join launch");
+  return DDP_OK;
+}
+
+extern "C" int ddp_act_backward(const void* dy, int64_t lddy, const void* z, int64_t ldz, void* dz, int64_t lddz,
+                                int64_t M, int64_t N, int32_t dtype, int32_t act, void* stream) {
+  const char* fn = "ddp_act_backward";
+  int st = check_common(fn, M, N, 0, dtype, act);
+  if (st != DDP_OK) return st;
+  if (M == 0 || N == 0) return DDP_OK;
+  const int eb = elem_bytes(dtype);
+  const Matrix m[] = {{dy, M, N, lddy, eb, "dy", false, false}, {z, M, N, ldz, eb, "z", false, false},
+                      {dz, M, N, lddz, eb, "dz", true, false}};
+  st = check_matrices(fn, m, 3, 0, 2);
+  if (st != DDP_OK) return st;
+  const dim3 grid(unsigned(std::min<int64_t>(div_up(M * div_up(N, 8), kThreads), 1 << 16)));
+  if (dtype == DDP_BF16)
+    hipLaunchKernelGGL(k_act_backward<DDP_BF16>, grid, dim3(kThreads), 0, as_stream(stream), dy, lddy, z, ldz, dz, lddz, M, N, act);
+  else
+    hipLaunchKernelGGL(k_act_backward<DDP_FP32>, grid, dim3(kThreads), 0, as_stream(stream), dy, lddy, z, ldz, dz, lddz, M, N, act);
+  DDP_HIP_TRY(hipGetLastError(), "ddp_act_backward: launch");
+  return DDP_OK;
+}
