@@ -10,10 +10,9 @@
 // in the forward product), or with k going from row to row ("across": w in
 // the input gradient, both operands of the weight gradient).
 //
-// A block computes a tile of C in steps of 128 bytes of k (64 bf16 or 32 fp32
-// values). Both operands' parts of a step lie in LDS as they lie in memory,
-// in 16-byte chunks, the next step's on their way while this one's are
-// multiplied. A lane of a 32 x 32 matrix instruction needs one row's k values
+// A block computes a tile of C in steps of 64 or 128 bytes of k. Both operands'
+// parts of a step lie in LDS as they lie in memory, in 16-byte chunks, the
+// next steps' on their way while this one's are multiplied. A lane of a 32 x 32 matrix instruction needs one row's k values
 // 8h .. 8h+7 (h: its half of the wave): 16 bytes of an "along" row, or, of an
 // "across" operand, eight rows' values of one column, which the transposing
 // LDS read gathers (bf16), or four single reads (fp32).
@@ -58,67 +57,90 @@ constexpr bool b_along(int dir) { return dir == DDP_LINEAR_FORWARD; }
 
 // ---------------------------------------------------------------- activations
 
-__device__ __forceinline__ float act_value(float z, int act) {
-  switch (act) {
-    case DDP_ACT_RELU:
-      return z > 0.0f ? z : (z != z ? z : 0.0f);
-    case DDP_ACT_GELU:
-      return 0.5f * z * (1.0f + erff(z * 0.70710678f));
-    case DDP_ACT_GELU_TANH: {
-      // 1 + tanh(u) = 2 / (1 + exp(-2u))
-      const float u2 = z * fmaf(0.0713548163f, z * z, 1.59576912f);  // 2 sqrt(2/pi) (z + 0.044715 z^3)
-      return z / (1.0f + __expf(-u2));
-    }
-    case DDP_ACT_SILU:
-      return z / (1.0f + __expf(-z));
-    default:
-      return z;
-  }
+// x / y by the reciprocal instruction (1 ulp): the outputs' last step takes
+// the vector units while the matrix units wait, so its length counts.
+__device__ __forceinline__ float quotient(float x, float y) { return x * __builtin_amdgcn_rcpf(y); }
+
+// 2 sqrt(2/pi) (z + 0.044715 z^3) = z (kTanh1 + kTanh3 z^2); 1 + tanh(u) = 2 / (1 + exp(-2u))
+constexpr float kTanh1 = 1.59576912f, kTanh3 = 0.0713548163f;
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
+  if constexpr (ACT == DDP_ACT_RELU) return z < 0.0f ? 0.0f : z;  // a NaN stays
+  if constexpr (ACT == DDP_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
+  if constexpr (ACT == DDP_ACT_GELU_TANH) return quotient(z, 1.0f + __expf(-z * fmaf(kTanh3, z * z, kTanh1)));
+  if constexpr (ACT == DDP_ACT_SILU) return quotient(z, 1.0f + __expf(-z));
+  return z;
 }
 
 // The slopes are flat to the last bit beyond |z| = 16 (silu: 104), where their
 // factors would become infinity times zero. A NaN stays.
 __device__ __forceinline__ float within(float z, float most) { return z > most ? most : z < -most ? -most : z; }
 
-__device__ __forceinline__ float act_slope(float z, int act) {
-  z = within(z, act == DDP_ACT_SILU ? 104.0f : 16.0f);
-  switch (act) {
-    case DDP_ACT_RELU:
-      return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
-    case DDP_ACT_GELU:
-      return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * 0.39894228f * __expf(-0.5f * z * z);
-    case DDP_ACT_GELU_TANH: {
-      const float z2 = z * z;
-      const float s = 1.0f / (1.0f + __expf(-z * fmaf(0.0713548163f, z2, 1.59576912f)));  // (1 + tanh u) / 2
-      // s + z s (1 - s) 2u'
-      return fmaf(z * s * (1.0f - s), fmaf(3.0f * 0.0713548163f, z2, 1.59576912f), s);
-    }
-    case DDP_ACT_SILU: {
-      const float s = 1.0f / (1.0f + __expf(-z));
-      return s * fmaf(z, 1.0f - s, 1.0f);
-    }
-    default:
-      return 1.0f;
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+  if constexpr (ACT == DDP_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
+  if constexpr (ACT == DDP_ACT_GELU) {
+    z = within(z, 16.0f);
+    return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * 0.39894228f * __expf(-0.5f * z * z);
   }
+  if constexpr (ACT == DDP_ACT_GELU_TANH) {
+    z = within(z, 16.0f);
+    const float z2 = z * z;
+    const float s = quotient(1.0f, 1.0f + __expf(-z * fmaf(kTanh3, z2, kTanh1)));  // (1 + tanh u) / 2
+    return fmaf(z * s * (1.0f - s), fmaf(3.0f * kTanh3, z2, kTanh1), s);             // s + z s (1 - s) 2u'
+  }
+  if constexpr (ACT == DDP_ACT_SILU) {
+    z = within(z, 104.0f);
+    const float s = quotient(1.0f, 1.0f + __expf(-z));
+    return s * fmaf(z, 1.0f - s, 1.0f);
+  }
+  return 1.0f;
 }
 
 // ---------------------------------------------------------------- eight outputs of a row
 
+// Eight elements of a row as they lie in memory: bf16 in `a`, fp32 in both.
+struct Raw8 {
+  u32x4 a, b;
+};
 // Elements [0, n) of eight at p (element-aligned), the rest zero.
 template <int DT>
-__device__ __forceinline__ void load8(const void* p, int64_t at, int n, float v[8]) {
-  if (n == 8) {
-    if constexpr (DT == DDP_FP32) {
-      const float* q = static_cast<const float*>(p) + at;
-      load4<DDP_FP32, false>(q, 0, v);
-      load4<DDP_FP32, false>(q, 1, v + 4);
+__device__ __forceinline__ Raw8 load_raw8(const void* p, int64_t at, int n) {
+  Raw8 r{};
+  if constexpr (DT == DDP_FP32) {
+    const float* q = static_cast<const float*>(p) + at;
+    if (n == 8) {
+      r.a = load_at<false, u32x4_at4>(q, 0);
+      r.b = load_at<false, u32x4_at4>(q, 1);
     } else {
-      const u32x4 w = load_at<false, u32x4_at2>(static_cast<const uint16_t*>(p) + at, 0);
-      for (int k = 0; k < 4; ++k) v[2 * k] = bf16_lo(w[k]), v[2 * k + 1] = bf16_hi(w[k]);
+      for (int k = 0; k < 4; ++k)
+        if (k < n) r.a[k] = __float_as_uint(q[k]);
+      for (int k = 4; k < 8; ++k)
+        if (k < n) r.b[k - 4] = __float_as_uint(q[k]);
     }
   } else {
-    for (int k = 0; k < 8; ++k) v[k] = k < n ? Ops<DT>::load1(p, at + k) : 0.0f;
+    const uint16_t* q = static_cast<const uint16_t*>(p) + at;
+    if (n == 8) {
+      r.a = load_at<false, u32x4_at2>(q, 0);
+    } else {
+      for (int k = 0; k < 8; ++k)
+        if (k < n) r.a[k >> 1] |= uint32_t(q[k]) << ((k & 1) * 16);
+    }
   }
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ void unpack8(const Raw8& r, float v[8]) {
+  if constexpr (DT == DDP_FP32) {
+    for (int k = 0; k < 4; ++k) v[k] = __uint_as_float(r.a[k]), v[4 + k] = __uint_as_float(r.b[k]);
+  } else {
+    for (int k = 0; k < 4; ++k) v[2 * k] = bf16_lo(r.a[k]), v[2 * k + 1] = bf16_hi(r.a[k]);
+  }
+}
+template <int DT>
+__device__ __forceinline__ void load8(const void* p, int64_t at, int n, float v[8]) {
+  unpack8<DT>(load_raw8<DT>(p, at, n), v);
 }
 
 template <int DT>
@@ -139,92 +161,119 @@ __device__ __forceinline__ void store8(void* p, int64_t at, int n, const float v
   }
 }
 
-// What an output needs besides its sum: the residual, add and z, or the old
-// gradient. Loaded ahead of the sums, which arrive later.
+// What eight outputs need besides their sums, as it lies in memory: the
+// residual, add and z, or the old gradient. Loaded ahead of their use.
 struct Extra {
-  float e[8], z[8];
+  Raw8 e, z;
 };
 
 template <int DT, int DIR>
 __device__ __forceinline__ void load_extra(const LinearArgs& g, int64_t i, int64_t j, int n, Extra& x) {
   if constexpr (DIR == DDP_LINEAR_BACKWARD_WEIGHT) {
-    if (g.accumulate) {
-      if (g.grad32)
-        load8<DDP_FP32>(g.c, i * g.ldc + j, n, x.e);
-      else
-        load8<DT>(g.c, i * g.ldc + j, n, x.e);
-    }
+    if (g.accumulate) x.e = g.grad32 ? load_raw8<DDP_FP32>(g.c, i * g.ldc + j, n) : load_raw8<DT>(g.c, i * g.ldc + j, n);
   } else {
-    if (g.e != nullptr) load8<DT>(g.e, i * g.lde + j, n, x.e);
-    if (DIR == DDP_LINEAR_BACKWARD_INPUT && g.z != nullptr) load8<DT>(g.z, i * g.ldz + j, n, x.z);
+    if (g.e != nullptr) x.e = load_raw8<DT>(g.e, i * g.lde + j, n);
+    if (DIR == DDP_LINEAR_BACKWARD_INPUT && g.act != DDP_ACT_NONE) x.z = load_raw8<DT>(g.z, i * g.ldz + j, n);
   }
 }
 
-// Eight sums of row i from column j on (n of them inside C) become outputs.
-template <int DT, int DIR>
-__device__ __forceinline__ void finish(const LinearArgs& g, int64_t i, int64_t j, int n, float v[8], const Extra& x,
-                                       const float bias[8]) {
-  if constexpr (DIR == DDP_LINEAR_FORWARD) {
-    if (g.bias != nullptr)
-      for (int k = 0; k < 8; ++k) v[k] += bias[k];
-    if (g.z != nullptr) store8<DT>(g.z, i * g.ldz + j, n, v);
-    for (int k = 0; k < 8; ++k) v[k] = act_value(v[k], g.act);
-    if (g.e != nullptr)
-      for (int k = 0; k < 8; ++k) v[k] += x.e[k];
-    store8<DT>(g.c, i * g.ldc + j, n, v);
-  } else if constexpr (DIR == DDP_LINEAR_BACKWARD_INPUT) {
-    if (g.z != nullptr)
-      for (int k = 0; k < 8; ++k) v[k] *= act_slope(x.z[k], g.act);
-    if (g.e != nullptr)
-      for (int k = 0; k < 8; ++k) v[k] += x.e[k];
-    store8<DT>(g.c, i * g.ldc + j, n, v);
+// Eight sums of row i from column j on (n of them inside C) become outputs:
+// what is done before the store of C, z's store with it ...
+template <int DT, int DIR, int ACT>
+__device__ __forceinline__ void before_store(const LinearArgs& g, int64_t i, int64_t j, int n, float v[8], const Extra& x,
+                                             const float bias[8]) {
+  float e[8];
+  if constexpr (DIR == DDP_LINEAR_BACKWARD_WEIGHT) {
+    if (g.accumulate) {
+      if (g.grad32)
+        unpack8<DDP_FP32>(x.e, e);
+      else
+        unpack8<DT>(x.e, e);
+      for (int k = 0; k < 8; ++k) v[k] += e[k];
+    }
   } else {
-    if (g.accumulate)
-      for (int k = 0; k < 8; ++k) v[k] += x.e[k];
-    if (g.grad32)
-      store8<DDP_FP32>(g.c, i * g.ldc + j, n, v);
-    else
-      store8<DT>(g.c, i * g.ldc + j, n, v);
+    if constexpr (DIR == DDP_LINEAR_FORWARD) {
+      for (int k = 0; k < 8; ++k) v[k] += bias[k];  // zeros without a bias
+      if (g.z != nullptr) store8<DT>(g.z, i * g.ldz + j, n, v);
+      for (int k = 0; k < 8; ++k) v[k] = act_value<ACT>(v[k]);
+    } else if constexpr (ACT != DDP_ACT_NONE) {
+      float z[8];
+      unpack8<DT>(x.z, z);
+      for (int k = 0; k < 8; ++k) v[k] *= act_slope<ACT>(z[k]);
+    }
+    if (g.e != nullptr) {
+      unpack8<DT>(x.e, e);
+      for (int k = 0; k < 8; ++k) v[k] += e[k];
+    }
   }
+}
+// ... and the store.
+template <int DT, int DIR>
+__device__ __forceinline__ void store_output(const LinearArgs& g, int64_t i, int64_t j, int n, const float v[8]) {
+  if (DIR == DDP_LINEAR_BACKWARD_WEIGHT && g.grad32)
+    store8<DDP_FP32>(g.c, i * g.ldc + j, n, v);
+  else
+    store8<DT>(g.c, i * g.ldc + j, n, v);
+}
+// Both, with the loads, for any activation.
+template <int DT, int DIR>
+__device__ __forceinline__ void finish(const LinearArgs& g, int64_t i, int64_t j, int n, float v[8], const float bias[8]) {
+  Extra x;
+  load_extra<DT, DIR>(g, i, j, n, x);
+  switch (g.act) {
+#define DDP_ACT_CASE(A)                                   \
+  case A:                                                 \
+    before_store<DT, DIR, A>(g, i, j, n, v, x, bias);     \
+    break;
+    DDP_ACT_CASE(DDP_ACT_RELU)
+    DDP_ACT_CASE(DDP_ACT_GELU)
+    DDP_ACT_CASE(DDP_ACT_GELU_TANH)
+    DDP_ACT_CASE(DDP_ACT_SILU)
+#undef DDP_ACT_CASE
+    default:
+      before_store<DT, DIR, DDP_ACT_NONE>(g, i, j, n, v, x, bias);
+  }
+  store_output<DT, DIR>(g, i, j, n, v);
 }
 
 // ---------------------------------------------------------------- an operand's tile
 
-// T rows of C's side (i or j) by 128 bytes of k, in LDS as 16-byte chunks.
-// "along": T rows of 8 chunks. A read takes the same chunk of 8 neighbouring
-// rows at a time, 128 bytes apart, so chunk c of row r is kept at c ^ (r & 7):
-// the reads then touch all banks.
-// "across": one row of T elements per k. The transposing read takes 4
-// neighbouring rows of 32 bytes at a time, so those are kept apart by
-// exchanging chunks by the row's last two bits.
+// T rows of C's side (i or j) by SB bytes of k, in LDS as 16-byte chunks.
+// "along": T rows of SB bytes. A read takes the same chunk of 16 neighbouring
+// rows at a time; 256 / SB rows fill the 64 banks, so chunk c of row r is kept
+// at c ^ (r / (256 / SB)) and the reads touch every bank once.
+// "across": one row of T elements per k. The transposing read takes 64 bytes
+// of 4 neighbouring rows at a time, which are kept apart by exchanging chunks
+// by the row's last two bits.
+// (Exchanges made for 32 banks ran 2 to 3 % slower.)
 // (The exchange is applied to the address that a lane loads from: a direct
 // load to LDS writes the wave's 64 chunks in lane order.)
-template <int DT, bool ALONG, int T, int THREADS>
+template <int DT, bool ALONG, int T, int SB, int THREADS>
 struct Tile {
   static constexpr int ES = DT == DDP_BF16 ? 2 : 4;
   static constexpr int V = 16 / ES;             // elements per chunk
-  static constexpr int STEP = 128 / ES;         // k per step
-  static constexpr int BYTES = T * 128;
-  static constexpr int ROW = T * ES;            // "across": bytes per row
-  static constexpr int CPR = ALONG ? 8 : ROW / 16;
-  static constexpr int N = T * 8 / THREADS;     // chunks per thread
-  static_assert(T * 8 % THREADS == 0, "whole chunks per thread");
+  static constexpr int STEP = SB / ES;          // k per step
+  static constexpr int BYTES = T * SB;
+  static constexpr int ROW = ALONG ? SB : T * ES;
+  static constexpr int CPR = ROW / 16;
+  static constexpr int N = BYTES / 16 / THREADS;  // chunks per thread
+  static_assert(BYTES % (16 * THREADS) == 0, "whole chunks per thread");
 
   static __device__ __forceinline__ int swizzle(int row) {
-    if (ALONG) return row & 7;
-    return DT == DDP_BF16 ? (row & 3) << 1 : 0;
+    if (ALONG) return (row / (256 / SB)) & (CPR - 1);
+    return DT == DDP_BF16 ? (row & 3) << 2 : 0;
   }
   // Chunk q of the tile in LDS: its row, and the chunk of memory it holds.
   static __device__ __forceinline__ int row_of(int q) { return q / CPR; }
   static __device__ __forceinline__ int col_of(int q) { return (q % CPR) ^ swizzle(q / CPR); }
 
   // This lane's part of the fragment for rows [32 * t, 32 * t + 32) from
-  // `base` on and the s-th quarter of the step.
+  // `base` on and the s-th 32 bytes of the step.
   static __device__ __forceinline__ u32x4 fragment(const char* lds, int base, int t, int s, int lane) {
     if constexpr (ALONG) {
       const int row = base + 32 * t + (lane & 31);
-      const int c = (2 * s + (lane >> 5)) ^ (lane & 7);
-      return *reinterpret_cast<const u32x4*>(lds + row * 128 + c * 16);
+      const int c = (2 * s + (lane >> 5)) ^ swizzle(lane & 31);  // as of `row`: base and 32 t are multiples of 32
+      return *reinterpret_cast<const u32x4*>(lds + row * SB + c * 16);
     } else if constexpr (DT == DDP_BF16) {
       const int group = lane >> 4, in = lane & 15;
       const int k = 16 * s + 8 * (group >> 1) + (in >> 2);
@@ -260,8 +309,8 @@ __device__ __forceinline__ f32x16 multiply(u32x4 row, u32x4 col, f32x16 d) {
 
 // ---------------------------------------------------------------- loading a tile
 
-constexpr uint32_t kFar = 0xfffffff0u;      // an offset outside every descriptor's range: reads as zeros
-constexpr uint32_t kMostRange = 0xf0000000u;
+constexpr uint32_t kFar = 0xfffffff0u;     // an offset outside every descriptor's range: reads as zeros
+constexpr int32_t kMostRange = 0x0f000000; // of a descriptor, in 16-byte chunks
 
 // Direct loads to LDS, for operands whose every chunk is 16-byte aligned and
 // whole. The descriptor ends with the operand, so a chunk past it reads as
@@ -269,56 +318,58 @@ constexpr uint32_t kMostRange = 0xf0000000u;
 // products are not stored).
 template <class TL, bool ALONG, int THREADS>
 struct DirectLoader {
-  const char* p;           // the tile at the current step
-  int64_t left;            // bytes from p to the operand's end
-  int64_t advance;         // bytes per step
-  int64_t k_left;          // terms left
-  uint32_t off[TL::N];     // of this lane's chunks from p
-  int32_t k_of[TL::N];     // first term of each, within the step
-  int wave;
+  const char* p;        // the tile at the current step
+  int64_t advance;      // bytes per step
+  int32_t left;         // chunks from p to the operand's end
+  int32_t k_left;       // terms left
+  uint32_t off[TL::N];  // of this lane's chunks, in bytes from p
+  int32_t wave;
+  u32x4 desc;
 
+  // First term, within the step, of this lane's n-th chunk.
+  __device__ __forceinline__ int k_of(int n) const {
+    const int q = (n * (THREADS / 64) + wave) * 64 + (int(threadIdx.x) & 63);
+    return ALONG ? TL::col_of(q) * TL::V : TL::row_of(q);
+  }
   __device__ __forceinline__ void init(const void* base, int64_t ld, int64_t side, int64_t K, int64_t s0, int64_t k0, int64_t k1) {
     const int lane = int(threadIdx.x) & 63;
     wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const int64_t rows = ALONG ? side : K, cols = ALONG ? K : side;
-    const int64_t start = ALONG ? (s0 * ld + k0) * TL::ES : (k0 * ld + s0) * TL::ES;
-    p = static_cast<const char*>(base) + start;
-    left = ((rows - 1) * ld + cols) * TL::ES - start;
-    advance = ALONG ? 128 : TL::STEP * ld * TL::ES;
-    k_left = k1 - k0;
+    const int64_t start = ALONG ? s0 * ld + k0 : k0 * ld + s0;
+    p = static_cast<const char*>(base) + start * TL::ES;
+    left = int32_t(((rows - 1) * ld + cols - start) / TL::V);
+    advance = ALONG ? TL::ROW : TL::STEP * ld * TL::ES;
+    k_left = int32_t(k1 - k0);
 #pragma unroll
     for (int n = 0; n < TL::N; ++n) {
       const int q = (n * (THREADS / 64) + wave) * 64 + lane;
-      const int row = TL::row_of(q), col = TL::col_of(q);
-      if (ALONG) {
-        const int64_t r = s0 + row < side ? row : side - 1 - s0;
-        off[n] = uint32_t(r * ld * TL::ES + col * 16);
-        k_of[n] = col * TL::V;
-      } else {
-        off[n] = uint32_t(int64_t(row) * ld * TL::ES + col * 16);
-        k_of[n] = row;
-      }
+      const int64_t row = TL::row_of(q);
+      const int64_t r = ALONG && s0 + row >= side ? side - 1 - s0 : row;
+      off[n] = uint32_t(r * ld * TL::ES + TL::col_of(q) * 16);
     }
   }
-  // Starts the loads of the current step into `lds` and moves on.
-  __device__ __forceinline__ void issue(const char* lds) {
+  // The current step's loads into `lds`: begin() and load(n) for every n,
+  // then end(). Loads that the sum does not need read as zeros.
+  __device__ __forceinline__ void begin() {
     const uint64_t a = reinterpret_cast<uint64_t>(p);
-    const uint32_t range = left <= 0 ? 0u : left < int64_t(kMostRange) ? uint32_t(left) : kMostRange;
-    const u32x4 desc = {uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(a))),
-                        uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(a >> 32))),
-                        uint32_t(__builtin_amdgcn_readfirstlane(range)), 0x00020000u};
+    const int32_t range = left < 0 ? 0 : left < kMostRange ? left : kMostRange;
+    desc = u32x4{uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(a))),
+                 uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(a >> 32))),
+                 uint32_t(__builtin_amdgcn_readfirstlane(range)) << 4, 0x00020000u};
+  }
+  __device__ __forceinline__ void load(const char* lds, int n) {
     const uint32_t to = uint32_t(reinterpret_cast<uintptr_t>((DDP_LDS const char*)lds));
-#pragma unroll
-    for (int n = 0; n < TL::N; ++n) {
-      const uint32_t o = k_of[n] < k_left ? off[n] : kFar;
-      const uint32_t m = uint32_t(__builtin_amdgcn_readfirstlane(to + (n * (THREADS / 64) + wave) * 1024));
-      // No output register: the load ends in LDS, and every use of it stands
-      // behind a wait for vmcnt(0) and a barrier. (With the builtin, the
-      // compiler waits for all direct loads before any read of LDS.)
-      asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(o), "s"(desc), "s"(m) : "m0");
-    }
+    const uint32_t m = uint32_t(__builtin_amdgcn_readfirstlane(to + (n * (THREADS / 64) + wave) * 1024));
+    uint32_t o = off[n];
+    if (k_left < TL::STEP) o = k_of(n) < k_left ? o : kFar;  // uniform: the last step only
+    // No output register: the load ends in LDS, and every use of it stands
+    // behind a wait for it and a barrier. (With the builtin, the
+    // compiler waits for all direct loads before any read of LDS.)
+    asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(o), "s"(desc), "s"(m) : "m0");
+  }
+  __device__ __forceinline__ void end() {
     p += advance;
-    left -= advance;
+    left -= int32_t(advance / 16);
     k_left -= TL::STEP;
   }
   __device__ __forceinline__ void commit(char*) {}
@@ -337,34 +388,32 @@ struct AnyLoader {
     base = static_cast<const char*>(b);
     ld = ld_, side = side_, s0 = s0_, k = k0, k1 = k1_;
   }
-  __device__ __forceinline__ void issue(const char*) {
-#pragma unroll
-    for (int n = 0; n < TL::N; ++n) {
-      const int q = n * THREADS + int(threadIdx.x);
-      const int row = TL::row_of(q), col = TL::col_of(q) * TL::V;
-      const int64_t r = ALONG ? (s0 + row < side ? s0 + row : side - 1) : k + row;
-      const int64_t e = ALONG ? k + col : s0 + col;    // first element in its row
-      const int64_t end = ALONG ? k1 : side;           // elements of the row that count
-      x[n] = u32x4{0u, 0u, 0u, 0u};
-      if (!ALONG && r >= k1) continue;
-      const char* p = base + (r * ld + e) * TL::ES;
-      if (e + TL::V <= end) {
-        if constexpr (DT == DDP_FP32)
-          x[n] = load_at<false, u32x4_at4>(p, 0);
-        else
-          x[n] = load_at<false, u32x4_at2>(p, 0);
-      } else if (e < end) {
-        if constexpr (DT == DDP_FP32) {
-          for (int j = 0; j < TL::V - 1; ++j)
-            if (e + j < end) x[n][j] = reinterpret_cast<const uint32_t*>(p)[j];
-        } else {
-          for (int j = 0; j < TL::V - 1; ++j)
-            if (e + j < end) x[n][j >> 1] |= uint32_t(reinterpret_cast<const uint16_t*>(p)[j]) << ((j & 1) * 16);
-        }
+  __device__ __forceinline__ void begin() {}
+  __device__ __forceinline__ void load(const char*, int n) {
+    const int q = n * THREADS + int(threadIdx.x);
+    const int row = TL::row_of(q), col = TL::col_of(q) * TL::V;
+    const int64_t r = ALONG ? (s0 + row < side ? s0 + row : side - 1) : k + row;
+    const int64_t e = ALONG ? k + col : s0 + col;    // first element in its row
+    const int64_t end = ALONG ? k1 : side;           // elements of the row that count
+    x[n] = u32x4{0u, 0u, 0u, 0u};
+    if (!ALONG && r >= k1) return;
+    const char* p = base + (r * ld + e) * TL::ES;
+    if (e + TL::V <= end) {
+      if constexpr (DT == DDP_FP32)
+        x[n] = load_at<false, u32x4_at4>(p, 0);
+      else
+        x[n] = load_at<false, u32x4_at2>(p, 0);
+    } else if (e < end) {
+      if constexpr (DT == DDP_FP32) {
+        for (int j = 0; j < TL::V - 1; ++j)
+          if (e + j < end) x[n][j] = reinterpret_cast<const uint32_t*>(p)[j];
+      } else {
+        for (int j = 0; j < TL::V - 1; ++j)
+          if (e + j < end) x[n][j >> 1] |= uint32_t(reinterpret_cast<const uint16_t*>(p)[j]) << ((j & 1) * 16);
       }
     }
-    k += TL::STEP;
   }
+  __device__ __forceinline__ void end() { k += TL::STEP; }
   __device__ __forceinline__ void commit(char* lds) {
 #pragma unroll
     for (int n = 0; n < TL::N; ++n) *reinterpret_cast<u32x4*>(lds + (n * THREADS + int(threadIdx.x)) * 16) = x[n];
@@ -378,14 +427,19 @@ template <int DT, int DIR, int TI, int TJ, int WI, int WJ, bool DIRECT>
 __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
   constexpr int THREADS = WI * WJ * 64;
   constexpr int FI = TI / WI / 32, FJ = TJ / WJ / 32;  // 32 x 32 products per wave
-  using TA = Tile<DT, a_along(DIR), TI, THREADS>;
-  using TB = Tile<DT, b_along(DIR), TJ, THREADS>;
+  // Steps of 128 bytes of k, one on its way while one is multiplied. (Four
+  // stages of 64 bytes, three of them on their way, ran 15 % slower: twice the
+  // barriers. 4 waves with 128 x 128 products each read a third less from LDS
+  // but have nobody to fill their waits: 9 % slower.)
+  constexpr int SB = 128, S = 2;
+  using TA = Tile<DT, a_along(DIR), TI, SB, THREADS>;
+  using TB = Tile<DT, b_along(DIR), TJ, SB, THREADS>;
   using LA = std::conditional_t<DIRECT, DirectLoader<TA, a_along(DIR), THREADS>, AnyLoader<DT, TA, a_along(DIR), THREADS>>;
   using LB = std::conditional_t<DIRECT, DirectLoader<TB, b_along(DIR), THREADS>, AnyLoader<DT, TB, b_along(DIR), THREADS>>;
   constexpr int STAGE = TA::BYTES + TB::BYTES;
   constexpr int PITCH = 32 * FJ + 4;  // floats; the outputs' way through LDS
-  static_assert(WI * WJ * 32 * PITCH * 4 <= 2 * STAGE, "the outputs' rows fit");
-  __shared__ __attribute__((aligned(1024))) char lds[2 * STAGE];
+  static_assert(WI * WJ * 32 * PITCH * 4 <= S * STAGE, "the outputs' rows fit");
+  __shared__ __attribute__((aligned(1024))) char lds[S * STAGE];
 
   // Blocks go to the 8 XCDs in turn: XCD x takes the tiles of eighth x, in
   // groups of 8 tile rows, so that blocks that share operands share an L2.
@@ -413,96 +467,182 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
     la.init(g.a, g.lda, g.I, g.K, i0, k0, k1);
     lb.init(g.b, g.ldb, g.J, g.K, j0, k0, k1);
     u32x4 fa[2][FI], fb[2][FJ];
-    const auto read = [&](const char* stage, int s, int to) {
-#pragma unroll
-      for (int a = 0; a < FI; ++a) fa[to][a] = TA::fragment(stage, wi, a, s, lane);
-#pragma unroll
-      for (int b = 0; b < FJ; ++b) fb[to][b] = TB::fragment(stage + TA::BYTES, wj, b, s, lane);
+    // Fragment m of quarter s: B's first, then A's.
+    const auto read_one = [&](const char* stage, int s, int to, int m) {
+      if (m < FJ)
+        fb[to][m] = TB::fragment(stage + TA::BYTES, wj, m, s, lane);
+      else
+        fa[to][m - FJ] = TA::fragment(stage, wi, m - FJ, s, lane);
     };
-    const auto product = [&](int from) {
+    // The products of the fragments in `from`, with step(m) after the m-th. The
+    // order written is the schedule: left to itself, the compiler moves the
+    // LDS reads down to the products that use them, and a wave then waits for
+    // each quarter's.
+    const auto products = [&](int from, auto&& step) {
 #pragma unroll
-      for (int a = 0; a < FI; ++a)
-#pragma unroll
-        for (int b = 0; b < FJ; ++b) acc[a][b] = multiply<DT>(fb[from][b], fa[from][a], acc[a][b]);
+      for (int m = 0; m < FI * FJ; ++m) {
+        const int a = m / FJ, b = m % FJ;
+        acc[a][b] = multiply<DT>(fb[from][b], fa[from][a], acc[a][b]);
+        __builtin_amdgcn_sched_barrier(0);
+        step(m);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     };
-    // The loads of a step have landed, and every wave is done with the other stage.
-    const auto turn = [&] {
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    // Every wave is done with the stage read last, and the loads of the next
+    // one have landed: all but this wave's last S - 2 steps', and, behind the
+    // barrier, every wave's.
+    const auto turn = [&](bool all) {
+      if (all)
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      else
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"((S - 2) * (TA::N + TB::N)) : "memory");
       __syncthreads();
     };
-    la.issue(lds);
-    lb.issue(lds + TA::BYTES);
-    la.commit(lds);
-    lb.commit(lds + TA::BYTES);
-    turn();
-    read(lds, 0, 0);
-    for (int t = 0; t < steps; ++t) {
-      const char* stage = lds + (t & 1) * STAGE;
-      char* next = lds + ((t & 1) ^ 1) * STAGE;
-      const bool more = t + 1 < steps;
-      if (more) {
-        la.issue(next);
-        lb.issue(next + TA::BYTES);
-      }
-      read(stage, 1, 1);
-      product(0);
-      read(stage, 2, 0);
-      product(1);
-      read(stage, 3, 1);
-      product(0);
-      if (more) {
-        la.commit(next);
-        lb.commit(next + TA::BYTES);
-        turn();
-        read(next, 0, 0);
-      }
-      product(1);
+    constexpr int P = FI * FJ, Q = SB / 32, LOADS = TA::N + TB::N;
+    const auto load_one = [&](char* stage, int n) {
+      if (n < TA::N)
+        la.load(stage, n);
+      else
+        lb.load(stage + TA::BYTES, n - TA::N);
+    };
+    const int first = steps < S - 1 ? steps : S - 1;
+    for (int t = 0; t < first; ++t) {
+      la.begin();
+      lb.begin();
+#pragma unroll
+      for (int n = 0; n < LOADS; ++n) load_one(lds + t * STAGE, n);
+      la.end();
+      lb.end();
+      la.commit(lds + t * STAGE);
+      lb.commit(lds + t * STAGE + TA::BYTES);
     }
-    __syncthreads();  // LDS is free for the outputs
+    turn(first < S - 1);
+#pragma unroll
+    for (int m = 0; m < FI + FJ; ++m) read_one(lds, 0, 0, m);
+    for (int t = 0; t < steps; ++t) {
+      const char* stage = lds + t % S * STAGE;
+      const char* next = lds + (t + 1) % S * STAGE;
+      char* to = lds + (t + S - 1) % S * STAGE;
+      const bool more = t + S - 1 < steps;
+      if (more) {
+        la.begin();
+        lb.begin();
+      }
+      // All but the last 32 bytes of k: after each product a read of the next
+      // 32 bytes, or one of the loads.
+#pragma unroll
+      for (int s = 0; s < Q - 1; ++s) {
+        products(s & 1, [&](int m) {
+#pragma unroll
+          for (int r = 0; r < FI + FJ; ++r)
+            if (r * P / (FI + FJ) == m) read_one(stage, s + 1, (s + 1) & 1, r);
+          if (more) {
+#pragma unroll
+            for (int n = 0; n < LOADS; ++n)
+              if (n * P / LOADS == m && s == 0) load_one(to, n);
+          }
+        });
+      }
+      if (more) {
+        la.end();
+        lb.end();
+        la.commit(to);
+        lb.commit(to + TA::BYTES);
+      }
+      if (t + 1 < steps) {
+        turn(!more);
+#pragma unroll
+        for (int m = 0; m < FI + FJ; ++m) read_one(next, 0, 0, m);
+      }
+      products((Q - 1) & 1, [](int) {});
+    }
   }
 
   // The outputs leave by rows: a wave writes 32 rows of its sums to LDS (a
   // lane holds four neighbouring columns of one row at a time) and reads them
   // back eight columns to a lane, so that loads and stores cover whole lines.
   // Each wave has its own part of LDS.
+  if (steps > 0) __syncthreads();  // every wave is done with the operands there
   float* const mine = reinterpret_cast<float*>(lds) + wave * 32 * PITCH;
   constexpr int LPR = 4 * FJ;        // lanes per row
   constexpr int RPP = 64 / LPR;      // rows per pass
-  constexpr int PASSES = 32 / RPP;
+  const int64_t i_lane = i0 + wi + lane / LPR;
   const int64_t j = j0 + wj + lane % LPR * 8;
   const int n = g.J - j >= 8 ? 8 : g.J - j > 0 ? int(g.J - j) : 0;
   float bias[8] = {};
   if (DIR == DDP_LINEAR_FORWARD && g.bias != nullptr && n > 0) load8<DT>(g.bias, j, n, bias);
+  // Rows leave in batches of two passes, so that their values and what they
+  // need besides stay in registers next to the sums. What a batch needs is
+  // loaded before the stores of the batch before it: a later load would wait
+  // for those, too. One copy of the code serves all batches.
+  constexpr int BATCH = 2, ROWS = BATCH * RPP, PER = 32 / ROWS;
+  const bool whole = i0 + TI <= g.I && j0 + TJ <= g.J;
   const int64_t jp = (g.J + 7) / 8 * 8;
+  Extra x[BATCH];
+  if (g.parts == 1 && whole) {
 #pragma unroll
-  for (int a = 0; a < FI; ++a) {
-    const int64_t i_first = i0 + wi + 32 * a + lane / LPR;
-    Extra x[PASSES];
-    if (g.parts == 1 && n > 0) {
+    for (int p = 0; p < BATCH; ++p) load_extra<DT, DIR>(g, i_lane + p * RPP, j, 8, x[p]);
+  }
+#pragma unroll 1
+  for (int it = 0; it < FI * PER; ++it) {
+    if (it % PER == 0) {
 #pragma unroll
-      for (int p = 0; p < PASSES; ++p)
-        if (i_first + p * RPP < g.I) load_extra<DT, DIR>(g, i_first + p * RPP, j, n, x[p]);
+      for (int c = 0; c < FI; ++c) {
+        if (c != it / PER) continue;
+#pragma unroll
+        for (int b = 0; b < FJ; ++b)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<f32x4*>(mine + (lane & 31) * PITCH + 32 * b + 8 * q + 4 * (lane >> 5)) =
+                f32x4{acc[c][b][4 * q], acc[c][b][4 * q + 1], acc[c][b][4 * q + 2], acc[c][b][4 * q + 3]};
+      }
+      __builtin_amdgcn_wave_barrier();
     }
+    float v[BATCH][8];
 #pragma unroll
-    for (int b = 0; b < FJ; ++b)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<f32x4*>(mine + (lane & 31) * PITCH + 32 * b + 8 * q + 4 * (lane >> 5)) =
-            f32x4{acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      const float* src = mine + (lane / LPR + p * RPP) * PITCH + lane % LPR * 8;
+    for (int p = 0; p < BATCH; ++p) {
+      const float* src = mine + (it % PER * ROWS + lane / LPR + p * RPP) * PITCH + lane % LPR * 8;
       const f32x4 lo = *reinterpret_cast<const f32x4*>(src), hi = *reinterpret_cast<const f32x4*>(src + 4);
-      float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      const int64_t i = i_first + p * RPP;
-      if (i >= g.I || n == 0) continue;
-      if (g.parts > 1)
-        store8<DDP_FP32>(g.partial, (part * g.I + i) * jp + j, 8, v);
-      else
-        finish<DT, DIR>(g, i, j, n, v, x[p], bias);
+      for (int k = 0; k < 4; ++k) v[p][k] = lo[k], v[p][4 + k] = hi[k];
     }
     __builtin_amdgcn_wave_barrier();
+    const int64_t i = i_lane + it * ROWS;
+    if (g.parts > 1) {
+#pragma unroll
+      for (int p = 0; p < BATCH; ++p)
+        if (i + p * RPP < g.I && n > 0) store8<DDP_FP32>(g.partial, (part * g.I + i + p * RPP) * jp + j, 8, v[p]);
+    } else if (whole) {
+      const auto values = [&](auto act) __attribute__((always_inline)) {
+#pragma unroll
+        for (int p = 0; p < BATCH; ++p) before_store<DT, DIR, decltype(act)::value>(g, i + p * RPP, j, 8, v[p], x[p], bias);
+      };
+      switch (g.act) {
+#define DDP_ACT_CASE(A)                           \
+  case A:                                         \
+    values(std::integral_constant<int, A>{});     \
+    break;
+        DDP_ACT_CASE(DDP_ACT_RELU)
+        DDP_ACT_CASE(DDP_ACT_GELU)
+        DDP_ACT_CASE(DDP_ACT_GELU_TANH)
+        DDP_ACT_CASE(DDP_ACT_SILU)
+#undef DDP_ACT_CASE
+        default:
+          values(std::integral_constant<int, DDP_ACT_NONE>{});
+      }
+      if (it + 1 < FI * PER) {
+#pragma unroll
+        for (int p = 0; p < BATCH; ++p) load_extra<DT, DIR>(g, i + ROWS + p * RPP, j, 8, x[p]);
+      }
+#pragma unroll
+      for (int p = 0; p < BATCH; ++p) store_output<DT, DIR>(g, i + p * RPP, j, 8, v[p]);
+    } else if (n > 0) {
+#pragma unroll 1
+      for (int p = 0; p < BATCH; ++p) {
+        float w[8];
+        for (int k = 0; k < 8; ++k) w[k] = p == 0 ? v[0][k] : v[1][k];
+        if (i + p * RPP < g.I) finish<DT, DIR>(g, i + p * RPP, j, n, w, bias);
+      }
+    }
   }
 }
 
@@ -514,8 +654,6 @@ __global__ __launch_bounds__(kThreads) void k_linear_join(LinearArgs g) {
   if (at >= g.I * jv) return;
   const int64_t i = at / jv, j = at % jv * 8;
   const int n = g.J - j >= 8 ? 8 : int(g.J - j);
-  Extra x;
-  load_extra<DT, DIR>(g, i, j, n, x);
   float bias[8] = {};
   if (DIR == DDP_LINEAR_FORWARD && g.bias != nullptr) load8<DT>(g.bias, j, n, bias);
   float v[8] = {};
@@ -524,7 +662,7 @@ __global__ __launch_bounds__(kThreads) void k_linear_join(LinearArgs g) {
     load8<DDP_FP32>(g.partial, (p * g.I + i) * jv * 8 + j, 8, w);
     for (int k = 0; k < 8; ++k) v[k] += w[k];
   }
-  finish<DT, DIR>(g, i, j, n, v, x, bias);
+  finish<DT, DIR>(g, i, j, n, v, bias);
 }
 
 // ---------------------------------------------------------------- the bias gradient
@@ -569,9 +707,9 @@ __global__ __launch_bounds__(kThreads) void k_bias_join(const float* partial, in
 
 // ---------------------------------------------------------------- element by element
 
-template <int DT>
+template <int DT, int ACT>
 __global__ __launch_bounds__(kThreads) void k_act_backward(const void* dy, int64_t lddy, const void* z, int64_t ldz,
-                                                           void* dz, int64_t lddz, int64_t M, int64_t N, int act) {
+                                                           void* dz, int64_t lddz, int64_t M, int64_t N) {
   const int64_t nv = (N + 7) / 8;
   for (int64_t at = int64_t(blockIdx.x) * kThreads + threadIdx.x; at < M * nv; at += int64_t(gridDim.x) * kThreads) {
     const int64_t m = at / nv, j = at % nv * 8;
@@ -579,7 +717,7 @@ __global__ __launch_bounds__(kThreads) void k_act_backward(const void* dy, int64
     float g[8], x[8];
     load8<DT>(dy, m * lddy + j, n, g);
     load8<DT>(z, m * ldz + j, n, x);
-    for (int k = 0; k < 8; ++k) g[k] *= act_slope(x[k], act);
+    for (int k = 0; k < 8; ++k) g[k] *= act_slope<ACT>(x[k]);
     store8<DT>(dz, m * lddz + j, n, g);
   }
 }
@@ -587,6 +725,24 @@ __global__ __launch_bounds__(kThreads) void k_act_backward(const void* dy, int64
 // ---------------------------------------------------------------- host side
 
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <int DT>
+void launch_act_backward(const void* dy, int64_t lddy, const void* z, int64_t ldz, void* dz, int64_t lddz, int64_t M,
+                         int64_t N, int32_t act, hipStream_t s) {
+  const dim3 grid(unsigned(std::min<int64_t>(div_up(M * div_up(N, 8), kThreads), 1 << 16))), block(kThreads);
+  switch (act) {
+#define DDP_ACT_CASE(A)                                                                                     \
+  case A:                                                                                                   \
+    hipLaunchKernelGGL((k_act_backward<DT, A>), grid, block, 0, s, dy, lddy, z, ldz, dz, lddz, M, N);        \
+    break;
+    DDP_ACT_CASE(DDP_ACT_NONE)
+    DDP_ACT_CASE(DDP_ACT_RELU)
+    DDP_ACT_CASE(DDP_ACT_GELU)
+    DDP_ACT_CASE(DDP_ACT_GELU_TANH)
+    DDP_ACT_CASE(DDP_ACT_SILU)
+#undef DDP_ACT_CASE
+  }
+}
 
 // How a product is cut. The tile is 256 x 256 where there are enough of them
 // to fill the device and the operands can be loaded directly, else 128 x 128,
@@ -598,7 +754,7 @@ struct Cut {
   int64_t part_k;
 };
 Cut cut_of(int64_t I, int64_t J, int64_t K, int dtype) {
-  const int64_t step = 128 / elem_bytes(dtype);
+  const int64_t step = 128 / elem_bytes(dtype);  // whole steps of either loader
   Cut c{div_up(I, 256) * div_up(J, 256) >= 192 && dtype == DDP_BF16, 1, std::max<int64_t>(step, round_up(K, step))};
   const int64_t tiles = div_up(I, 128) * div_up(J, 128), steps = div_up(K, step);
   if (!c.big_if_direct && tiles < 256 && steps > 4) {
@@ -645,11 +801,14 @@ int launch_product(LinearArgs g, const Cut& c, hipStream_t s) {
   g.parts = c.parts;
   g.part_k = c.part_k;
   // Direct loads need whole, aligned chunks: the contiguous index of each
-  // operand a multiple of a chunk, and offsets within a tile below 2^32.
-  const auto direct = [&](const void* p, int64_t ld, int64_t contiguous) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % V == 0 && contiguous % V == 0 && ld <= (int64_t(1) << 21);
+  // operand a multiple of a chunk, offsets within a tile below 2^32 bytes and
+  // the whole operand below 2^31 chunks.
+  const auto direct = [&](const void* p, int64_t ld, int64_t rows, int64_t contiguous) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % V == 0 && contiguous % V == 0 && ld <= (int64_t(1) << 21) &&
+           rows * (ld / V) < (int64_t(1) << 31);
   };
-  const bool d = direct(g.a, g.lda, a_along(DIR) ? g.K : g.I) && direct(g.b, g.ldb, b_along(DIR) ? g.K : g.J);
+  const bool d = direct(g.a, g.lda, a_along(DIR) ? g.I : g.K, a_along(DIR) ? g.K : g.I) &&
+                 direct(g.b, g.ldb, b_along(DIR) ? g.J : g.K, b_along(DIR) ? g.K : g.J);
   int st;
   if (!d)
     st = launch_tiles<DT, DIR, 128, 2, 2, false>(g, s);
@@ -863,11 +1022,11 @@ extern "C" int ddp_act_backward(const void* dy, int64_t lddy, const void* z, int
                       {dz, M, N, lddz, eb, "dz", true, false}};
   st = check_matrices(fn, m, 3, 0, 2);
   if (st != DDP_OK) return st;
-  const dim3 grid(unsigned(std::min<int64_t>(div_up(M * div_up(N, 8), kThreads), 1 << 16)));
+  hipStream_t s = as_stream(stream);
   if (dtype == DDP_BF16)
-    hipLaunchKernelGGL(k_act_backward<DDP_BF16>, grid, dim3(kThreads), 0, as_stream(stream), dy, lddy, z, ldz, dz, lddz, M, N, act);
+    launch_act_backward<DDP_BF16>(dy, lddy, z, ldz, dz, lddz, M, N, act, s);
   else
-    hipLaunchKernelGGL(k_act_backward<DDP_FP32>, grid, dim3(kThreads), 0, as_stream(stream), dy, lddy, z, ldz, dz, lddz, M, N, act);
+    launch_act_backward<DDP_FP32>(dy, lddy, z, ldz, dz, lddz, M, N, act, s);
   DDP_HIP_TRY(hipGetLastError(), "ddp_act_backward: launch");
   return DDP_OK;
 }
