@@ -166,7 +166,8 @@ def _ptr_array(xs):
 
 def _stream(stream):
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        # torch.cuda.current_stream() without making its Stream object (3 us of a small call)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
@@ -520,11 +521,12 @@ def ddp_copy_probe(dst, src, nbytes=None, stream=None):
 NORMS = {"l2": 0, "max": 1}
 
 
-def _stream_context(stream):
-    """Allocations made under it belong to `stream` (None: the current one)."""
+def _empty(shape, dtype, stream):
+    """Memory that belongs to `stream` (None: the current one)."""
     if stream is None:
-        return torch.cuda.stream(None)
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+        return torch.empty(shape, dtype=dtype, device="cuda")
+    with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))):
+        return torch.empty(shape, dtype=dtype, device="cuda")
 
 
 def _device_tensors(tensors, dtype, numels, what):
@@ -559,8 +561,7 @@ class GradSet:
     def norm(self, kind="l2", out=None, stream=None):
         """The norm, as a float32 device tensor of one element (`out` if given)."""
         if out is None:
-            with _stream_context(stream):
-                out = torch.empty((), dtype=torch.float32, device="cuda")
+            out = _empty((), torch.float32, stream)
         elif out.dtype != torch.float32 or out.numel() != 1:
             raise ValueError("out must hold one float32")
         _check(_get_lib().ddp_grads_norm(self._h, NORMS[kind], out.data_ptr(), _stream(stream)))
@@ -657,11 +658,12 @@ def _matrix(t, rows, cols, dtype, what):
     """(pointer, leading dimension) of a rows x cols matrix; (None, cols) for None."""
     if t is None:
         return None, cols
-    if not t.is_cuda or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or t.dtype != dtype:
+    if t.dtype is not dtype or t.shape != (rows, cols) or not t.is_cuda:
         raise ValueError(f"{what} must be a {rows} x {cols} matrix of {dtype} on the GPU")
-    if cols > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"the rows of {what} must be contiguous")
-    return t.data_ptr(), (t.stride(0) if rows > 1 else max(cols, 1))
+    return t.data_ptr(), (ld if rows > 1 else max(cols, 1))
 
 
 def _vector(t, n, dtype, what):
@@ -674,17 +676,16 @@ def _vector(t, n, dtype, what):
 
 def _scratch(nbytes, workspace, stream):
     """The caller's workspace, or torch memory that belongs to the stream."""
-    if workspace is None and nbytes:
-        with _stream_context(stream):
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
-    return workspace, (0, None) if workspace is None else (workspace.numel() * workspace.element_size(), workspace.data_ptr())
+    if workspace is None:
+        if not nbytes:
+            return None, (0, None)
+        workspace = _empty(nbytes, torch.uint8, stream)
+        return workspace, (nbytes, workspace.data_ptr())
+    return workspace, (workspace.numel() * workspace.element_size(), workspace.data_ptr())
 
 
 def _result(out, rows, cols, dtype, stream):
-    if out is None:
-        with _stream_context(stream):
-            out = torch.empty(rows, cols, dtype=dtype, device="cuda")
-    return out
+    return _empty((rows, cols), dtype, stream) if out is None else out
 
 
 def linear_forward(x, w, bias=None, residual=None, act="none", keep=False, out=None, z=None, workspace=None, stream=None):

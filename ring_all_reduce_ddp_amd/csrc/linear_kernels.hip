@@ -49,6 +49,7 @@ struct LinearArgs {
   int32_t parts;       // blocks that share a tile's sum
   int64_t part_k;      // terms of one part (whole steps)
   float* partial;      // parts > 1: [part][I][round_up(J, 8)]
+  float* row_sums;     // weight gradient: [part * tiles_j + tile_j][I], sums of A's rows (NULL: not wanted)
   int32_t tiles_i, tiles_j;
 };
 
@@ -244,7 +245,7 @@ __device__ __forceinline__ void finish(const LinearArgs& g, int64_t i, int64_t j
 // at c ^ (r / (256 / SB)) and the reads touch every bank once.
 // "across": one row of T elements per k. The transposing read takes 64 bytes
 // of 4 neighbouring rows at a time, which are kept apart by exchanging chunks
-// by the row's last two bits.
+// by the row's low bits.
 // (Exchanges made for 32 banks ran 2 to 3 % slower.)
 // (The exchange is applied to the address that a lane loads from: a direct
 // load to LDS writes the wave's 64 chunks in lane order.)
@@ -261,7 +262,8 @@ struct Tile {
 
   static __device__ __forceinline__ int swizzle(int row) {
     if (ALONG) return (row / (256 / SB)) & (CPR - 1);
-    return DT == DDP_BF16 ? (row & 3) << 2 : 0;
+    if (DT != DDP_BF16) return 0;
+    return CPR > 8 ? (row & 3) << 2 : (row >> 1 & 1) << 2;  // rows of 128 bytes: two fill the banks as they lie
   }
   // Chunk q of the tile in LDS: its row, and the chunk of memory it holds.
   static __device__ __forceinline__ int row_of(int q) { return q / CPR; }
@@ -305,6 +307,16 @@ __device__ __forceinline__ f32x16 multiply(u32x4 row, u32x4 col, f32x16 d) {
       d = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(row[k]), __uint_as_float(col[k]), d, 0, 0, 0);
     return d;
   }
+}
+
+// The sum of a fragment's values in this lane: one row's, over its half of k.
+template <int DT>
+__device__ __forceinline__ float sum_of(u32x4 f) {
+  if constexpr (DT == DDP_BF16)
+    return ((bf16_lo(f[0]) + bf16_hi(f[0])) + (bf16_lo(f[1]) + bf16_hi(f[1]))) +
+           ((bf16_lo(f[2]) + bf16_hi(f[2])) + (bf16_lo(f[3]) + bf16_hi(f[3])));
+  else
+    return (__uint_as_float(f[0]) + __uint_as_float(f[1])) + (__uint_as_float(f[2]) + __uint_as_float(f[3]));
 }
 
 // ---------------------------------------------------------------- loading a tile
@@ -375,42 +387,99 @@ struct DirectLoader {
   __device__ __forceinline__ void commit(char*) {}
 };
 
-// Through registers, for operands of any alignment and width: whole chunks as
-// one load at their element's alignment, those over an edge element by
-// element, zeros past the sum's end.
+// Through registers, for operands of any alignment whose rows have a chunk's
+// elements at least. Every chunk is one load at its element's alignment,
+// without a branch that writes its registers (with one, each load is waited
+// for before the next starts: twice as slow). A chunk that runs over the
+// end of its row is loaded from as far back as it fits and shifted into place
+// when it goes to LDS, zeros following; one past the sum's end is shifted out
+// whole.
 template <int DT, class TL, bool ALONG, int THREADS>
 struct AnyLoader {
-  const char* base;
+  static constexpr int kWidth = TL::CPR * TL::V;  // "across": elements of a row in the tile
+  const char* p;         // the tile at the current step
+  int64_t row_bytes;
+  int32_t k_left;        // terms left
+  int32_t width;         // "across": elements of a row that exist
+  bool shifted;          // some chunk of the step is to be shifted
+  int64_t off[TL::N];    // of this lane's chunks, in bytes from p
+  int32_t shift[TL::N];  // elements to shift out
+  u32x4 x[TL::N];
+
+  static __device__ __forceinline__ int chunk(int n) { return n * THREADS + int(threadIdx.x); }
+  __device__ __forceinline__ void init(const void* base, int64_t ld, int64_t side, int64_t, int64_t s0, int64_t k0, int64_t k1) {
+    row_bytes = ld * TL::ES;
+    p = static_cast<const char*>(base) + (ALONG ? s0 * ld + k0 : k0 * ld + s0) * TL::ES;
+    k_left = int32_t(k1 - k0);
+    width = side - s0 < kWidth ? int32_t(side - s0) : kWidth;
+#pragma unroll
+    for (int n = 0; n < TL::N; ++n) {
+      const int row = TL::row_of(chunk(n)), col = TL::col_of(chunk(n)) * TL::V;
+      const int64_t r = ALONG && s0 + row >= side ? side - 1 - s0 : row;
+      const int back = !ALONG && col + TL::V > width ? col + TL::V - width : 0;
+      off[n] = r * row_bytes + (col - back) * TL::ES;  // from p, perhaps negative; never before the row
+      shift[n] = back;
+    }
+  }
+  __device__ __forceinline__ void begin() { shifted = k_left < TL::STEP || (!ALONG && width < kWidth); }
+  __device__ __forceinline__ void load(const char*, int n) {
+    int64_t o = off[n];
+    if (k_left < TL::STEP) {  // uniform: the last step
+      const int row = TL::row_of(chunk(n)), col = TL::col_of(chunk(n)) * TL::V;
+      if (ALONG) {
+        shift[n] = col + TL::V > k_left ? col + TL::V - k_left : 0;
+        o -= shift[n] * TL::ES;
+      } else if (row >= k_left) {
+        o -= (row - (k_left - 1)) * row_bytes;
+        shift[n] = TL::V;
+      }
+    }
+    if constexpr (DT == DDP_FP32)
+      x[n] = load_at<false, u32x4_at4>(p + o, 0);
+    else
+      x[n] = load_at<false, u32x4_at2>(p + o, 0);
+  }
+  __device__ __forceinline__ void end() {
+    p += ALONG ? TL::ROW : TL::STEP * row_bytes;
+    k_left -= TL::STEP;
+  }
+  __device__ __forceinline__ void commit(char* lds) {
+    if (shifted) {
+#pragma unroll
+      for (int n = 0; n < TL::N; ++n) {
+        const int bits = shift[n] * TL::ES * 8;
+        const unsigned __int128 v = __builtin_bit_cast(unsigned __int128, x[n]);
+        x[n] = bits < 128 ? __builtin_bit_cast(u32x4, v >> bits) : u32x4{0u, 0u, 0u, 0u};
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < TL::N; ++n) *reinterpret_cast<u32x4*>(lds + chunk(n) * 16) = x[n];
+  }
+};
+
+// Element by element, for rows shorter than a chunk.
+template <int DT, class TL, bool ALONG, int THREADS>
+struct ShortLoader {
+  const void* base;
   int64_t ld, side, s0, k, k1;
   u32x4 x[TL::N];
 
   __device__ __forceinline__ void init(const void* b, int64_t ld_, int64_t side_, int64_t, int64_t s0_, int64_t k0, int64_t k1_) {
-    base = static_cast<const char*>(b);
-    ld = ld_, side = side_, s0 = s0_, k = k0, k1 = k1_;
+    base = b, ld = ld_, side = side_, s0 = s0_, k = k0, k1 = k1_;
   }
   __device__ __forceinline__ void begin() {}
   __device__ __forceinline__ void load(const char*, int n) {
     const int q = n * THREADS + int(threadIdx.x);
     const int row = TL::row_of(q), col = TL::col_of(q) * TL::V;
     const int64_t r = ALONG ? (s0 + row < side ? s0 + row : side - 1) : k + row;
-    const int64_t e = ALONG ? k + col : s0 + col;    // first element in its row
-    const int64_t end = ALONG ? k1 : side;           // elements of the row that count
+    const int64_t e = ALONG ? k + col : s0 + col, end = ALONG ? k1 : side;
     x[n] = u32x4{0u, 0u, 0u, 0u};
-    if (!ALONG && r >= k1) return;
-    const char* p = base + (r * ld + e) * TL::ES;
-    if (e + TL::V <= end) {
+    for (int j = 0; j < TL::V; ++j) {
+      if (e + j >= end || (!ALONG && r >= k1)) continue;
       if constexpr (DT == DDP_FP32)
-        x[n] = load_at<false, u32x4_at4>(p, 0);
+        x[n][j] = static_cast<const uint32_t*>(base)[r * ld + e + j];
       else
-        x[n] = load_at<false, u32x4_at2>(p, 0);
-    } else if (e < end) {
-      if constexpr (DT == DDP_FP32) {
-        for (int j = 0; j < TL::V - 1; ++j)
-          if (e + j < end) x[n][j] = reinterpret_cast<const uint32_t*>(p)[j];
-      } else {
-        for (int j = 0; j < TL::V - 1; ++j)
-          if (e + j < end) x[n][j >> 1] |= uint32_t(reinterpret_cast<const uint16_t*>(p)[j]) << ((j & 1) * 16);
-      }
+        x[n][j >> 1] |= uint32_t(static_cast<const uint16_t*>(base)[r * ld + e + j]) << ((j & 1) * 16);
     }
   }
   __device__ __forceinline__ void end() { k += TL::STEP; }
@@ -420,10 +489,16 @@ struct AnyLoader {
   }
 };
 
+enum Loading { kDirect, kAny, kShort };
+template <int LOAD, int DT, class TL, bool ALONG, int THREADS>
+using LoaderOf = std::conditional_t<LOAD == kDirect, DirectLoader<TL, ALONG, THREADS>,
+                                    std::conditional_t<LOAD == kAny, AnyLoader<DT, TL, ALONG, THREADS>,
+                                                       ShortLoader<DT, TL, ALONG, THREADS>>>;
+
 // ---------------------------------------------------------------- the product
 
 // Tile TI x TJ of C by WI x WJ waves.
-template <int DT, int DIR, int TI, int TJ, int WI, int WJ, bool DIRECT>
+template <int DT, int DIR, int TI, int TJ, int WI, int WJ, int LOAD>
 __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
   constexpr int THREADS = WI * WJ * 64;
   constexpr int FI = TI / WI / 32, FJ = TJ / WJ / 32;  // 32 x 32 products per wave
@@ -434,8 +509,8 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
   constexpr int SB = 128, S = 2;
   using TA = Tile<DT, a_along(DIR), TI, SB, THREADS>;
   using TB = Tile<DT, b_along(DIR), TJ, SB, THREADS>;
-  using LA = std::conditional_t<DIRECT, DirectLoader<TA, a_along(DIR), THREADS>, AnyLoader<DT, TA, a_along(DIR), THREADS>>;
-  using LB = std::conditional_t<DIRECT, DirectLoader<TB, b_along(DIR), THREADS>, AnyLoader<DT, TB, b_along(DIR), THREADS>>;
+  using LA = LoaderOf<LOAD, DT, TA, a_along(DIR), THREADS>;
+  using LB = LoaderOf<LOAD, DT, TB, b_along(DIR), THREADS>;
   constexpr int STAGE = TA::BYTES + TB::BYTES;
   constexpr int PITCH = 32 * FJ + 4;  // floats; the outputs' way through LDS
   static_assert(WI * WJ * 32 * PITCH * 4 <= S * STAGE, "the outputs' rows fit");
@@ -460,6 +535,13 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
   for (int a = 0; a < FI; ++a)
 #pragma unroll
     for (int b = 0; b < FJ; ++b) acc[a][b] = f32x16{};
+  // The bias gradient is the sum of A's rows, whose fragments pass through
+  // the registers here anyway: every block of a tile row adds up its share of
+  // the steps (the first column of waves does), on vector units that the
+  // products leave idle. A pass of its own over dz took 12 us at 8192 x 2048.
+  const int tile_j = in_group / rows;
+  const bool sum_rows = DIR == DDP_LINEAR_BACKWARD_WEIGHT && g.row_sums != nullptr && wave % WJ == 0;
+  float row_sum[FI] = {};
 
   if (steps > 0) {
     LA la;
@@ -524,6 +606,13 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
       const char* next = lds + (t + 1) % S * STAGE;
       char* to = lds + (t + S - 1) % S * STAGE;
       const bool more = t + S - 1 < steps;
+      const bool sum_now = sum_rows && t % g.tiles_j == tile_j;
+      const auto add_rows = [&](int from) {
+        if (DIR == DDP_LINEAR_BACKWARD_WEIGHT && sum_now) {
+#pragma unroll
+          for (int a = 0; a < FI; ++a) row_sum[a] += sum_of<DT>(fa[from][a]);
+        }
+      };
       if (more) {
         la.begin();
         lb.begin();
@@ -542,6 +631,7 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
               if (n * P / LOADS == m && s == 0) load_one(to, n);
           }
         });
+        add_rows(s & 1);
       }
       if (more) {
         la.end();
@@ -555,6 +645,16 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
         for (int m = 0; m < FI + FJ; ++m) read_one(next, 0, 0, m);
       }
       products((Q - 1) & 1, [](int) {});
+      add_rows((Q - 1) & 1);
+    }
+  }
+
+  if (DIR == DDP_LINEAR_BACKWARD_WEIGHT && sum_rows) {
+#pragma unroll
+    for (int a = 0; a < FI; ++a) {
+      const float r = row_sum[a] + __shfl_xor(row_sum[a], 32);  // both halves of k
+      const int64_t i = i0 + wi + 32 * a + lane;
+      if (lane < 32 && i < g.I) g.row_sums[(int64_t(part) * g.tiles_j + tile_j) * g.I + i] = r;
     }
   }
 
@@ -667,42 +767,132 @@ __global__ __launch_bounds__(kThreads) void k_linear_join(LinearArgs g) {
 
 // ---------------------------------------------------------------- the bias gradient
 
-// Sums of dz's columns: a block takes kBiasRows rows of 512 columns (8 a
-// lane, each of the 4 waves every fourth row) and leaves one partial row.
-constexpr int kBiasRows = 256;
-
-template <int DT>
-__global__ __launch_bounds__(kThreads) void k_bias_parts(const void* dz, int64_t ld, int64_t M, int64_t N, float* partial) {
-  __shared__ float sums[4][512];
-  const int lane = int(threadIdx.x) & 63, wave = int(threadIdx.x) >> 6;
-  const int64_t j = int64_t(blockIdx.x) * 512 + lane * 8;
-  const int n = N - j >= 8 ? 8 : N - j > 0 ? int(N - j) : 0;
-  const int64_t m1 = std::min<int64_t>(M, int64_t(blockIdx.y + 1) * kBiasRows);
-  float s[8] = {};
-  if (n > 0) {
-#pragma unroll 8
-    for (int64_t m = int64_t(blockIdx.y) * kBiasRows + wave; m < m1; m += 4) {
-      float v[8];
-      load8<DT>(dz, m * ld + j, n, v);
-      for (int k = 0; k < 8; ++k) s[k] += v[k];
-    }
+// db (+)= sums of the columns of `rows` rows at src: the partial sums that the
+// weight gradient's blocks leave (or dz itself, where there are none of those
+// because the layer has no inputs). Four threads share a column.
+template <int SRC, int DST>
+__global__ __launch_bounds__(kThreads) void k_column_sums(const void* src, int64_t ld, int64_t rows, int64_t N, void* db,
+                                                          int accumulate) {
+  __shared__ float sums[4][64];
+  const int c = int(threadIdx.x) & 63, group = int(threadIdx.x) >> 6;
+  const int64_t col = int64_t(blockIdx.x) * 64 + c;
+  float s = 0.0f;
+  if (col < N) {
+#pragma unroll 4
+    for (int64_t r = group; r < rows; r += 4) s += Ops<SRC>::load1(src, r * ld + col);
   }
-  for (int k = 0; k < 8; ++k) sums[wave][lane * 8 + k] = s[k];
+  sums[group][c] = s;
   __syncthreads();
-  for (int c = threadIdx.x; c < 512; c += kThreads) {
-    const int64_t col = int64_t(blockIdx.x) * 512 + c;
-    if (col < N) partial[int64_t(blockIdx.y) * N + col] = (sums[0][c] + sums[1][c]) + (sums[2][c] + sums[3][c]);
-  }
+  if (group != 0 || col >= N) return;
+  s = (sums[0][c] + sums[1][c]) + (sums[2][c] + sums[3][c]);
+  if (accumulate) s += Ops<DST>::load1(db, col);
+  Ops<DST>::store1(db, col, DST == DDP_BF16 ? round_bf16(s) : s);
 }
 
+// ---------------------------------------------------------------- few rows
+
+// The forward product for up to kFewRows rows of x (tokens of an answer): w
+// is read once and each value meets every row's, so the bound is w's bytes. A
+// block takes 4 rows of w, its waves every fourth kilobyte of each; x stays in
+// the caches. (1 row, 8192 x 2048 bf16: NNN us, against 15 in 128 x 128 tiles.)
+constexpr int kFewRows = 4, kFewOuts = 4;
+
+// V = 16 / element size values of a row from k on, zeros past K.
 template <int DT>
-__global__ __launch_bounds__(kThreads) void k_bias_join(const float* partial, int64_t parts, int64_t N, void* db, int accumulate) {
-  const int64_t c = int64_t(blockIdx.x) * kThreads + threadIdx.x;
-  if (c >= N) return;
-  float s = 0.0f;
-  for (int64_t p = 0; p < parts; ++p) s += partial[p * N + c];
-  if (accumulate) s += Ops<DT>::load1(db, c);
-  Ops<DT>::store1(db, c, DT == DDP_BF16 ? round_bf16(s) : s);
+__device__ __forceinline__ u32x4 load_chunk(const void* p, int64_t at, int64_t k, int64_t K) {
+  constexpr int V = DT == DDP_BF16 ? 8 : 4;
+  if constexpr (DT == DDP_BF16) {
+    const uint16_t* q = static_cast<const uint16_t*>(p) + at;
+    if (k + V <= K) return load_at<false, u32x4_at2>(q, 0);
+    u32x4 r{};
+    for (int e = 0; e < V; ++e)
+      if (k + e < K) r[e >> 1] |= uint32_t(q[e]) << ((e & 1) * 16);
+    return r;
+  } else {
+    const float* q = static_cast<const float*>(p) + at;
+    if (k + V <= K) return load_at<false, u32x4_at4>(q, 0);
+    u32x4 r{};
+    for (int e = 0; e < V; ++e)
+      if (k + e < K) r[e] = __float_as_uint(q[e]);
+    return r;
+  }
+}
+template <int DT>
+__device__ __forceinline__ float dot_chunk(u32x4 a, u32x4 b, float s) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (DT == DDP_BF16)
+      s = fmaf(bf16_hi(a[e]), bf16_hi(b[e]), fmaf(bf16_lo(a[e]), bf16_lo(b[e]), s));
+    else
+      s = fmaf(__uint_as_float(a[e]), __uint_as_float(b[e]), s);
+  }
+  return s;
+}
+
+template <int DT, int M>
+__global__ __launch_bounds__(kThreads) void k_linear_few(LinearArgs g) {
+  constexpr int V = DT == DDP_BF16 ? 8 : 4, OUTS = kFewOuts * M;
+  __shared__ float sums[4][OUTS];
+  const int lane = int(threadIdx.x) & 63, wave = int(threadIdx.x) >> 6;
+  const int64_t j0 = int64_t(blockIdx.x) * kFewOuts;
+  float acc[OUTS] = {};  // [r * M + m]
+#pragma unroll 1
+  for (int64_t k = int64_t(threadIdx.x) * V; k < g.K; k += kThreads * V) {
+    u32x4 w[kFewOuts], x[M];
+#pragma unroll
+    for (int r = 0; r < kFewOuts; ++r) w[r] = load_chunk<DT>(g.b, (j0 + r < g.J ? j0 + r : g.J - 1) * g.ldb + k, k, g.K);
+#pragma unroll
+    for (int m = 0; m < M; ++m) x[m] = load_chunk<DT>(g.a, (m < g.I ? m : g.I - 1) * g.lda + k, k, g.K);
+#pragma unroll
+    for (int r = 0; r < kFewOuts; ++r)
+#pragma unroll
+      for (int m = 0; m < M; ++m) acc[r * M + m] = dot_chunk<DT>(w[r], x[m], acc[r * M + m]);
+  }
+  // Across the wave, halving the values a lane holds at each exchange: OUTS + 4
+  // exchanges or so instead of 6 OUTS. Lane bit d decides which half it keeps.
+  int kept = OUTS, index = 0;
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) {
+    if (kept > 1) {
+      kept /= 2;
+      const bool upper = (lane & d) != 0;
+      index += upper ? kept : 0;
+#pragma unroll
+      for (int v = 0; v < OUTS / 2; ++v) {
+        if (v >= kept) continue;
+        const float keep = upper ? acc[v + kept] : acc[v], give = upper ? acc[v] : acc[v + kept];
+        acc[v] = keep + __shfl_xor(give, d);
+      }
+    } else {
+      acc[0] += __shfl_xor(acc[0], d);
+    }
+  }
+  if (lane % (64 / OUTS) == 0) sums[wave][index] = acc[0];
+  __syncthreads();
+  const int r = int(threadIdx.x) / M, m = int(threadIdx.x) % M;
+  if (r >= kFewOuts || m >= g.I || j0 + r >= g.J) return;
+  const int64_t j = j0 + r;
+  float z = (sums[0][r * M + m] + sums[1][r * M + m]) + (sums[2][r * M + m] + sums[3][r * M + m]);
+  if (g.bias != nullptr) z += Ops<DT>::load1(g.bias, j);
+  const auto rounded = [](float v) { return DT == DDP_BF16 ? round_bf16(v) : v; };
+  if (g.z != nullptr) Ops<DT>::store1(g.z, m * g.ldz + j, rounded(z));
+  float y = z;
+  switch (g.act) {
+    case DDP_ACT_RELU:
+      y = act_value<DDP_ACT_RELU>(z);
+      break;
+    case DDP_ACT_GELU:
+      y = act_value<DDP_ACT_GELU>(z);
+      break;
+    case DDP_ACT_GELU_TANH:
+      y = act_value<DDP_ACT_GELU_TANH>(z);
+      break;
+    case DDP_ACT_SILU:
+      y = act_value<DDP_ACT_SILU>(z);
+      break;
+  }
+  if (g.e != nullptr) y += Ops<DT>::load1(g.e, m * g.lde + j);
+  Ops<DT>::store1(g.c, m * g.ldc + j, rounded(y));
 }
 
 // ---------------------------------------------------------------- element by element
@@ -744,34 +934,72 @@ void launch_act_backward(const void* dy, int64_t lddy, const void* z, int64_t ld
   }
 }
 
-// How a product is cut. The tile is 256 x 256 where there are enough of them
-// to fill the device and the operands can be loaded directly, else 128 x 128,
-// with the sum in parts when those are few. The parts do not depend on
-// alignment, so the workspace is known from the sizes.
+// How a product is cut: the tile's side (256 needs direct loads), and in how
+// many parts the sum. Up to kFewRows rows of a forward product go without
+// tiles.
 struct Cut {
-  bool big_if_direct;
-  int32_t parts;
-  int64_t part_k;
+  bool few = false;
+  int tile = 128;
+  int32_t parts = 1;
+  int64_t part_k = 0;
 };
-Cut cut_of(int64_t I, int64_t J, int64_t K, int dtype) {
-  const int64_t step = 128 / elem_bytes(dtype);  // whole steps of either loader
-  Cut c{div_up(I, 256) * div_up(J, 256) >= 192 && dtype == DDP_BF16, 1, std::max<int64_t>(step, round_up(K, step))};
-  const int64_t tiles = div_up(I, 128) * div_up(J, 128), steps = div_up(K, step);
-  if (!c.big_if_direct && tiles < 256 && steps > 4) {
-    const int64_t want = std::min(div_up(512, tiles), steps / 4);
-    if (want > 1) {
-      const int64_t per = div_up(steps, want);
-      c.part_k = per * step;
-      c.parts = int32_t(div_up(steps, per));
+
+// The cut with the least time by a rough model, in cycles, of what was measured on
+// MI355X: a CU's time for one step of a tile when its blocks fill it (`step`),
+// a block's own time per step when it is alone (kAlone), a tile's start and
+// outputs (`ends`), and the join of parts, a launch and their bytes.
+Cut cut_of(int dir, int64_t I, int64_t J, int64_t K, int dtype, bool direct) {
+  Cut best;
+  if (dir == DDP_LINEAR_FORWARD && I <= kFewRows) {
+    best.few = true;
+    return best;
+  }
+  struct Shape {
+    int tile, fit;        // blocks that fit a CU
+    int64_t step, ends;
+  };
+  static const Shape bf16[3] = {{64, 5, 380, 1500}, {128, 2, 1100, 4500}, {256, 1, 3400, 24000}};
+  static const Shape fp32[2] = {{64, 5, 1150, 1500}, {128, 2, 4700, 4500}};
+  constexpr int64_t kCus = 256, kAlone = 1800, kStart = 6000, kJoin = 14000, kBytesPerCycle = 2500;
+  const Shape* shapes = dtype == DDP_BF16 ? bf16 : fp32;
+  const int64_t row = std::min(a_along(dir) ? K : I, b_along(dir) ? K : J);  // the operands' shorter rows
+  const int n_shapes = row < 16 / elem_bytes(dtype) ? 1 : dtype == DDP_BF16 && direct ? 3 : 2;
+  const int64_t step = 128 / elem_bytes(dtype), steps = std::max<int64_t>(1, div_up(K, step));
+  int64_t least = INT64_MAX;
+  for (int k = 0; k < n_shapes; ++k) {
+    const Shape& sh = shapes[k];
+    const int64_t tiles = div_up(I, sh.tile) * div_up(J, sh.tile);
+    for (int want : {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 28, 32, 40, 48, 64}) {
+      if (want > 1 && (want > steps / 2 || tiles * want > 4 * kCus * sh.fit)) break;
+      const int64_t per = div_up(steps, want), parts = div_up(steps, per);
+      const int64_t on_cu = div_up(tiles * parts, kCus);
+      int64_t t = std::max(div_up(on_cu, sh.fit) * (kStart + per * kAlone), kStart + on_cu * (per * sh.step + sh.ends));
+      if (parts > 1) t += kJoin + (parts + 2) * I * J * 4 / kBytesPerCycle;
+      if (t >= least) continue;
+      least = t;
+      best.tile = sh.tile;
+      best.parts = int32_t(parts);
+      best.part_k = per * step;
     }
   }
-  return c;
+  return best;
 }
 
 int64_t partial_bytes(const Cut& c, int64_t I, int64_t J) {
   return c.parts > 1 ? round_up(int64_t(c.parts) * I * round_up(J, 8) * 4, 256) : 0;
 }
-int64_t bias_bytes(int64_t M, int64_t N) { return round_up(div_up(M, kBiasRows) * N * 4, 256); }
+// The bias gradient's partial rows, one per part and tile column.
+int64_t bias_bytes(const Cut& c, int64_t I, int64_t J) { return round_up(c.parts * div_up(J, c.tile) * I * 4, 256); }
+
+// Scratch of a product: for either loader, as the sizes alone do not tell which.
+int64_t scratch_bytes(int dir, int64_t I, int64_t J, int64_t K, int dtype, bool bias) {
+  int64_t most = 0;
+  for (bool direct : {false, true}) {
+    const Cut c = cut_of(dir, I, J, K, dtype, direct);
+    most = std::max(most, partial_bytes(c, I, J) + (bias ? bias_bytes(c, I, J) : 0));
+  }
+  return most;
+}
 
 // The sizes of a direction as those of C = A B^T.
 void product_sizes(int dir, int64_t M, int64_t N, int64_t K, int64_t* I, int64_t* J, int64_t* S) {
@@ -783,39 +1011,61 @@ void product_sizes(int dir, int64_t M, int64_t N, int64_t K, int64_t* I, int64_t
     *I = N, *J = K, *S = M;
 }
 
-template <int DT, int DIR, int T, int WI, int WJ, bool DIRECT>
+template <int DT, int DIR, int T, int WI, int WJ, int LOAD>
 int launch_tiles(LinearArgs& g, hipStream_t s) {
   const int64_t ti = div_up(g.I, T), tj = div_up(g.J, T);
   if (ti * tj * g.parts >= (int64_t(1) << 30)) return fail(DDP_EINVAL, "ddp_linear: too many tiles for one launch");
   g.tiles_i = int32_t(ti);
   g.tiles_j = int32_t(tj);
   const dim3 grid(unsigned(round_up(ti * tj * g.parts, 8))), block(WI * WJ * 64);
-  hipLaunchKernelGGL((k_linear<DT, DIR, T, T, WI, WJ, DIRECT>), grid, block, 0, s, g);
+  hipLaunchKernelGGL((k_linear<DT, DIR, T, T, WI, WJ, LOAD>), grid, block, 0, s, g);
   DDP_HIP_TRY(hipGetLastError(), "ddp_linear: launch");
   return DDP_OK;
 }
 
+// The product of g's operands; the workspace starts with the parts' sums, and
+// with want_rows has the row sums behind them.
 template <int DT, int DIR>
-int launch_product(LinearArgs g, const Cut& c, hipStream_t s) {
+int launch_product(LinearArgs& g, void* workspace, bool want_rows, hipStream_t s) {
   constexpr int V = 16 / (DT == DDP_BF16 ? 2 : 4);
-  g.parts = c.parts;
-  g.part_k = c.part_k;
   // Direct loads need whole, aligned chunks: the contiguous index of each
   // operand a multiple of a chunk, offsets within a tile below 2^32 bytes and
   // the whole operand below 2^31 chunks.
-  const auto direct = [&](const void* p, int64_t ld, int64_t rows, int64_t contiguous) {
+  const auto aligned = [&](const void* p, int64_t ld, int64_t rows, int64_t contiguous) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % V == 0 && contiguous % V == 0 && ld <= (int64_t(1) << 21) &&
            rows * (ld / V) < (int64_t(1) << 31);
   };
-  const bool d = direct(g.a, g.lda, a_along(DIR) ? g.I : g.K, a_along(DIR) ? g.K : g.I) &&
-                 direct(g.b, g.ldb, b_along(DIR) ? g.J : g.K, b_along(DIR) ? g.K : g.J);
-  int st;
-  if (!d)
-    st = launch_tiles<DT, DIR, 128, 2, 2, false>(g, s);
-  else if (DT == DDP_BF16 && c.big_if_direct)
-    st = launch_tiles<DT, DIR, DT == DDP_BF16 ? 256 : 128, 2, DT == DDP_BF16 ? 4 : 2, true>(g, s);
-  else
-    st = launch_tiles<DT, DIR, 128, 2, 2, true>(g, s);
+  const bool direct = aligned(g.a, g.lda, a_along(DIR) ? g.I : g.K, a_along(DIR) ? g.K : g.I) &&
+                      aligned(g.b, g.ldb, b_along(DIR) ? g.J : g.K, b_along(DIR) ? g.K : g.J);
+  const Cut c = cut_of(DIR, g.I, g.J, g.K, DT, direct);
+  const bool shorter = (a_along(DIR) ? g.K : g.I) < V || (b_along(DIR) ? g.K : g.J) < V;  // rows than a chunk
+  if constexpr (DIR == DDP_LINEAR_FORWARD) {
+    if (c.few) {
+      const dim3 grid(unsigned(div_up(g.J, kFewOuts))), block(kThreads);
+      if (g.I == 1)
+        hipLaunchKernelGGL((k_linear_few<DT, 1>), grid, block, 0, s, g);
+      else if (g.I == 2)
+        hipLaunchKernelGGL((k_linear_few<DT, 2>), grid, block, 0, s, g);
+      else
+        hipLaunchKernelGGL((k_linear_few<DT, kFewRows>), grid, block, 0, s, g);
+      DDP_HIP_TRY(hipGetLastError(), "ddp_linear: launch");
+      return DDP_OK;
+    }
+  }
+  g.parts = c.parts;
+  g.part_k = c.part_k;
+  g.partial = static_cast<float*>(workspace);
+  if (want_rows) g.row_sums = reinterpret_cast<float*>(static_cast<char*>(workspace) + partial_bytes(c, g.I, g.J));
+  int st = DDP_OK;
+  if constexpr (DT == DDP_BF16) {
+    if (c.tile == 256) st = launch_tiles<DT, DIR, 256, 2, 4, kDirect>(g, s);
+  }
+  if (shorter)
+    st = launch_tiles<DT, DIR, 64, 2, 2, kShort>(g, s);
+  else if (c.tile == 128)
+    st = direct ? launch_tiles<DT, DIR, 128, 2, 2, kDirect>(g, s) : launch_tiles<DT, DIR, 128, 2, 2, kAny>(g, s);
+  else if (c.tile == 64)
+    st = direct ? launch_tiles<DT, DIR, 64, 2, 2, kDirect>(g, s) : launch_tiles<DT, DIR, 64, 2, 2, kAny>(g, s);
   if (st != DDP_OK || g.parts == 1) return st;
   const int64_t blocks = div_up(g.I * div_up(g.J, 8), kThreads);
   hipLaunchKernelGGL((k_linear_join<DT, DIR>), dim3(unsigned(blocks)), dim3(kThreads), 0, s, g);
@@ -840,13 +1090,14 @@ int check_matrices(const char* fn, const Matrix* m, int n, int in_place, int out
   for (int k = 0; k < n; ++k) {
     const Matrix& x = m[k];
     if (x.p == nullptr && x.may_be_null) continue;
-    if (x.ld < x.cols) return fail(DDP_EINVAL, std::string(fn) + ": the leading dimension of " + x.what + " is less than its columns");
-    if (x.ld > (int64_t(1) << 31)) return fail(DDP_EINVAL, std::string(fn) + ": the leading dimension of " + x.what + " is too large");
+    if (x.ld < x.cols || x.ld > (int64_t(1) << 40)) return fail(DDP_EINVAL, std::string(fn) + ": the leading dimension of " + x.what + " is less than its columns, or absurd");
     if (x.bytes() == 0) continue;
     if (reinterpret_cast<uintptr_t>(x.p) % uintptr_t(x.eb) != 0)
       return fail(DDP_EINVAL, std::string(fn) + ": " + x.what + " is not aligned to its element");
     int st = check_range(x.p, x.bytes(), fn, x.what);
     if (st != DDP_OK) return st;
+    if (x.rows > 1 && x.ld > (int64_t(1) << 22))  // offsets within a tile are 32 bits wide
+      return fail(DDP_EINVAL, std::string(fn) + ": the leading dimension of " + x.what + " is over 2^22");
   }
   for (int k = 0; k < n; ++k) {
     if (!m[k].written || m[k].p == nullptr) continue;
@@ -863,7 +1114,7 @@ int check_matrices(const char* fn, const Matrix* m, int n, int in_place, int out
 int check_common(const char* fn, int64_t M, int64_t N, int64_t K, int32_t dtype, int32_t act) {
   if (!valid_dtype(dtype)) return fail(DDP_EINVAL, std::string(fn) + ": unknown dtype");
   if (act < DDP_ACT_NONE || act > DDP_ACT_SILU) return fail(DDP_EINVAL, std::string(fn) + ": unknown activation");
-  const int64_t most = int64_t(1) << 31;
+  const int64_t most = int64_t(1) << 31;  // sums and rows are counted in 32 bits
   if (M < 0 || N < 0 || K < 0 || M >= most || N >= most || K >= most)
     return fail(DDP_EINVAL, std::string(fn) + ": M, N and K must lie in [0, 2^31)");
   return DDP_OK;
@@ -892,8 +1143,7 @@ extern "C" int ddp_linear_workspace(int32_t direction, int64_t M, int64_t N, int
   if (st != DDP_OK) return st;
   int64_t I, J, S;
   product_sizes(direction, M, N, K, &I, &J, &S);
-  *bytes = partial_bytes(cut_of(I, J, S, dtype), I, J) +
-           (direction == DDP_LINEAR_BACKWARD_WEIGHT ? bias_bytes(M, N) : 0);
+  *bytes = scratch_bytes(direction, I, J, S, dtype, direction == DDP_LINEAR_BACKWARD_WEIGHT);
   return DDP_OK;
 }
 
@@ -906,8 +1156,7 @@ extern "C" int ddp_linear_forward(const void* x, int64_t ldx, const void* w, int
   if (st != DDP_OK) return st;
   if (M == 0 || N == 0) return DDP_OK;
   const int eb = elem_bytes(dtype);
-  const Cut c = cut_of(M, N, K, dtype);
-  const int64_t need = partial_bytes(c, M, N);
+  const int64_t need = scratch_bytes(DDP_LINEAR_FORWARD, M, N, K, dtype, false);
   const Matrix m[] = {{x, M, K, ldx, eb, "x", false, false},       {w, N, K, ldw, eb, "w", false, false},
                       {bias, 1, N, N, eb, "bias", false, true},    {residual, M, N, ldr, eb, "residual", false, true},
                       {y, M, N, ldy, eb, "y", true, false},        {z, M, N, ldz, eb, "z", true, true},
@@ -921,9 +1170,8 @@ extern "C" int ddp_linear_forward(const void* x, int64_t ldx, const void* w, int
   g.I = M, g.J = N, g.K = K;
   g.c = y, g.ldc = ldy, g.z = z, g.ldz = ldz, g.e = residual, g.lde = ldr, g.bias = bias;
   g.act = act;
-  g.partial = static_cast<float*>(workspace);
-  return dtype == DDP_BF16 ? launch_product<DDP_BF16, DDP_LINEAR_FORWARD>(g, c, as_stream(stream))
-                           : launch_product<DDP_FP32, DDP_LINEAR_FORWARD>(g, c, as_stream(stream));
+  return dtype == DDP_BF16 ? launch_product<DDP_BF16, DDP_LINEAR_FORWARD>(g, workspace, false, as_stream(stream))
+                           : launch_product<DDP_FP32, DDP_LINEAR_FORWARD>(g, workspace, false, as_stream(stream));
 }
 
 extern "C" int ddp_linear_backward_input(const void* dz, int64_t lddz, const void* w, int64_t ldw, const void* z,
@@ -936,8 +1184,7 @@ extern "C" int ddp_linear_backward_input(const void* dz, int64_t lddz, const voi
   if (z == nullptr && act != DDP_ACT_NONE) return fail(DDP_EINVAL, std::string(fn) + ": an activation's slope needs z");
   if (M == 0 || K == 0) return DDP_OK;
   const int eb = elem_bytes(dtype);
-  const Cut c = cut_of(M, K, N, dtype);
-  const int64_t need = partial_bytes(c, M, K);
+  const int64_t need = scratch_bytes(DDP_LINEAR_BACKWARD_INPUT, M, K, N, dtype, false);
   const Matrix m[] = {{dz, M, N, lddz, eb, "dz", false, false}, {w, N, K, ldw, eb, "w", false, false},
                       {z, M, K, ldz, eb, "z", false, true},     {add, M, K, ldadd, eb, "add", false, true},
                       {dx, M, K, lddx, eb, "dx", true, false},
@@ -951,9 +1198,8 @@ extern "C" int ddp_linear_backward_input(const void* dz, int64_t lddz, const voi
   g.I = M, g.J = K, g.K = N;
   g.c = dx, g.ldc = lddx, g.z = const_cast<void*>(z), g.ldz = ldz, g.e = add, g.lde = ldadd;
   g.act = act;
-  g.partial = static_cast<float*>(workspace);
-  return dtype == DDP_BF16 ? launch_product<DDP_BF16, DDP_LINEAR_BACKWARD_INPUT>(g, c, as_stream(stream))
-                           : launch_product<DDP_FP32, DDP_LINEAR_BACKWARD_INPUT>(g, c, as_stream(stream));
+  return dtype == DDP_BF16 ? launch_product<DDP_BF16, DDP_LINEAR_BACKWARD_INPUT>(g, workspace, false, as_stream(stream))
+                           : launch_product<DDP_FP32, DDP_LINEAR_BACKWARD_INPUT>(g, workspace, false, as_stream(stream));
 }
 
 extern "C" int ddp_linear_backward_weight(const void* dz, int64_t lddz, const void* x, int64_t ldx, void* dw,
@@ -968,9 +1214,7 @@ extern "C" int ddp_linear_backward_weight(const void* dz, int64_t lddz, const vo
   if (accumulate != 0 && accumulate != 1) return fail(DDP_EINVAL, std::string(fn) + ": accumulate must be 0 or 1");
   if (N == 0) return DDP_OK;
   const int eb = elem_bytes(dtype), gb = elem_bytes(grad_dtype);
-  const Cut c = cut_of(N, K, M, dtype);
-  const int64_t parts_need = K > 0 ? partial_bytes(c, N, K) : 0;
-  const int64_t need = parts_need + (db != nullptr ? bias_bytes(M, N) : 0);
+  const int64_t need = scratch_bytes(DDP_LINEAR_BACKWARD_WEIGHT, N, K, M, dtype, db != nullptr);
   const Matrix m[] = {{dz, M, N, lddz, eb, "dz", false, false}, {x, M, K, ldx, eb, "x", false, false},
                       {dw, N, K, lddw, gb, "dw", true, false},  {db, 1, N, N, gb, "db", true, true},
                       {need > 0 ? workspace : nullptr, 1, need, need, 1, "workspace", true, true}};
@@ -979,35 +1223,34 @@ extern "C" int ddp_linear_backward_weight(const void* dz, int64_t lddz, const vo
   st = check_matrices(fn, m, 5, -1, -1);
   if (st != DDP_OK) return st;
   hipStream_t s = as_stream(stream);
+  const void* sums = dz;  // what the bias gradient is summed from: without inputs, dz itself
+  int64_t sums_ld = lddz, sums_rows = M;
   if (K > 0) {
     LinearArgs g{};
     g.a = dz, g.lda = lddz, g.b = x, g.ldb = ldx;
     g.I = N, g.J = K, g.K = M;
     g.c = dw, g.ldc = lddw;
     g.grad32 = grad_dtype == DDP_FP32, g.accumulate = accumulate;
-    g.partial = static_cast<float*>(workspace);
-    st = dtype == DDP_BF16 ? launch_product<DDP_BF16, DDP_LINEAR_BACKWARD_WEIGHT>(g, c, s)
-                           : launch_product<DDP_FP32, DDP_LINEAR_BACKWARD_WEIGHT>(g, c, s);
+    st = dtype == DDP_BF16 ? launch_product<DDP_BF16, DDP_LINEAR_BACKWARD_WEIGHT>(g, workspace, db != nullptr, s)
+                           : launch_product<DDP_FP32, DDP_LINEAR_BACKWARD_WEIGHT>(g, workspace, db != nullptr, s);
     if (st != DDP_OK) return st;
+    sums = g.row_sums, sums_ld = N, sums_rows = int64_t(g.parts) * g.tiles_j;
   }
   if (db == nullptr) return DDP_OK;
-  float* partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + parts_need);
-  const int64_t parts = div_up(M, kBiasRows);
-  if (parts > 65535) return fail(DDP_EINVAL, std::string(fn) + ": too many rows for the bias gradient");
-  if (parts > 0) {
-    const dim3 grid(unsigned(div_up(N, 512)), unsigned(parts));
-    if (dtype == DDP_BF16)
-      hipLaunchKernelGGL(k_bias_parts<DDP_BF16>, grid, dim3(kThreads), 0, s, dz, lddz, M, N, partial);
+  const dim3 grid(unsigned(div_up(N, 64))), block(kThreads);
+  const bool from16 = K == 0 && dtype == DDP_BF16;
+  if (grad_dtype == DDP_BF16) {
+    if (from16)
+      hipLaunchKernelGGL((k_column_sums<DDP_BF16, DDP_BF16>), grid, block, 0, s, sums, sums_ld, sums_rows, N, db, accumulate);
     else
-      hipLaunchKernelGGL(k_bias_parts<DDP_FP32>, grid, dim3(kThreads), 0, s, dz, lddz, M, N, partial);
-    DDP_HIP_TRY(hipGetLastError(), "ddp_linear_backward_weight: bias launch");
+      hipLaunchKernelGGL((k_column_sums<DDP_FP32, DDP_BF16>), grid, block, 0, s, sums, sums_ld, sums_rows, N, db, accumulate);
+  } else {
+    if (from16)
+      hipLaunchKernelGGL((k_column_sums<DDP_BF16, DDP_FP32>), grid, block, 0, s, sums, sums_ld, sums_rows, N, db, accumulate);
+    else
+      hipLaunchKernelGGL((k_column_sums<DDP_FP32, DDP_FP32>), grid, block, 0, s, sums, sums_ld, sums_rows, N, db, accumulate);
   }
-  const dim3 grid(unsigned(div_up(N, kThreads)));
-  if (grad_dtype == DDP_BF16)
-    hipLaunchKernelGGL(k_bias_join<DDP_BF16>, grid, dim3(kThreads), 0, s, partial, parts, N, db, accumulate);
-  else
-    hipLaunchKernelGGL(k_bias_join<DDP_FP32>, grid, dim3(kThreads), 0, s, partial, parts, N, db, accumulate);
-  DDP_HIP_TRY(hipGetLastError(), "ddp_linear_backward_weight: bias join launch");
+  DDP_HIP_TRY(hipGetLastError(), "ddp_linear_backward_weight: bias launch");
   return DDP_OK;
 }
 
