@@ -15,6 +15,7 @@ library is loaded so that both use the single HIP runtime that torch ships.
 """
 
 import ctypes
+import functools
 import os
 import sys
 
@@ -649,8 +650,13 @@ LINEAR_FORWARD, LINEAR_BACKWARD_INPUT, LINEAR_BACKWARD_WEIGHT = 0, 1, 2
 
 def linear_workspace(direction, m, n, k, dtype):
     """Bytes of scratch that a linear call of these sizes needs."""
+    return _linear_workspace(int(direction), int(m), int(n), int(k), dtype_code(dtype))
+
+
+@functools.lru_cache(maxsize=4096)
+def _linear_workspace(direction, m, n, k, code):
     b = ctypes.c_int64()
-    _check(_get_lib().ddp_linear_workspace(int(direction), int(m), int(n), int(k), dtype_code(dtype), ctypes.byref(b)))
+    _check(_get_lib().ddp_linear_workspace(direction, m, n, k, code, ctypes.byref(b)))
     return b.value
 
 
@@ -703,7 +709,7 @@ def linear_forward(x, w, bias=None, residual=None, act="none", keep=False, out=N
     rp, ldr = _matrix(residual, m, n, dt, "residual")
     yp, ldy = _matrix(y, m, n, dt, "out")
     zp, ldz = _matrix(z, m, n, dt, "z")
-    ws, (nbytes, p) = _scratch(linear_workspace(LINEAR_FORWARD, m, n, k, code), workspace, stream)
+    ws, (nbytes, p) = _scratch(_linear_workspace(LINEAR_FORWARD, m, n, k, code), workspace, stream)
     _check(_get_lib().ddp_linear_forward(xp, ldx, wp, ldw, _vector(bias, n, dt, "bias"), rp, ldr, yp, ldy, zp, ldz,
                                          m, n, k, code, ACTIVATIONS[act], p, nbytes, _stream(stream)))
     return y if z is None else (y, z)
@@ -721,7 +727,7 @@ def linear_backward_input(dz, w, act="none", z=None, add=None, out=None, workspa
     zp, ldz = _matrix(z, m, k, dt, "z")
     ap, lda = _matrix(add, m, k, dt, "add")
     op, ldo = _matrix(dx, m, k, dt, "out")
-    ws, (nbytes, p) = _scratch(linear_workspace(LINEAR_BACKWARD_INPUT, m, n, k, code), workspace, stream)
+    ws, (nbytes, p) = _scratch(_linear_workspace(LINEAR_BACKWARD_INPUT, m, n, k, code), workspace, stream)
     _check(_get_lib().ddp_linear_backward_input(gp, ldg, wp, ldw, zp, ldz, ap, lda, op, ldo, m, n, k, code,
                                                 ACTIVATIONS[act], p, nbytes, _stream(stream)))
     return dx
@@ -738,7 +744,7 @@ def linear_backward_weight(dz, x, dw, db=None, accumulate=False, workspace=None,
     xp, ldx = _matrix(x, m, k, dt, "x")
     wp, ldw = _matrix(dw, n, k, gt, "dw")
     bp = _vector(db, n, gt, "db")
-    ws, (nbytes, p) = _scratch(linear_workspace(LINEAR_BACKWARD_WEIGHT, m, n, k, code), workspace, stream)
+    ws, (nbytes, p) = _scratch(_linear_workspace(LINEAR_BACKWARD_WEIGHT, m, n, k, code), workspace, stream)
     _check(_get_lib().ddp_linear_backward_weight(gp, ldg, xp, ldx, wp, ldw, bp, m, n, k, code, dtype_code(gt),
                                                  1 if accumulate else 0, p, nbytes, _stream(stream)))
 

@@ -361,7 +361,8 @@ struct DirectLoader {
     }
   }
   // The current step's loads into `lds`: begin() and load(n) for every n,
-  // then end(). Loads that the sum does not need read as zeros.
+  // then end(). Loads that the sum does not need read as zeros (FULL: it needs
+  // all of them).
   __device__ __forceinline__ void begin() {
     const uint64_t a = reinterpret_cast<uint64_t>(p);
     const int32_t range = left < 0 ? 0 : left < kMostRange ? left : kMostRange;
@@ -369,11 +370,12 @@ struct DirectLoader {
                  uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(a >> 32))),
                  uint32_t(__builtin_amdgcn_readfirstlane(range)) << 4, 0x00020000u};
   }
+  template <bool FULL>
   __device__ __forceinline__ void load(const char* lds, int n) {
     const uint32_t to = uint32_t(reinterpret_cast<uintptr_t>((DDP_LDS const char*)lds));
     const uint32_t m = uint32_t(__builtin_amdgcn_readfirstlane(to + (n * (THREADS / 64) + wave) * 1024));
     uint32_t o = off[n];
-    if (k_left < TL::STEP) o = k_of(n) < k_left ? o : kFar;  // uniform: the last step only
+    if (!FULL && k_left < TL::STEP) o = k_of(n) < k_left ? o : kFar;
     // No output register: the load ends in LDS, and every use of it stands
     // behind a wait for it and a barrier. (With the builtin, the
     // compiler waits for all direct loads before any read of LDS.)
@@ -422,9 +424,10 @@ struct AnyLoader {
     }
   }
   __device__ __forceinline__ void begin() { shifted = k_left < TL::STEP || (!ALONG && width < kWidth); }
+  template <bool FULL>
   __device__ __forceinline__ void load(const char*, int n) {
     int64_t o = off[n];
-    if (k_left < TL::STEP) {  // uniform: the last step
+    if (!FULL && k_left < TL::STEP) {
       const int row = TL::row_of(chunk(n)), col = TL::col_of(chunk(n)) * TL::V;
       if (ALONG) {
         shift[n] = col + TL::V > k_left ? col + TL::V - k_left : 0;
@@ -468,6 +471,7 @@ struct ShortLoader {
     base = b, ld = ld_, side = side_, s0 = s0_, k = k0, k1 = k1_;
   }
   __device__ __forceinline__ void begin() {}
+  template <bool FULL>
   __device__ __forceinline__ void load(const char*, int n) {
     const int q = n * THREADS + int(threadIdx.x);
     const int row = TL::row_of(q), col = TL::col_of(q) * TL::V;
@@ -506,15 +510,15 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
   // stages of 64 bytes, three of them on their way, ran 15 % slower: twice the
   // barriers. 4 waves with 128 x 128 products each read a third less from LDS
   // but have nobody to fill their waits: 9 % slower.)
-  constexpr int SB = 128, S = 2;
+  constexpr int SB = 128;
   using TA = Tile<DT, a_along(DIR), TI, SB, THREADS>;
   using TB = Tile<DT, b_along(DIR), TJ, SB, THREADS>;
   using LA = LoaderOf<LOAD, DT, TA, a_along(DIR), THREADS>;
   using LB = LoaderOf<LOAD, DT, TB, b_along(DIR), THREADS>;
   constexpr int STAGE = TA::BYTES + TB::BYTES;
   constexpr int PITCH = 32 * FJ + 4;  // floats; the outputs' way through LDS
-  static_assert(WI * WJ * 32 * PITCH * 4 <= S * STAGE, "the outputs' rows fit");
-  __shared__ __attribute__((aligned(1024))) char lds[S * STAGE];
+  static_assert(WI * WJ * 32 * PITCH * 4 <= 2 * STAGE, "the outputs' rows fit");
+  __shared__ __attribute__((aligned(1024))) char lds[2 * STAGE];
 
   // Blocks go to the 8 XCDs in turn: XCD x takes the tiles of eighth x, in
   // groups of 8 tile rows, so that blocks that share operands share an L2.
@@ -570,50 +574,33 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
         __builtin_amdgcn_sched_barrier(0);
       }
     };
-    // Every wave is done with the stage read last, and the loads of the next
-    // one have landed: all but this wave's last S - 2 steps', and, behind the
-    // barrier, every wave's.
-    const auto turn = [&](bool all) {
-      if (all)
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-      else
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"((S - 2) * (TA::N + TB::N)) : "memory");
+    // Every wave is done with the stage read last, and every wave's loads of
+    // the next one have landed.
+    const auto turn = [&] {
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
       __syncthreads();
     };
     constexpr int P = FI * FJ, Q = SB / 32, LOADS = TA::N + TB::N;
-    const auto load_one = [&](char* stage, int n) {
+    const auto load_one = [&](char* stage, int n, auto full) __attribute__((always_inline)) {
       if (n < TA::N)
-        la.load(stage, n);
+        la.template load<decltype(full)::value>(stage, n);
       else
-        lb.load(stage + TA::BYTES, n - TA::N);
+        lb.template load<decltype(full)::value>(stage + TA::BYTES, n - TA::N);
     };
-    const int first = steps < S - 1 ? steps : S - 1;
-    for (int t = 0; t < first; ++t) {
-      la.begin();
-      lb.begin();
-#pragma unroll
-      for (int n = 0; n < LOADS; ++n) load_one(lds + t * STAGE, n);
-      la.end();
-      lb.end();
-      la.commit(lds + t * STAGE);
-      lb.commit(lds + t * STAGE + TA::BYTES);
-    }
-    turn(first < S - 1);
-#pragma unroll
-    for (int m = 0; m < FI + FJ; ++m) read_one(lds, 0, 0, m);
-    for (int t = 0; t < steps; ++t) {
-      const char* stage = lds + t % S * STAGE;
-      const char* next = lds + (t + 1) % S * STAGE;
-      char* to = lds + (t + S - 1) % S * STAGE;
-      const bool more = t + S - 1 < steps;
-      const bool sum_now = sum_rows && t % g.tiles_j == tile_j;
+    int until_rows = tile_j;  // steps until the next one whose rows this block adds up
+    // One step: its products, with the next step's loads under way (MORE; FULL:
+    // all of whose terms exist).
+    const auto one_step = [&](const char* stage, char* next, auto more, auto full) __attribute__((always_inline)) {
+      constexpr bool MORE = decltype(more)::value;
+      const bool sum_now = DIR == DDP_LINEAR_BACKWARD_WEIGHT && until_rows == 0;
+      if (DIR == DDP_LINEAR_BACKWARD_WEIGHT) until_rows = sum_now ? g.tiles_j - 1 : until_rows - 1;
       const auto add_rows = [&](int from) {
-        if (DIR == DDP_LINEAR_BACKWARD_WEIGHT && sum_now) {
+        if (DIR == DDP_LINEAR_BACKWARD_WEIGHT && sum_now && sum_rows) {
 #pragma unroll
           for (int a = 0; a < FI; ++a) row_sum[a] += sum_of<DT>(fa[from][a]);
         }
       };
-      if (more) {
+      if (MORE) {
         la.begin();
         lb.begin();
       }
@@ -621,32 +608,54 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
       // 32 bytes, or one of the loads.
 #pragma unroll
       for (int s = 0; s < Q - 1; ++s) {
-        products(s & 1, [&](int m) {
+        products(s & 1, [&](int m) __attribute__((always_inline)) {
 #pragma unroll
           for (int r = 0; r < FI + FJ; ++r)
             if (r * P / (FI + FJ) == m) read_one(stage, s + 1, (s + 1) & 1, r);
-          if (more) {
+          if (MORE) {
 #pragma unroll
             for (int n = 0; n < LOADS; ++n)
-              if (n * P / LOADS == m && s == 0) load_one(to, n);
+              if (n * P / LOADS == m && s == 0) load_one(next, n, full);
           }
         });
         add_rows(s & 1);
       }
-      if (more) {
+      if (MORE) {
         la.end();
         lb.end();
-        la.commit(to);
-        lb.commit(to + TA::BYTES);
-      }
-      if (t + 1 < steps) {
-        turn(!more);
+        la.commit(next);
+        lb.commit(next + TA::BYTES);
+        turn();
 #pragma unroll
         for (int m = 0; m < FI + FJ; ++m) read_one(next, 0, 0, m);
       }
       products((Q - 1) & 1, [](int) {});
       add_rows((Q - 1) & 1);
+    };
+    constexpr std::integral_constant<bool, true> yes{};
+    constexpr std::integral_constant<bool, false> no{};
+    la.begin();
+    lb.begin();
+#pragma unroll
+    for (int n = 0; n < LOADS; ++n) load_one(lds, n, no);
+    la.end();
+    lb.end();
+    la.commit(lds);
+    lb.commit(lds + TA::BYTES);
+    turn();
+#pragma unroll
+    for (int m = 0; m < FI + FJ; ++m) read_one(lds, 0, 0, m);
+    // Two steps at a time while the next ones are whole: the stages are fixed
+    // then, and a wave's instructions between its products are few. (They
+    // issue one by one, some 5 cycles each, while its products wait.)
+    const int whole_steps = int((k1 - k0) / TA::STEP);
+    int t = 0;
+    for (; t + 2 < whole_steps; t += 2) {
+      one_step(lds, lds + STAGE, yes, yes);
+      one_step(lds + STAGE, lds, yes, yes);
     }
+    for (; t + 1 < steps; ++t) one_step(lds + (t & 1) * STAGE, lds + ((t & 1) ^ 1) * STAGE, yes, no);
+    one_step(lds + (t & 1) * STAGE, nullptr, no, no);
   }
 
   if (DIR == DDP_LINEAR_BACKWARD_WEIGHT && sum_rows) {
@@ -944,45 +953,71 @@ struct Cut {
   int64_t part_k = 0;
 };
 
-// The cut with the least time by a rough model, in cycles, of what was measured on
-// MI355X: a CU's time for one step of a tile when its blocks fill it (`step`),
-// a block's own time per step when it is alone (kAlone), a tile's start and
-// outputs (`ends`), and the join of parts, a launch and their bytes.
-Cut cut_of(int dir, int64_t I, int64_t J, int64_t K, int dtype, bool direct) {
+// The cut with the least time by a rough model in cycles. Its constants were
+// fitted to the times of 120 products of 5 to 8192 rows, 64 to 8192 columns
+// and terms, odd and even, on MI355X, each cut in up to 27 ways: the cut it
+// picks takes 1.8 % longer than the best of them in the mean, 14 % at worst.
+// A tile's step (128 bytes of k) takes `step` cycles of a CU that its blocks
+// fill and `alone` of a block by itself, its outputs `ends`; parts cost a
+// launch and their bytes.
+Cut cut_by_model(int dir, int32_t I, int32_t J, int32_t K, int dtype, bool direct) {
   Cut best;
   if (dir == DDP_LINEAR_FORWARD && I <= kFewRows) {
     best.few = true;
     return best;
   }
   struct Shape {
-    int tile, fit;        // blocks that fit a CU
-    int64_t step, ends;
+    int32_t tile, fit;  // `fit` blocks share a CU
+    float step, alone, ends;
   };
-  static const Shape bf16[3] = {{64, 5, 380, 1500}, {128, 2, 1100, 4500}, {256, 1, 3400, 24000}};
-  static const Shape fp32[2] = {{64, 5, 1150, 1500}, {128, 2, 4700, 4500}};
-  constexpr int64_t kCus = 256, kAlone = 1800, kStart = 6000, kJoin = 14000, kBytesPerCycle = 2500;
-  const Shape* shapes = dtype == DDP_BF16 ? bf16 : fp32;
-  const int64_t row = std::min(a_along(dir) ? K : I, b_along(dir) ? K : J);  // the operands' shorter rows
+  static const Shape shapes[2][2][3] = {
+      // fp32: loads at any alignment, direct loads
+      {{{64, 5, 1300, 1820, 1000}, {128, 2, 4420, 5460, 4800}, {}}, {{64, 5, 1150, 1400, 1500}, {128, 2, 4090, 4690, 3900}, {}}},
+      // bf16
+      {{{64, 5, 610, 1190, 1200}, {128, 2, 1790, 2900, 3800}, {}},
+       {{64, 5, 440, 890, 1300}, {128, 2, 1400, 1460, 3600}, {256, 1, 1630, 2700, 13800}}}};
+  constexpr float kStart = 2200, kJoin = 10800, kBytesPerCycle = 3000;
+  constexpr int32_t kCus = 256;
+  const auto up = [](int64_t a, int64_t b) { return int32_t((a + b - 1) / b); };
+  const int32_t row = std::min(a_along(dir) ? K : I, b_along(dir) ? K : J);  // the operands' shorter rows
   const int n_shapes = row < 16 / elem_bytes(dtype) ? 1 : dtype == DDP_BF16 && direct ? 3 : 2;
-  const int64_t step = 128 / elem_bytes(dtype), steps = std::max<int64_t>(1, div_up(K, step));
-  int64_t least = INT64_MAX;
+  const int32_t step = 128 / elem_bytes(dtype), steps = std::max(1, up(K, step));
+  float least = INFINITY;
   for (int k = 0; k < n_shapes; ++k) {
-    const Shape& sh = shapes[k];
-    const int64_t tiles = div_up(I, sh.tile) * div_up(J, sh.tile);
-    for (int want : {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 28, 32, 40, 48, 64}) {
+    const Shape& sh = shapes[dtype == DDP_BF16][direct][k];
+    const int64_t tiles = int64_t(up(I, sh.tile)) * up(J, sh.tile);
+    for (int32_t want : {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 28, 32}) {
       if (want > 1 && (want > steps / 2 || tiles * want > 4 * kCus * sh.fit)) break;
-      const int64_t per = div_up(steps, want), parts = div_up(steps, per);
-      const int64_t on_cu = div_up(tiles * parts, kCus);
-      int64_t t = std::max(div_up(on_cu, sh.fit) * (kStart + per * kAlone), kStart + on_cu * (per * sh.step + sh.ends));
-      if (parts > 1) t += kJoin + (parts + 2) * I * J * 4 / kBytesPerCycle;
+      const int32_t per = up(steps, want), parts = up(steps, per), on_cu = up(tiles * parts, kCus);
+      float t = std::max(float(up(on_cu, sh.fit)) * (kStart + float(per) * sh.alone),
+                         kStart + float(on_cu) * (float(per) * sh.step + sh.ends));
+      if (parts > 1) t += kJoin + float(parts + 2) * float(I) * float(J) * (4 / kBytesPerCycle);
       if (t >= least) continue;
       least = t;
       best.tile = sh.tile;
-      best.parts = int32_t(parts);
-      best.part_k = per * step;
+      best.parts = parts;
+      best.part_k = int64_t(per) * step;
     }
   }
   return best;
+}
+
+// The same, remembered per thread for the sizes seen last: the model takes a
+// microsecond or two, and a call asks it three times.
+Cut cut_of(int dir, int64_t I, int64_t J, int64_t K, int dtype, bool direct) {
+  struct Seen {
+    int64_t key[4] = {-1, -1, -1, -1};
+    Cut cut;
+  };
+  static thread_local Seen seen[64];
+  const int64_t key[4] = {I, J, K, dir * 4 + dtype * 2 + int(direct)};
+  const uint64_t h = (uint64_t(I) * 31 + uint64_t(J) * 7 + uint64_t(K)) * 8 + uint64_t(key[3]);
+  Seen& s = seen[(h ^ (h >> 7)) % 64];
+  if (!std::equal(key, key + 4, s.key)) {
+    s.cut = cut_by_model(dir, int32_t(I), int32_t(J), int32_t(K), dtype, direct);
+    std::copy(key, key + 4, s.key);
+  }
+  return s.cut;
 }
 
 int64_t partial_bytes(const Cut& c, int64_t I, int64_t J) {
