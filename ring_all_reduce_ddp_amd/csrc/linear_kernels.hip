@@ -359,11 +359,12 @@ struct DirectLoader {
       const int64_t r = ALONG && s0 + row >= side ? side - 1 - s0 : row;
       off[n] = uint32_t(r * ld * TL::ES + TL::col_of(q) * 16);
     }
+    describe();
   }
-  // The current step's loads into `lds`: begin() and load(n) for every n,
-  // then end(). Loads that the sum does not need read as zeros (FULL: it needs
+  // The current step's loads into `lds`: load(n) for every n, then end().
+  // Loads that the sum does not need read as zeros (FULL: it needs
   // all of them).
-  __device__ __forceinline__ void begin() {
+  __device__ __forceinline__ void describe() {
     const uint64_t a = reinterpret_cast<uint64_t>(p);
     const int32_t range = left < 0 ? 0 : left < kMostRange ? left : kMostRange;
     desc = u32x4{uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(a))),
@@ -385,6 +386,7 @@ struct DirectLoader {
     p += advance;
     left -= int32_t(advance / 16);
     k_left -= TL::STEP;
+    describe();
   }
   __device__ __forceinline__ void commit(char*) {}
 };
@@ -423,7 +425,6 @@ struct AnyLoader {
       shift[n] = back;
     }
   }
-  __device__ __forceinline__ void begin() { shifted = k_left < TL::STEP || (!ALONG && width < kWidth); }
   template <bool FULL>
   __device__ __forceinline__ void load(const char*, int n) {
     int64_t o = off[n];
@@ -443,6 +444,7 @@ struct AnyLoader {
       x[n] = load_at<false, u32x4_at2>(p + o, 0);
   }
   __device__ __forceinline__ void end() {
+    shifted = k_left < TL::STEP || (!ALONG && width < kWidth);
     p += ALONG ? TL::ROW : TL::STEP * row_bytes;
     k_left -= TL::STEP;
   }
@@ -470,7 +472,6 @@ struct ShortLoader {
   __device__ __forceinline__ void init(const void* b, int64_t ld_, int64_t side_, int64_t, int64_t s0_, int64_t k0, int64_t k1_) {
     base = b, ld = ld_, side = side_, s0 = s0_, k = k0, k1 = k1_;
   }
-  __device__ __forceinline__ void begin() {}
   template <bool FULL>
   __device__ __forceinline__ void load(const char*, int n) {
     const int q = n * THREADS + int(threadIdx.x);
@@ -600,10 +601,6 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
           for (int a = 0; a < FI; ++a) row_sum[a] += sum_of<DT>(fa[from][a]);
         }
       };
-      if (MORE) {
-        la.begin();
-        lb.begin();
-      }
       // All but the last 32 bytes of k: after each product a read of the next
       // 32 bytes, or one of the loads.
 #pragma unroll
@@ -616,26 +613,30 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
 #pragma unroll
             for (int n = 0; n < LOADS; ++n)
               if (n * P / LOADS == m && s == 0) load_one(next, n, full);
+            if (s == 1 && m == P / 2) {
+              la.end();
+              lb.end();
+            }
           }
         });
         add_rows(s & 1);
       }
       if (MORE) {
-        la.end();
-        lb.end();
         la.commit(next);
         lb.commit(next + TA::BYTES);
         turn();
-#pragma unroll
-        for (int m = 0; m < FI + FJ; ++m) read_one(next, 0, 0, m);
       }
-      products((Q - 1) & 1, [](int) {});
+      products((Q - 1) & 1, [&](int m) __attribute__((always_inline)) {
+        if (MORE) {
+#pragma unroll
+          for (int r = 0; r < FI + FJ; ++r)
+            if (r * P / (FI + FJ) == m) read_one(next, 0, 0, r);
+        }
+      });
       add_rows((Q - 1) & 1);
     };
     constexpr std::integral_constant<bool, true> yes{};
     constexpr std::integral_constant<bool, false> no{};
-    la.begin();
-    lb.begin();
 #pragma unroll
     for (int n = 0; n < LOADS; ++n) load_one(lds, n, no);
     la.end();
