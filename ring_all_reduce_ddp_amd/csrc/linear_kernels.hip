@@ -955,12 +955,12 @@ struct Cut {
 };
 
 // The cut with the least time by a rough model in cycles. Its constants were
-// fitted to the times of 120 products of 5 to 8192 rows, 64 to 8192 columns
+// fitted to the times of 250 products of 5 to 8192 rows, 64 to 8192 columns
 // and terms, odd and even, on MI355X, each cut in up to 27 ways: the cut it
-// picks takes 1.8 % longer than the best of them in the mean, 14 % at worst.
+// picks takes 1.9 % longer than the best of them in the mean, 31 % at worst.
 // A tile's step (128 bytes of k) takes `step` cycles of a CU that its blocks
 // fill and `alone` of a block by itself, its outputs `ends`; parts cost a
-// launch and their bytes.
+// launch, a round each, and their bytes.
 Cut cut_by_model(int dir, int32_t I, int32_t J, int32_t K, int dtype, bool direct) {
   Cut best;
   if (dir == DDP_LINEAR_FORWARD && I <= kFewRows) {
@@ -973,11 +973,11 @@ Cut cut_by_model(int dir, int32_t I, int32_t J, int32_t K, int dtype, bool direc
   };
   static const Shape shapes[2][2][3] = {
       // fp32: loads at any alignment, direct loads
-      {{{64, 5, 1300, 1820, 1000}, {128, 2, 4420, 5460, 4800}, {}}, {{64, 5, 1150, 1400, 1500}, {128, 2, 4090, 4690, 3900}, {}}},
+      {{{64, 5, 1160, 1880, 1500}, {128, 2, 3840, 4670, 5400}, {}}, {{64, 5, 1050, 1140, 1230}, {128, 2, 3920, 3700, 2970}, {}}},
       // bf16
-      {{{64, 5, 610, 1190, 1200}, {128, 2, 1790, 2900, 3800}, {}},
-       {{64, 5, 440, 890, 1300}, {128, 2, 1400, 1460, 3600}, {256, 1, 1630, 2700, 13800}}}};
-  constexpr float kStart = 2200, kJoin = 10800, kBytesPerCycle = 3000;
+      {{{64, 5, 620, 1150, 1050}, {128, 2, 1850, 2040, 3350}, {}},
+       {{64, 5, 440, 850, 2190}, {128, 2, 920, 1010, 4340}, {256, 1, 2100, 2290, 10160}}}};
+  constexpr float kStart = 2000, kJoin = 13100, kPart = 320, kBytesPerCycle = 3160;
   constexpr int32_t kCus = 256;
   const auto up = [](int64_t a, int64_t b) { return int32_t((a + b - 1) / b); };
   const int32_t row = std::min(a_along(dir) ? K : I, b_along(dir) ? K : J);  // the operands' shorter rows
@@ -992,7 +992,7 @@ Cut cut_by_model(int dir, int32_t I, int32_t J, int32_t K, int dtype, bool direc
       const int32_t per = up(steps, want), parts = up(steps, per), on_cu = up(tiles * parts, kCus);
       float t = std::max(float(up(on_cu, sh.fit)) * (kStart + float(per) * sh.alone),
                          kStart + float(on_cu) * (float(per) * sh.step + sh.ends));
-      if (parts > 1) t += kJoin + float(parts + 2) * float(I) * float(J) * (4 / kBytesPerCycle);
+      if (parts > 1) t += kJoin + float(parts) * kPart + float(parts + 2) * float(I) * float(J) * (4 / kBytesPerCycle);
       if (t >= least) continue;
       least = t;
       best.tile = sh.tile;
