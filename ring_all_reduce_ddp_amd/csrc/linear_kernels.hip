@@ -10,12 +10,22 @@
 // in the forward product), or with k going from row to row ("across": w in
 // the input gradient, both operands of the weight gradient).
 //
-// A block computes a tile of C in steps of 64 or 128 bytes of k. Both operands'
-// parts of a step lie in LDS as they lie in memory, in 16-byte chunks, the
-// next steps' on their way while this one's are multiplied. A lane of a 32 x 32 matrix instruction needs one row's k values
-// 8h .. 8h+7 (h: its half of the wave): 16 bytes of an "along" row, or, of an
-// "across" operand, eight rows' values of one column, which the transposing
-// LDS read gathers (bf16), or four single reads (fp32).
+// A block computes a tile of C in steps of 128 bytes of k. Both operands' parts
+// of a step lie in LDS as they lie in memory, in 16-byte chunks, the next
+// step's on their way while this one's are multiplied. A lane of a 32 x 32
+// matrix instruction needs one row's k values 8h .. 8h+7 (h: its half of the
+// wave): 16 bytes of an "along" row, or, of an "across" operand, eight rows'
+// values of one column, which the transposing LDS read gathers (bf16), or four
+// single reads (fp32).
+//
+// What bounds it: a 256 x 256 tile's step of bf16 is 2048 cycles of the matrix
+// instructions and, at 128 bytes a cycle, 2031 of LDS (196 KB read by 8 waves,
+// 64 KB written), so the two have to overlap throughout, and a wave's other
+// instructions have to fit between its products. Measured, 8192 x 2048 x 8192
+// on random data: forward 204 us (1350 TFLOP/s), weight gradient 210, input
+// gradient to 8192 x 2048 203; a 256 x 256 tile's outputs take 7 to 15 us more,
+// in which its CU multiplies nothing. Power takes part of it: on zeros the same
+// products run a fifth faster. fp32: 150 TFLOP/s, the instructions' rate.
 #include <algorithm>
 #include <cmath>
 #include <new>
@@ -522,14 +532,17 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
   __shared__ __attribute__((aligned(1024))) char lds[2 * STAGE];
 
   // Blocks go to the 8 XCDs in turn: XCD x takes the tiles of eighth x, in
-  // groups of 8 tile rows, so that blocks that share operands share an L2.
+  // groups of 4 tile rows, so that blocks that share operands share an L2
+  // (8192 x 8192 x 2048 forward with z kept: 254 us; groups of 8, 258, of 1,
+  // 283; tiles in the blocks' order, 299).
   const int tiles = g.tiles_i * g.tiles_j;
   const int at = int(blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8);
   if (at >= tiles * g.parts) return;
   const int part = at / tiles, tile = at % tiles;
-  const int group = tile / (8 * g.tiles_j), in_group = tile % (8 * g.tiles_j);
-  const int rows = g.tiles_i - 8 * group < 8 ? g.tiles_i - 8 * group : 8;
-  const int64_t i0 = int64_t(8 * group + in_group % rows) * TI, j0 = int64_t(in_group / rows) * TJ;
+  constexpr int GROUP = 4;
+  const int group = tile / (GROUP * g.tiles_j), in_group = tile % (GROUP * g.tiles_j);
+  const int rows = g.tiles_i - GROUP * group < GROUP ? g.tiles_i - GROUP * group : GROUP;
+  const int64_t i0 = int64_t(GROUP * group + in_group % rows) * TI, j0 = int64_t(in_group / rows) * TJ;
   const int64_t k0 = part * g.part_k, k1 = k0 + g.part_k < g.K ? k0 + g.part_k : g.K;
   const int steps = int((k1 - k0 + TA::STEP - 1) / TA::STEP);
 
@@ -563,8 +576,8 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
     };
     // The products of the fragments in `from`, with step(m) after the m-th. The
     // order written is the schedule: left to itself, the compiler moves the
-    // LDS reads down to the products that use them, and a wave then waits for
-    // each quarter's.
+    // LDS reads down to the products that use them (8192 x 2048 x 8192 forward:
+    // 212 us against 205).
     const auto products = [&](int from, auto&& step) {
 #pragma unroll
       for (int m = 0; m < FI * FJ; ++m) {
@@ -804,7 +817,9 @@ __global__ __launch_bounds__(kThreads) void k_column_sums(const void* src, int64
 // The forward product for up to kFewRows rows of x (tokens of an answer): w
 // is read once and each value meets every row's, so the bound is w's bytes. A
 // block takes 4 rows of w, its waves every fourth kilobyte of each; x stays in
-// the caches. (1 row, 8192 x 2048 bf16: NNN us, against 15 in 128 x 128 tiles.)
+// the caches. (1 row, 8192 x 2048 bf16: 6 us, 5.6 TB/s with w in the Infinity
+// Cache, against 15 in 128 x 128 tiles; 8 rows took 40 this way and 19 in
+// tiles.)
 constexpr int kFewRows = 4, kFewOuts = 4;
 
 // V = 16 / element size values of a row from k on, zeros past K.
