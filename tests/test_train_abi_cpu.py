@@ -68,3 +68,95 @@ def test_adamw_arguments():
     assert out.value is None
     refused(lib.ddp_adamw_step(None, 1e-3, 0.9, 0.99, 1e-8, 0.0, 0.0, None, None), "opt is NULL")
     lib.ddp_adamw_free(None)
+
+
+A = 0x100000      # addresses that are never read: the refusals come first
+FAR = 1 << 30
+
+
+
+def forward_args(**change):
+    """ddp_linear_forward on 4 x 8 outputs of 16 inputs, fp32, with everything asked for."""
+    a = dict(x=A, ldx=16, w=A + FAR, ldw=16, bias=A + 2 * FAR, residual=A + 3 * FAR, ldr=8, y=A + 4 * FAR, ldy=8,
+             z=A + 5 * FAR, ldz=8, M=4, N=8, K=16, dtype=0, act=1, workspace=A + 6 * FAR, workspace_bytes=FAR, stream=None)
+    assert set(change) <= set(a)
+    a.update(change)
+    return list(a.values())
+
+
+@pytest.mark.parametrize("change, match", [
+    (dict(dtype=9), "unknown dtype"), (dict(act=-1), "unknown activation"), (dict(act=99), "unknown activation"),
+    (dict(M=-1), "M, N and K"), (dict(N=-1), "M, N and K"), (dict(K=1 << 31), "M, N and K"),
+    (dict(x=None), "x"), (dict(w=None), "w"), (dict(y=None), "y"),
+    (dict(x=A + 2), "x is not aligned"), (dict(bias=A + 2 * FAR + 1), "bias is not aligned"),
+    (dict(ldx=15), "leading dimension of x"), (dict(ldw=15), "leading dimension of w"), (dict(ldy=7), "leading dimension of y"),
+    (dict(ldz=7), "leading dimension of z"), (dict(ldr=7), "leading dimension of residual"),
+    (dict(ldw=(1 << 30) + 1), "over 2^22"), (dict(ldx=1 << 62), "over 2^22"),
+    (dict(y=A + 16), "y overlaps x"), (dict(z=A + 4 * FAR), "overlaps"), (dict(residual=A + 4 * FAR + 4), "overlaps"),
+    (dict(residual=A + 4 * FAR, ldr=9), "overlaps"), (dict(y=A + FAR + 508), "y overlaps w"),
+])
+def test_linear_forward_arguments(change, match):
+    refused(rar.lib.ddp_linear_forward(*forward_args(**change)), match)
+
+
+def test_linear_forward_of_nothing():
+    assert rar.lib.ddp_linear_forward(*forward_args(M=0, x=None, y=None)) == rar.DDP_OK
+    assert rar.lib.ddp_linear_forward(*forward_args(N=0, w=None, y=None)) == rar.DDP_OK
+
+
+def backward_input_args(**change):
+    a = dict(dz=A, lddz=8, w=A + FAR, ldw=16, z=A + 2 * FAR, ldz=16, add=A + 3 * FAR, ldadd=16, dx=A + 4 * FAR, lddx=16,
+             M=4, N=8, K=16, dtype=0, act=1, workspace=A + 6 * FAR, workspace_bytes=FAR, stream=None)
+    assert set(change) <= set(a)
+    a.update(change)
+    return list(a.values())
+
+
+@pytest.mark.parametrize("change, match", [
+    (dict(dtype=-1), "unknown dtype"), (dict(act=99), "unknown activation"), (dict(M=-1), "M, N and K"),
+    (dict(z=None), "needs z"), (dict(dz=None), "dz"), (dict(w=None), "w"), (dict(dx=None), "dx"),
+    (dict(lddz=7), "leading dimension of dz"), (dict(lddx=15), "leading dimension of dx"), (dict(ldadd=15), "leading dimension of add"),
+    (dict(dx=A), "dx overlaps dz"), (dict(dx=A + 2 * FAR), "dx overlaps z"), (dict(dx=A + 3 * FAR + 4), "dx overlaps add"),
+])
+def test_linear_backward_input_arguments(change, match):
+    refused(rar.lib.ddp_linear_backward_input(*backward_input_args(**change)), match)
+
+
+def backward_weight_args(**change):
+    a = dict(dz=A, lddz=8, x=A + FAR, ldx=16, dw=A + 2 * FAR, lddw=16, db=A + 3 * FAR, M=4, N=8, K=16, dtype=0,
+             grad_dtype=0, accumulate=0, workspace=A + 6 * FAR, workspace_bytes=FAR, stream=None)
+    assert set(change) <= set(a)
+    a.update(change)
+    return list(a.values())
+
+
+@pytest.mark.parametrize("change, match", [
+    (dict(dtype=5), "unknown dtype"), (dict(grad_dtype=1), "grad_dtype"), (dict(accumulate=2), "accumulate"),
+    (dict(K=-1), "M, N and K"), (dict(dz=None), "dz"), (dict(x=None), "x"), (dict(dw=None), "dw"),
+    (dict(dw=A + FAR), "dw overlaps x"), (dict(db=A + 2 * FAR + 8), "overlaps"), (dict(lddw=15), "leading dimension of dw"),
+    (dict(workspace=None), "workspace needs"), (dict(workspace_bytes=3), "workspace needs"),
+    (dict(workspace=A + 6 * FAR + 8), "16-byte aligned"), (dict(workspace=A + 2 * FAR), "overlaps"),
+])
+def test_linear_backward_weight_arguments(change, match):
+    refused(rar.lib.ddp_linear_backward_weight(*backward_weight_args(**change)), match)
+
+
+@pytest.mark.parametrize("change, match", [
+    (dict(dtype=2), "unknown dtype"), (dict(act=99), "unknown activation"), (dict(N=-1), "M, N and K"),
+    (dict(dy=None), "dy"), (dict(z=None), "z"), (dict(dz=None), "dz"), (dict(lddy=7), "leading dimension of dy"),
+    (dict(dz=A + 4), "dz overlaps dy"), (dict(dz=A + FAR), "dz overlaps z"),
+])
+def test_act_backward_arguments(change, match):
+    a = dict(dy=A, lddy=8, z=A + FAR, ldz=8, dz=A + 2 * FAR, lddz=8, M=4, N=8, dtype=0, act=1, stream=None)
+    assert set(change) <= set(a)
+    a.update(change)
+    refused(rar.lib.ddp_act_backward(*a.values()), match)
+
+
+def test_linear_workspace_arguments():
+    lib, out = rar.lib, ctypes.c_int64(7)
+    refused(lib.ddp_linear_workspace(0, 1, 1, 1, 0, None), "bytes is NULL")
+    refused(lib.ddp_linear_workspace(3, 1, 1, 1, 0, ctypes.byref(out)), "direction")
+    refused(lib.ddp_linear_workspace(0, -1, 1, 1, 0, ctypes.byref(out)), "M, N and K")
+    refused(lib.ddp_linear_workspace(0, 1, 1, 1, 4, ctypes.byref(out)), "dtype")
+    assert out.value == 0
