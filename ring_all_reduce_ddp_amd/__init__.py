@@ -573,6 +573,8 @@ class GradSet:
         or into another GradSet; `norm` is a float32 device tensor."""
         if norm.dtype != torch.float32 or norm.numel() != 1:
             raise ValueError("norm must hold one float32")
+        if into is not None and not into._h:   # NULL would mean in place
+            raise ValueError("into is freed")
         _check(_get_lib().ddp_grads_clip(self._h, None if into is None else into._h, float(max_norm),
                                          norm.data_ptr(), _stream(stream)))
 

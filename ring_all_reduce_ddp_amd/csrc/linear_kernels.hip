@@ -542,7 +542,8 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
   // Steps of 128 bytes of k, one on its way while one is multiplied. (Four
   // stages of 64 bytes, three of them on their way, ran 15 % slower: twice the
   // barriers. 4 waves with 128 x 128 products each read a third less from LDS
-  // but have nobody to fill their waits: 9 % slower.)
+  // but have nobody to fill their waits: as fast without outputs to speak of,
+  // 8192 x 8192 x 2048 input gradient through gelu_tanh 303 us against 269.)
   constexpr int SB = 128;
   using TA = Tile<DT, a_along(DIR), TI, SB, THREADS>;
   using TB = Tile<DT, b_along(DIR), TJ, SB, THREADS>;

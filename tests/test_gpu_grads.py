@@ -247,3 +247,15 @@ def test_refusals():
         s.norm(out=torch.empty((), dtype=torch.float64, device="cuda"))
     with pytest.raises(KeyError):
         s.norm("l1")
+
+
+def test_a_freed_set_is_refused():
+    a, b = (torch.full((10,), 4.0, device="cuda") for _ in range(2))
+    s, into = rar.GradSet([a]), rar.GradSet([b])
+    norm = s.norm()
+    into.free()
+    with pytest.raises(ValueError, match="into is freed"):   # not in place
+        s.clip(1.0, norm, into=into)
+    with pytest.raises(rar.DDPError, match="grads is NULL"):
+        into.norm()
+    assert (a == 4.0).all() and (b == 4.0).all()
