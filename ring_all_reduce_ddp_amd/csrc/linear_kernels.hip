@@ -56,6 +56,7 @@ struct LinearArgs {
   int32_t act;
   int32_t grad32;      // weight gradient: dw is fp32
   int32_t accumulate;  // weight gradient: add to dw
+  int32_t stream_z;    // forward: z's stores pass the caches
   int32_t parts;       // blocks that share a tile's sum
   int64_t part_k;      // terms of one part (whole steps)
   float* partial;      // parts > 1: [part][I][round_up(J, 8)]
@@ -177,17 +178,27 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, int n, float v[
   unpack8<DT>(load_raw8<DT>(p, at, n), v);
 }
 
+template <int DT, bool NT>
+__device__ __forceinline__ void store_all8(void* p, int64_t at, const float v[8]) {
+  if constexpr (DT == DDP_FP32) {
+    float* q = static_cast<float*>(p) + at;
+    store4<DDP_FP32, NT>(q, 0, v);
+    store4<DDP_FP32, NT>(q, 1, v + 4);
+  } else {
+    store_at<NT, u32x4_at2>(static_cast<uint16_t*>(p) + at, 0,
+                            u32x4{round_bf16x2(v[0], v[1]), round_bf16x2(v[2], v[3]), round_bf16x2(v[4], v[5]),
+                                  round_bf16x2(v[6], v[7])});
+  }
+}
 template <int DT>
-__device__ __forceinline__ void store8(void* p, int64_t at, int n, const float v[8]) {
+__device__ __forceinline__ void store8(void* p, int64_t at, int n, const float v[8], bool streamed = false) {
   if (n == 8) {
-    if constexpr (DT == DDP_FP32) {
-      float* q = static_cast<float*>(p) + at;
-      store4<DDP_FP32, false>(q, 0, v);
-      store4<DDP_FP32, false>(q, 1, v + 4);
+    if (streamed) {  // between marks, or the compiler makes the two stores one, and that not a streamed one
+      asm volatile("; streamed");
+      store_all8<DT, true>(p, at, v);
+      asm volatile("; to here");
     } else {
-      store_at<false, u32x4_at2>(static_cast<uint16_t*>(p) + at, 0,
-                                 u32x4{round_bf16x2(v[0], v[1]), round_bf16x2(v[2], v[3]), round_bf16x2(v[4], v[5]),
-                                       round_bf16x2(v[6], v[7])});
+      store_all8<DT, false>(p, at, v);
     }
   } else {
     for (int k = 0; k < 8; ++k)
@@ -228,7 +239,7 @@ __device__ __forceinline__ void before_store(const LinearArgs& g, int64_t i, int
   } else {
     if constexpr (DIR == DDP_LINEAR_FORWARD) {
       for (int k = 0; k < 8; ++k) v[k] += bias[k];  // zeros without a bias
-      if (g.z != nullptr) store8<DT>(g.z, i * g.ldz + j, n, v);
+      if (g.z != nullptr) store8<DT>(g.z, i * g.ldz + j, n, v, g.stream_z != 0);
       for (int k = 0; k < 8; ++k) v[k] = act_value<ACT>(v[k]);
     } else if constexpr (ACT != DDP_ACT_NONE) {
       float z[8];
@@ -1139,6 +1150,15 @@ int launch_product(LinearArgs& g, void* workspace, bool want_rows, hipStream_t s
       return DDP_OK;
     }
   }
+  // z waits for the backward pass, the rest of what the call touches does not:
+  // where all of it is much for the Infinity Cache, z leaves it to y (a layer
+  // and the one after it, rows x inputs x outputs and back, with z cached and
+  // streamed: 8192 x 2048 x 8192 512 and 467 us, 8192 x 1536 x 6144, 244 MB, 327
+  // and 293, 4096 x 2048 x 8192, 184 MB, 275 and 257; 8192 x 1024 x 4096, 159
+  // MB, 143 and 144, with their backward pass 480 and 484; 4096 x 1024 x 4096
+  // 88.3 and 88.7). C streamed too is read back too slowly: 487, 325, 267.
+  if (DIR == DDP_LINEAR_FORWARD && g.z != nullptr)
+    g.stream_z = (g.I * g.K + g.J * g.K + g.I * g.J * (g.e != nullptr ? 3 : 2)) * elem_bytes(DT) > kInfinityCacheBytes / 3 * 2;
   g.parts = c.parts;
   g.part_k = c.part_k;
   g.partial = static_cast<float*>(workspace);
