@@ -433,3 +433,10 @@ def test_refusals():
     assert lib.ddp_linear_forward(*args(1 << 30)) == rar.DDP_EINVAL and b"past the end" in lib.ddp_last_error()
     assert lib.ddp_linear_forward(*args(16, m=-1)) == rar.DDP_EINVAL and b"M, N and K" in lib.ddp_last_error()
     assert f is torch.float32
+
+
+@pytest.mark.parametrize("size, dtype, layout", [((8201, 5600, 72), "bf16", (0, 0)), ((8201, 5603, 41), "bf16", (3, 1)),
+                                                 ((5001, 4600, 40), "fp32", (0, 0))], ids=str)
+def test_kept_z_beyond_the_cache(size, dtype, layout):
+    """y and z of over two thirds of the Infinity Cache: z's stores pass it."""
+    forward_case(*size, dtype, "gelu", True, False, True, *layout)
