@@ -422,8 +422,10 @@ struct DirectLoader {
     if (!FULL && k_left < TL::STEP) o = k_of(n) < k_left ? o : kFar;
     // No output register: the load ends in LDS, and every use of it stands
     // behind a wait for it and a barrier. (With the builtin, the
-    // compiler waits for all direct loads before any read of LDS.)
-    asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(o), "s"(desc), "s"(m) : "m0");
+    // compiler waits for all direct loads before any read of LDS.) A direct
+    // load needs one wait state after a write of M0, which nobody adds inside
+    // assembly.
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(o), "s"(desc), "s"(m) : "m0");
   }
   __device__ __forceinline__ void end() {
     p += advance;
