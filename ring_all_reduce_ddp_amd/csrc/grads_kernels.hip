@@ -148,13 +148,14 @@ constexpr int kClipParts = 4;
 // kClipParts blocks share a tile, 2048 elements each (300M bf16 into fp32: 302
 // us with 4, 354 with 1, 362 with 8). Blocks go to the 8 XCDs in turn, so block b
 // takes part b / 8 of eighth b % 8: each XCD walks memory of its own (302
-// against 309 us; 1.8 GB, 6.0 TB/s).
+// against 309 us; 1.8 GB, 6.0 TB/s). A launch's parts begin with `begin`.
 template <int SRC, int DST, bool NTL, bool NTS>
 __global__ __launch_bounds__(kThreads) void k_grads_clip(const GradTile* src, const GradTile* dst,
-                                                         unsigned int n_parts, float max_norm, const float* norm) {
+                                                         unsigned int begin, unsigned int n_parts, float max_norm,
+                                                         const float* norm) {
   constexpr int kPart = kGradTile / kClipParts;
   constexpr int U = kPart / (kThreads * 4);
-  const unsigned int at = blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;  // the grid is a multiple of 8
+  const unsigned int at = begin + blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;  // the grid is a multiple of 8
   if (at >= n_parts) return;
   const GradTile a = table_entry(src, at / kClipParts);
   void* const to = table_entry(dst, at / kClipParts).p;
@@ -203,10 +204,12 @@ void launch_norm(const ddp_grads* g, float* norm, hipStream_t s) {
 
 template <int SRC, int DST>
 void launch_clip(const ddp_grads* g, const ddp_grads* into, float max_norm, const float* norm, hipStream_t s) {
-  const unsigned int parts = unsigned(g->n_tiles * kClipParts);
-  const dim3 grid((parts + 7) / 8 * 8), block(kThreads);
+  const int64_t parts = g->n_tiles * kClipParts;
   const auto launch = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, block, 0, s, g->tiles, into->tiles, parts, max_norm, norm);
+    for (int64_t p = 0; p < parts; p += kMaxGrid) {
+      const dim3 grid(unsigned(round_up(std::min(parts - p, kMaxGrid), 8))), block(kThreads);
+      hipLaunchKernelGGL(kernel, grid, block, 0, s, g->tiles, into->tiles, unsigned(p), unsigned(parts), max_norm, norm);
+    }
   };
   // Stores stream past the caches into another set, which leaves the cache to the
   // gradients that the norm has just read (25.6M fp32, 102 MB: both 51 us
@@ -303,7 +306,7 @@ extern "C" int ddp_grads_create(void* const* grads, const int64_t* numels, int32
         tiles.push_back({static_cast<char*>(grads[i]) + e * eb, int32_t(std::min<int64_t>(kGradTile, numels[i] - e)), i});
     }
     if (tiles.size() >= (size_t(1) << 31) / kClipParts)
-      return fail(DDP_EINVAL, std::string(fn) + ": too many elements for one launch");
+      return fail(DDP_EINVAL, std::string(fn) + ": too many elements");
     g = new ddp_grads;
     g->dtype = dtype;
     if (n > 0) {

@@ -16,6 +16,9 @@ namespace ddp {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;  // threads per block of every streaming kernel (4 waves of 64)
+// Blocks per launch, at most: a dispatch holds fewer than 2^32 threads, and
+// blocks have up to 512. What needs more takes several launches.
+constexpr int64_t kMaxGrid = int64_t(1) << 22;
 
 // The N rank base pointers, passed by value in the kernel arguments (512 bytes).
 struct RankPtrs {

@@ -8,8 +8,6 @@
 
 namespace ddp {
 
-constexpr int64_t kMaxGrid = int64_t(1) << 22;
-
 __device__ __forceinline__ int wrap(int x, int n) {  // x in [0, 2n)
   return x >= n ? x - n : x;
 }
