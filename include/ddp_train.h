@@ -88,7 +88,7 @@ int ddp_adamw_create(const ddp_grads* grads, void* const* params, void* const* e
 /* Releases an optimizer (NULL is accepted); no work that uses it may be left. */
 void ddp_adamw_free(ddp_adamw* opt);
 
-/* ddp_adamw_step: one AdamW step in one launch. With t = *step_dev + 1 and
+/* ddp_adamw_step: one AdamW step, in one launch up to 2.1e9 elements. With t = *step_dev + 1 and
  * f = 1 if norm_dev is NULL, else min(1, max_norm / (*norm_dev + 1e-6)):
  *   g = f * grad
  *   m = beta1 m + (1 - beta1) g

@@ -44,6 +44,8 @@ struct AdamArgs {
   const float* norm;   // NULL: no clipping
   long long* step;
   unsigned int* tickets;
+  int32_t begin;       // the launch's first tile
+  int32_t last;        // whether the step's last launch: it moves the count on
 };
 
 // 1 - b^t = -expm1(t ln b). The product is made in fp64 and rounded once, and
@@ -79,7 +81,7 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const AdamTile* tiles, int64
   constexpr int U = kAdamTile / 256;   // vectors of four per lane
   __shared__ float st[4][kAdamTile];
   AdamTile tile{};
-  const unsigned int at = blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;  // the grid is a multiple of 8
+  const unsigned int at = unsigned(a.begin) + blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;  // the grid is a multiple of 8
   if (at < n_tiles) tile = table_entry(tiles, at);  // else an empty one
   const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / 64), lane = int(threadIdx.x) % 64;
   float x[U][4];
@@ -134,19 +136,26 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const AdamTile* tiles, int64
       if (tile.c != nullptr) Ops<DDP_BF16>::store1(tile.c, e, round_bf16(y.p));
     }
   }
-  // The step count moves on when every block has read it: the last block to
-  // finish writes it.
+  // The step count moves on when every block has read it: the last block of
+  // the last launch to finish writes it.
+  if (!a.last) return;
   __syncthreads();
   if (threadIdx.x == 0 && is_last_block(a.tickets)) *a.step = t;
 }
 
 template <int DT>
-void launch_adamw(const AdamTile* tiles, int64_t n_tiles, int64_t bytes, const AdamArgs& a, hipStream_t s) {
-  const dim3 grid(unsigned(std::max<int64_t>(8, (n_tiles + 7) / 8 * 8))), block(kThreads);
-  if (bytes > kInfinityCacheBytes)
-    hipLaunchKernelGGL((k_adamw<DT, true>), grid, block, 0, s, tiles, n_tiles, a);
-  else
-    hipLaunchKernelGGL((k_adamw<DT, false>), grid, block, 0, s, tiles, n_tiles, a);
+void launch_adamw(const AdamTile* tiles, int64_t n_tiles, int64_t bytes, AdamArgs a, hipStream_t s) {
+  int64_t t = 0;
+  do {  // no tiles: one launch, which counts the step
+    a.begin = int32_t(t);
+    a.last = t + kMaxGrid >= n_tiles;
+    const dim3 grid(unsigned(std::max<int64_t>(8, round_up(std::min(n_tiles - t, kMaxGrid), 8)))), block(kThreads);
+    if (bytes > kInfinityCacheBytes)
+      hipLaunchKernelGGL((k_adamw<DT, true>), grid, block, 0, s, tiles, n_tiles, a);
+    else
+      hipLaunchKernelGGL((k_adamw<DT, false>), grid, block, 0, s, tiles, n_tiles, a);
+    t += kMaxGrid;
+  } while (t < n_tiles);
 }
 
 }  // namespace
@@ -212,7 +221,7 @@ extern "C" int ddp_adamw_create(const ddp_grads* grads, void* const* params, voi
     }
     st = check_disjoint(spans, fn);
     if (st != DDP_OK) return st;
-    if (tiles.size() >= (size_t(1) << 31)) return fail(DDP_EINVAL, std::string(fn) + ": too many elements for one launch");
+    if (tiles.size() >= (size_t(1) << 31)) return fail(DDP_EINVAL, std::string(fn) + ": too many elements");
     o = new ddp_adamw;
     o->dtype = grads->dtype;
     o->dev = grads->dev;

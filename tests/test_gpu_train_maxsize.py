@@ -31,3 +31,23 @@ def test_clip_of_more_parts_than_a_launch_has_blocks():
     print(f"[clip] {n} elements", flush=True)
     rar.GradSet([t]).clip(1.0, torch.full((), 4.0, device="cuda"))
     assert all_equal(t, 0.25)   # 1 / 4.000001 rounds to it
+
+
+def test_adamw_of_more_tiles_than_a_launch_has_blocks():
+    """Blocks of 512 elements, fp32 state and bf16 gradients (120 GB). Every
+    element's first step is checked: m = (1 - b1) g and v = (1 - b2) g^2 as they
+    are rounded, p one lr away."""
+    n = BLOCKS * 512 + 513
+    g = torch.full((n,), 0.5, dtype=torch.bfloat16, device="cuda")
+    p, m, v = (torch.zeros(n, device="cuda") for _ in range(3))
+    steps = torch.zeros((), dtype=torch.int64, device="cuda")
+    opt = rar.AdamW(rar.GradSet([g]), [p], [m], [v], steps)
+    print(f"[adamw] {n} elements", flush=True)
+    opt.step(0.25, betas=(0.5, 0.75), eps=0.0, weight_decay=0.0)
+    assert int(steps) == 1
+    # the moments are exact, their corrections 1/2 and 1/4 and p = -lr but for a few roundings
+    assert all_equal(m, 0.25) and all_equal(v, 0.0625)
+    assert all_equal(p, float(p[0])) and abs(float(p[0]) + 0.25) <= 0.25 * 8 * 2.0 ** -24
+    opt.step(0.25, betas=(0.5, 0.75), eps=0.0, weight_decay=0.0)
+    assert int(steps) == 2
+    assert all_equal(m, 0.375) and all_equal(v, 0.109375)
