@@ -62,6 +62,7 @@ struct LinearArgs {
   float* partial;      // parts > 1: [part][I][round_up(J, 8)]
   float* row_sums;     // weight gradient: [part * tiles_j + tile_j][I], sums of A's rows (NULL: not wanted)
   int32_t tiles_i, tiles_j;
+  int32_t begin;    // the launch's first block
 };
 
 constexpr bool a_along(int dir) { return dir != DDP_LINEAR_BACKWARD_WEIGHT; }
@@ -572,7 +573,7 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
   // (8192 x 8192 x 2048 forward with z kept: 254 us; groups of 8, 258, of 1,
   // 283; tiles in the blocks' order, 299).
   const int tiles = g.tiles_i * g.tiles_j;
-  const int at = int(blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8);
+  const int at = g.begin + int(blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8);
   if (at >= tiles * g.parts) return;
   const int part = at / tiles, tile = at % tiles;
   constexpr int GROUP = 4;
@@ -844,10 +845,10 @@ __global__ __launch_bounds__(kThreads) void k_linear_join(LinearArgs g) {
 // because the layer has no inputs). Four threads share a column.
 template <int SRC, int DST>
 __global__ __launch_bounds__(kThreads) void k_column_sums(const void* src, int64_t ld, int64_t rows, int64_t N, void* db,
-                                                          int accumulate) {
+                                                          int accumulate, int64_t begin) {
   __shared__ float sums[4][64];
   const int c = int(threadIdx.x) & 63, group = int(threadIdx.x) >> 6;
-  const int64_t col = int64_t(blockIdx.x) * 64 + c;
+  const int64_t col = begin + int64_t(blockIdx.x) * 64 + c;
   float s = 0.0f;
   if (col < N) {
 #pragma unroll 4
@@ -908,7 +909,7 @@ __global__ __launch_bounds__(kThreads) void k_linear_few(LinearArgs g) {
   constexpr int V = DT == DDP_BF16 ? 8 : 4, OUTS = kFewOuts * M;
   __shared__ float sums[4][OUTS];
   const int lane = int(threadIdx.x) & 63, wave = int(threadIdx.x) >> 6;
-  const int64_t j0 = int64_t(blockIdx.x) * kFewOuts;
+  const int64_t j0 = (int64_t(g.begin) + blockIdx.x) * kFewOuts;
   float acc[OUTS] = {};  // [r * M + m]
 #pragma unroll 1
   for (int64_t k = int64_t(threadIdx.x) * V; k < g.K; k += kThreads * V) {
@@ -989,6 +990,12 @@ __global__ __launch_bounds__(kThreads) void k_act_backward(const void* dy, int64
 // ---------------------------------------------------------------- host side
 
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// `blocks` blocks in launches of kMaxGrid at most: launch(first block, grid).
+template <class F>
+void launch_blocks(int64_t blocks, F&& launch) {
+  for (int64_t b = 0; b < blocks; b += kMaxGrid) launch(b, dim3(unsigned(std::min(blocks - b, kMaxGrid))));
+}
 
 template <int DT>
 void launch_act_backward(const void* dy, int64_t lddy, const void* z, int64_t ldz, void* dz, int64_t lddz, int64_t M,
@@ -1117,8 +1124,10 @@ int launch_tiles(LinearArgs& g, hipStream_t s) {
   if (ti * tj * g.parts >= (int64_t(1) << 30)) return fail(DDP_EINVAL, "ddp_linear: too many tiles for one launch");
   g.tiles_i = int32_t(ti);
   g.tiles_j = int32_t(tj);
-  const dim3 grid(unsigned(round_up(ti * tj * g.parts, 8))), block(WI * WJ * 64);
-  hipLaunchKernelGGL((k_linear<DT, DIR, T, T, WI, WJ, LOAD>), grid, block, 0, s, g);
+  launch_blocks(round_up(ti * tj * g.parts, 8), [&](int64_t begin, dim3 grid) {
+    g.begin = int32_t(begin);
+    hipLaunchKernelGGL((k_linear<DT, DIR, T, T, WI, WJ, LOAD>), grid, dim3(WI * WJ * 64), 0, s, g);
+  });
   DDP_HIP_TRY(hipGetLastError(), "ddp_linear: launch");
   return DDP_OK;
 }
@@ -1141,13 +1150,15 @@ int launch_product(LinearArgs& g, void* workspace, bool want_rows, hipStream_t s
   const bool shorter = (a_along(DIR) ? g.K : g.I) < V || (b_along(DIR) ? g.K : g.J) < V;  // rows than a chunk
   if constexpr (DIR == DDP_LINEAR_FORWARD) {
     if (c.few) {
-      const dim3 grid(unsigned(div_up(g.J, kFewOuts))), block(kThreads);
-      if (g.I == 1)
-        hipLaunchKernelGGL((k_linear_few<DT, 1>), grid, block, 0, s, g);
-      else if (g.I == 2)
-        hipLaunchKernelGGL((k_linear_few<DT, 2>), grid, block, 0, s, g);
-      else
-        hipLaunchKernelGGL((k_linear_few<DT, kFewRows>), grid, block, 0, s, g);
+      launch_blocks(div_up(g.J, kFewOuts), [&](int64_t begin, dim3 grid) {
+        g.begin = int32_t(begin);
+        if (g.I == 1)
+          hipLaunchKernelGGL((k_linear_few<DT, 1>), grid, dim3(kThreads), 0, s, g);
+        else if (g.I == 2)
+          hipLaunchKernelGGL((k_linear_few<DT, 2>), grid, dim3(kThreads), 0, s, g);
+        else
+          hipLaunchKernelGGL((k_linear_few<DT, kFewRows>), grid, dim3(kThreads), 0, s, g);
+      });
       DDP_HIP_TRY(hipGetLastError(), "ddp_linear: launch");
       return DDP_OK;
     }
@@ -1176,7 +1187,7 @@ int launch_product(LinearArgs& g, void* workspace, bool want_rows, hipStream_t s
   else if (c.tile == 64)
     st = direct ? launch_tiles<DT, DIR, 64, 2, 2, kDirect>(g, s) : launch_tiles<DT, DIR, 64, 2, 2, kAny>(g, s);
   if (st != DDP_OK || g.parts == 1) return st;
-  const int64_t blocks = div_up(g.I * div_up(g.J, 8), kThreads);
+  const int64_t blocks = div_up(g.I * div_up(g.J, 8), kThreads);  // parts come with few tiles: one launch
   hipLaunchKernelGGL((k_linear_join<DT, DIR>), dim3(unsigned(blocks)), dim3(kThreads), 0, s, g);
   DDP_HIP_TRY(hipGetLastError(), "ddp_linear: join launch");
   return DDP_OK;
@@ -1352,19 +1363,16 @@ extern "C" int ddp_linear_backward_weight(const void* dz, int64_t lddz, const vo
     sums = g.row_sums, sums_ld = N, sums_rows = int64_t(g.parts) * g.tiles_j;
   }
   if (db == nullptr) return DDP_OK;
-  const dim3 grid(unsigned(div_up(N, 64))), block(kThreads);
   const bool from16 = K == 0 && dtype == DDP_BF16;
-  if (grad_dtype == DDP_BF16) {
-    if (from16)
-      hipLaunchKernelGGL((k_column_sums<DDP_BF16, DDP_BF16>), grid, block, 0, s, sums, sums_ld, sums_rows, N, db, accumulate);
+  launch_blocks(div_up(N, 64), [&](int64_t begin, dim3 grid) {
+    const auto launch = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, s, sums, sums_ld, sums_rows, N, db, accumulate, begin * 64);
+    };
+    if (grad_dtype == DDP_BF16)
+      from16 ? launch(k_column_sums<DDP_BF16, DDP_BF16>) : launch(k_column_sums<DDP_FP32, DDP_BF16>);
     else
-      hipLaunchKernelGGL((k_column_sums<DDP_FP32, DDP_BF16>), grid, block, 0, s, sums, sums_ld, sums_rows, N, db, accumulate);
-  } else {
-    if (from16)
-      hipLaunchKernelGGL((k_column_sums<DDP_BF16, DDP_FP32>), grid, block, 0, s, sums, sums_ld, sums_rows, N, db, accumulate);
-    else
-      hipLaunchKernelGGL((k_column_sums<DDP_FP32, DDP_FP32>), grid, block, 0, s, sums, sums_ld, sums_rows, N, db, accumulate);
-  }
+      from16 ? launch(k_column_sums<DDP_BF16, DDP_FP32>) : launch(k_column_sums<DDP_FP32, DDP_FP32>);
+  });
   DDP_HIP_TRY(hipGetLastError(), "ddp_linear_backward_weight: bias launch");
   return DDP_OK;
 }

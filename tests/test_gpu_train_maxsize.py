@@ -51,3 +51,29 @@ def test_adamw_of_more_tiles_than_a_launch_has_blocks():
     opt.step(0.25, betas=(0.5, 0.75), eps=0.0, weight_decay=0.0)
     assert int(steps) == 2
     assert all_equal(m, 0.375) and all_equal(v, 0.109375)
+
+
+def whole(shape, most):
+    """Whole numbers in [-most, most], small enough that bf16 and the sums below hold them exactly."""
+    return torch.empty(shape, dtype=torch.bfloat16, device="cuda").random_(0, 2 * most + 1).sub_(most)
+
+
+def test_few_rows_of_more_outputs_than_a_launch_has_blocks():
+    """Blocks of four outputs."""
+    n, k = BLOCKS * 4 + 5, 8
+    x, w = whole((1, k), 2), whole((n, k), 2)
+    print(f"[few rows] {n} outputs", flush=True)
+    y = rar.linear_forward(x, w)
+    assert torch.equal(y[0], (w * x).sum(1))
+
+
+def test_products_of_more_tiles_than_a_launch_has_blocks():
+    """Tiles of 64 rows and one column: forward, input gradient, weight and bias gradient."""
+    m = BLOCKS * 64 + 65
+    tall, one, dz = whole((m, 1), 9), whole((1, 1), 9), whole((1, m), 9)
+    print(f"[tiles] {m} rows", flush=True)
+    assert torch.equal(rar.linear_forward(tall, one), tall * one)
+    assert torch.equal(rar.linear_backward_input(tall, one), tall * one)
+    dw, db = torch.empty_like(tall), torch.empty(m, dtype=torch.bfloat16, device="cuda")
+    rar.linear_backward_weight(dz, one, dw, db)
+    assert torch.equal(dw, dz.t() * one) and torch.equal(db, dz[0])
