@@ -52,7 +52,7 @@ int ddp_grads_create(void* const* grads, const int64_t* numels, int32_t n, int32
  * made from it, may be left. */
 void ddp_grads_free(ddp_grads* grads);
 
-/* ddp_grads_norm: *norm_dev (a device float, overwritten) receives
+/* ddp_grads_norm: *norm_dev (a device float, overwritten, in none of the tensors) receives
  *   DDP_NORM_L2:  sqrt(sum g^2) over every element of every tensor;
  *   DDP_NORM_MAX: max |g|.
  * The squares are summed in fp64, so no finite fp32 gradient overflows or
@@ -67,7 +67,8 @@ int ddp_grads_norm(ddp_grads* grads, int32_t kind, float* norm_dev, void* stream
  * dtype), none of whose tensors overlaps one of `grads`, or NULL to scale
  * `grads` in place, where a factor of 1 leaves the gradients untouched. *norm_dev is
  * read when the launch runs: the value of ddp_grads_norm on the same stream, or one
- * combined from several sets' by the caller. A NaN norm gives NaN gradients;
+ * combined from several sets' by the caller; it lies in none of the tensors that
+ * are written. A NaN norm gives NaN gradients;
  * an infinite one gives f = 0. max_norm >= 0 (infinity: never clip a finite norm). */
 int ddp_grads_clip(const ddp_grads* grads, const ddp_grads* into, float max_norm, const float* norm_dev,
                    void* stream);
@@ -99,7 +100,8 @@ void ddp_adamw_free(ddp_adamw* opt);
  * The gradients are left as they are: clipping costs no pass of its own. If
  * norm_dev is given and *norm_dev is not finite, the step is skipped: nothing
  * is written. lr, eps, weight_decay and max_norm >= 0; beta1 and beta2 in
- * [0, 1). max_norm is not looked at without norm_dev. Calls on one optimizer
+ * [0, 1). max_norm is not looked at without norm_dev, which lies in nothing
+ * that the step writes. Calls on one optimizer
  * must be ordered. */
 int ddp_adamw_step(ddp_adamw* opt, double lr, double beta1, double beta2, double eps, double weight_decay,
                    double max_norm, const float* norm_dev, void* stream);

@@ -170,6 +170,7 @@ struct ddp_adamw {
   ddp::AdamTile* tiles = nullptr;
   unsigned int* tickets = nullptr;
   int64_t* step = nullptr;
+  std::vector<ddp::Span> written;  // everything but the gradients, by address
 };
 
 using namespace ddp;
@@ -228,6 +229,8 @@ extern "C" int ddp_adamw_create(const ddp_grads* grads, void* const* params, voi
     o->n_tiles = int64_t(tiles.size());
     o->bytes = grads->total * (elem_bytes(grads->dtype) + 12 + (params_bf16 == nullptr ? 0 : 2));
     o->step = step_dev;
+    for (const Span& w : spans)
+      if (w.what != std::string("grads")) o->written.push_back(w);
     const size_t table = size_t(round_up(int64_t(sizeof(AdamTile) * tiles.size()), 256));
     hipError_t e = hipMalloc(&o->memory, table + kTicketBytes);
     if (e != hipSuccess) {
@@ -275,6 +278,8 @@ extern "C" int ddp_adamw_step(ddp_adamw* o, double lr, double beta1, double beta
   if (norm_dev != nullptr) {
     if (!(max_norm >= 0.0)) return fail(DDP_EINVAL, std::string(fn) + ": max_norm is negative or not a number");
     st = check_scalar(norm_dev, 4, fn, "norm_dev");
+    if (st != DDP_OK) return st;
+    st = check_norm_apart(norm_dev, o->written, fn);
     if (st != DDP_OK) return st;
   }
   AdamArgs a{};

@@ -252,6 +252,16 @@ int check_disjoint(std::vector<Span>& spans, const char* fn) {
   return DDP_OK;
 }
 
+int check_norm_apart(const float* norm_dev, const std::vector<Span>& written, const char* fn) {
+  // the first span that ends behind the norm's start
+  const auto s = std::partition_point(written.begin(), written.end(), [&](const Span& w) {
+    return reinterpret_cast<uintptr_t>(w.p) + uint64_t(w.bytes) <= reinterpret_cast<uintptr_t>(norm_dev);
+  });
+  if (s != written.end() && spans_overlap(norm_dev, sizeof(float), s->p, s->bytes))
+    return fail(DDP_EINVAL, std::string(fn) + ": norm_dev and " + span_name(*s) + " overlap");
+  return DDP_OK;
+}
+
 int check_scalar(const void* p, int64_t bytes, const char* fn, const char* what) {
   int st = check_range(p, bytes, fn, what);
   if (st != DDP_OK) return st;
@@ -313,6 +323,7 @@ extern "C" int ddp_grads_create(void* const* grads, const int64_t* numels, int32
       g->ptrs.assign(grads, grads + n);
       g->numels.assign(numels, numels + n);
     }
+    g->spans = std::move(spans);
     g->total = total;
     g->lo = lo;
     g->hi = hi;
@@ -366,6 +377,8 @@ extern "C" int ddp_grads_norm(ddp_grads* g, int32_t kind, float* norm_dev, void*
   if (st != DDP_OK) return st;
   st = check_scalar(norm_dev, 4, fn, "norm_dev");
   if (st != DDP_OK) return st;
+  st = check_norm_apart(norm_dev, g->spans, fn);
+  if (st != DDP_OK) return st;
   hipStream_t s = as_stream(stream);
   if (g->dtype == DDP_FP32)
     kind == DDP_NORM_L2 ? launch_norm<DDP_FP32, DDP_NORM_L2>(g, norm_dev, s) : launch_norm<DDP_FP32, DDP_NORM_MAX>(g, norm_dev, s);
@@ -390,6 +403,8 @@ extern "C" int ddp_grads_clip(const ddp_grads* g, const ddp_grads* into, float m
     if (st != DDP_OK) return st;
   }
   st = check_scalar(norm_dev, 4, fn, "norm_dev");
+  if (st != DDP_OK) return st;
+  st = check_norm_apart(norm_dev, into->spans, fn);
   if (st != DDP_OK) return st;
   if (g->n_tiles == 0) return DDP_OK;
   hipStream_t s = as_stream(stream);

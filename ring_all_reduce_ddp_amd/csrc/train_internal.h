@@ -107,6 +107,10 @@ struct Span {
 // DDP_EINVAL, naming both, if two of the spans overlap (empty ones do not).
 int check_disjoint(std::vector<Span>& spans, const char* fn);
 bool spans_overlap(const void* a, int64_t abytes, const void* b, int64_t bbytes);
+// DDP_EINVAL if the norm's place overlaps one of `written`: sorted, disjoint
+// spans (as check_disjoint leaves them) that the call's blocks write while others
+// read the norm, or read until it is written.
+int check_norm_apart(const float* norm_dev, const std::vector<Span>& written, const char* fn);
 // DDP_EINVAL unless `dev` is the current device.
 int check_device(int dev, const char* fn);
 // p: a device pointer to an aligned scalar of `bytes` bytes.
@@ -119,6 +123,7 @@ struct ddp_grads {
   int dev = 0;
   std::vector<void*> ptrs;
   std::vector<int64_t> numels;
+  std::vector<ddp::Span> spans;   // of the tensors that are not empty, by address
   int64_t total = 0;              // elements
   uintptr_t lo = 0, hi = 0;       // addresses from the lowest tensor's start to the highest one's end
   int64_t n_tiles = 0;

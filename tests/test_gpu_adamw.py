@@ -194,3 +194,17 @@ def test_refusals():
     with pytest.raises(ValueError, match="together"):
         opt.step(max_norm=1.0, **OPT)
     assert int(t) == 0 and bool((p == 1).all())
+
+
+def test_a_norm_inside_the_state_is_refused():
+    g, p, m, v = (torch.ones(100, device="cuda") for _ in range(4))
+    c = torch.ones(100, dtype=torch.bfloat16, device="cuda")
+    t = torch.zeros((), dtype=torch.int64, device="cuda")
+    opt = rar.AdamW(rar.GradSet([g]), [p], [m], [v], t, params_bf16=[c])
+    for inside, what in ((p[0], "params"), (m[99], "exp_avg"), (v[50], "exp_avg_sq"), (c.view(torch.float32)[49], "params_bf16"),
+                         (t.view(1).view(torch.float32)[1], "step_dev")):
+        with pytest.raises(rar.DDPError, match="norm_dev and " + what):
+            opt.step(max_norm=1.0, norm=inside, **OPT)
+    assert int(t) == 0 and bool((p == 1).all())
+    opt.step(max_norm=1.0, norm=g[3], **OPT)   # the gradients are only read
+    assert int(t) == 1

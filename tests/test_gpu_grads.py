@@ -259,3 +259,23 @@ def test_a_freed_set_is_refused():
     with pytest.raises(rar.DDPError, match="grads is NULL"):
         into.norm()
     assert (a == 4.0).all() and (b == 4.0).all()
+
+
+def test_a_norm_inside_what_is_written_is_refused():
+    big = torch.ones(100, device="cuda")
+    s, into = rar.GradSet([big[10:20], big[40:60]]), rar.GradSet([big[20:30], big[70:90]])
+    norm = s.norm(out=big[25])   # another set's tensor is none of the norm's business
+    for at in (10, 19, 40, 59):
+        with pytest.raises(rar.DDPError, match="norm_dev and grads"):
+            s.norm(out=big[at])
+        with pytest.raises(rar.DDPError, match="norm_dev and grads"):
+            s.clip(1.0, big[at])
+    for at in (20, 25, 89):
+        with pytest.raises(rar.DDPError, match="norm_dev and grads"):
+            s.clip(1.0, big[at], into=into)
+    assert float(norm) == pytest.approx(math.sqrt(30.0), rel=U) and int((big == 1).sum()) == 99
+    for at in (9, 39, 60, 99):
+        s.norm(out=big[at])
+    s.clip(1.0, big[45], into=into)   # among the gradients, which are only read
+    f = 1 / (1 + 1e-6)
+    assert ((into.tensors[0].double() - f).abs() <= 5 * U).all() and ((into.tensors[1].double() - f).abs() <= 5 * U).all()
