@@ -110,7 +110,8 @@ int ddp_adamw_step(ddp_adamw* opt, double lr, double beta1, double beta2, double
  * Matrices are row-major: element (i, j) of a matrix with leading dimension
  * ld lies at i * ld + j; ld >= its number of columns and, with more than one
  * row, ld <= 2^22. Pointers are aligned to
- * the element; no other alignment is needed. M, N, K >= 0: M rows (tokens),
+ * the element; no other alignment is needed. Matrices that must not overlap
+ * share no element; column blocks of one buffer do not. M, N, K >= 0: M rows (tokens),
  * K input and N output features; weights are w[N][K].
  * `dtype` is the type of x, w, bias, residual, y, z, dz, dx and add. Products
  * are summed in fp32: bf16 on the bf16 matrix instructions, fp32 on the fp32

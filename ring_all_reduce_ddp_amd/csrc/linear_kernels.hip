@@ -1204,6 +1204,20 @@ struct Matrix {
   int64_t bytes() const { return rows > 0 && cols > 0 ? ((rows - 1) * ld + cols) * eb : 0; }
 };
 
+// Whether two matrices share a byte. Of one pitch (or one of them a single
+// row, which has none), they may lie side by side as column blocks.
+bool matrices_overlap(const Matrix& a, const Matrix& b) {
+  if (!spans_overlap(a.p, a.bytes(), b.p, b.bytes())) return false;
+  if (a.rows == 1 && b.rows == 1) return true;
+  const uint64_t pa = uint64_t(a.ld) * a.eb, pb = uint64_t(b.ld) * b.eb;
+  if (a.rows > 1 && b.rows > 1 && pa != pb) return true;
+  const uint64_t pitch = a.rows > 1 ? pa : pb;
+  const uint64_t wa = uint64_t(a.cols) * a.eb, wb = uint64_t(b.cols) * b.eb;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  const uint64_t ahead = y >= x ? (y - x) % pitch : (pitch - (x - y) % pitch) % pitch;  // of b's columns, before a's begin again
+  return ahead < wa || ahead + wb > pitch;
+}
+
 // Every matrix lies in its allocation, and what is written overlaps nothing
 // else, except that matrix `in_place` may be matrix `out` (the same place and rows).
 int check_matrices(const char* fn, const Matrix* m, int n, int in_place, int out) {
@@ -1223,7 +1237,7 @@ int check_matrices(const char* fn, const Matrix* m, int n, int in_place, int out
     for (int o = 0; o < n; ++o) {
       if (o == k || m[o].p == nullptr) continue;
       if (k == out && o == in_place && m[o].p == m[k].p && m[o].ld == m[k].ld) continue;
-      if (spans_overlap(m[k].p, m[k].bytes(), m[o].p, m[o].bytes()))
+      if (matrices_overlap(m[k], m[o]))
         return fail(DDP_EINVAL, std::string(fn) + ": " + m[k].what + " overlaps " + m[o].what);
     }
   }

@@ -440,3 +440,31 @@ def test_refusals():
 def test_kept_z_beyond_the_cache(size, dtype, layout):
     """y and z of over two thirds of the Infinity Cache: z's stores pass it."""
     forward_case(*size, dtype, "gelu", True, False, True, *layout)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("m, n, k", [(300, 256, 128), (70, 33, 41), (3, 72, 40)])
+def test_column_blocks_of_one_buffer(m, n, k, dtype):
+    """Inputs and outputs side by side in one buffer: the results of separate ones, and the inputs stay."""
+    g = gen(11)
+    x, w, r = matrix(g, m, k, dtype), matrix(g, n, k, dtype), matrix(g, m, n, dtype)
+    want, want_z = rar.linear_forward(x, w, residual=r, act="silu", keep=True)
+    want_dx = rar.linear_backward_input(r, w, add=x)
+    wide = torch.full((m, 3 * n + k), math.nan, device="cuda").to(DT[dtype])
+    y, z, r2, x2 = wide.split([n, n, n, k], 1)
+    r2.copy_(r)
+    x2.copy_(x)
+    rar.linear_forward(x2, w, residual=r2, act="silu", out=y, z=z)
+    # loads of another alignment may take another cut of the sum
+    tol = 4 * (k + 2) * U * (x.double().abs() @ w.double().abs().t())
+    close(z, want_z.double(), tol + (B if dtype == "bf16" else U) * want_z.double().abs(), dtype, "z")
+    close(y, want.double(), 2 * tol + 2 * (B if dtype == "bf16" else 8 * U) * (want.double().abs() + r.double().abs()), dtype, "y")
+    assert torch.equal(x2, x) and torch.equal(r2, r)
+    wide = torch.full((m, 2 * k + n), math.nan, device="cuda").to(DT[dtype])
+    dx, a, dz = wide.split([k, k, n], 1)
+    a.copy_(x)
+    dz.copy_(r)
+    rar.linear_backward_input(dz, w, add=a, out=dx)
+    tol = 4 * (n + 2) * U * (r.double().abs() @ w.double().abs())
+    close(dx, want_dx.double(), tol + (B if dtype == "bf16" else U) * (want_dx.double().abs() + x.double().abs()), dtype, "dx")
+    assert torch.equal(a, x) and torch.equal(dz, r)

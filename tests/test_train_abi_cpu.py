@@ -160,3 +160,22 @@ def test_linear_workspace_arguments():
     refused(lib.ddp_linear_workspace(0, -1, 1, 1, 0, ctypes.byref(out)), "M, N and K")
     refused(lib.ddp_linear_workspace(0, 1, 1, 1, 4, ctypes.byref(out)), "dtype")
     assert out.value == 0
+
+
+@pytest.mark.parametrize("change, overlaps", [
+    # y (4 x 8, of fp32) beside the residual, z and x in one buffer with rows of 32 and 40 elements
+    (dict(y=A, ldy=32, residual=A + 32, ldr=32), False), (dict(y=A + 32, ldy=32, residual=A, ldr=32), False),
+    (dict(y=A, ldy=32, residual=A + 28, ldr=32), True), (dict(y=A + 28, ldy=32, residual=A, ldr=32), True),
+    (dict(y=A, ldy=32, z=A + 96, ldz=32), False), (dict(y=A, ldy=32, z=A + 100, ldz=32), True),
+    (dict(y=A + 100, ldy=32, z=A, ldz=32), True), (dict(y=A, ldy=32, z=A + 128 + 32, ldz=32), False),
+    (dict(y=A, ldy=32, z=A + 128 - 4, ldz=32), True), (dict(y=A + 64, ldy=40, x=A, ldx=40), False),
+    (dict(y=A + 60, ldy=40, x=A, ldx=40), True), (dict(y=A, ldy=32, z=A + 32, ldz=33), True),
+    # the bias, one row, in the gap behind y's columns
+    (dict(y=A, ldy=32, bias=A + 128 + 64), False), (dict(y=A, ldy=32, bias=A + 128 + 100), True),
+    (dict(y=A, ldy=32, bias=A + 128 + 28), True),
+])
+def test_column_blocks_of_one_buffer_do_not_overlap(change, overlaps):
+    """On addresses of no allocation, which is what a call without overlap is refused for."""
+    base = dict(x=A + 7 * FAR)
+    status = rar.lib.ddp_linear_forward(*forward_args(**{**base, **change}))
+    refused(status, "overlaps" if overlaps else "not inside a device allocation")
