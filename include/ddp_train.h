@@ -122,6 +122,11 @@ int ddp_adamw_step(ddp_adamw* opt, double lr, double beta1, double beta2, double
  *   DDP_ACT_GELU       z/2 (1 + erf(z / sqrt 2))
  *   DDP_ACT_GELU_TANH  z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))
  *   DDP_ACT_SILU       z / (1 + exp(-z))
+ * With fp32 data a value is off by a few 2^-24 of itself (for negative z, where
+ * the exponential rules, times the exponent: gelu z^2 / 2, gelu_tanh 0.07 |z|^3).
+ * With bf16 data faster forms are used, whose errors hide behind the result's
+ * rounding: exponentials are off by 2^-24 times their argument, and gelu by 1.5e-7
+ * |z| at most, which is 2e-3 of it at z = -5 and more below, where it is under 2e-6.
  * Workspace: with few output tiles the long sum is cut into parts, which need
  * scratch on the device: ddp_linear_workspace gives the bytes (0 if none) for
  * a direction and shape on the current device. A call with less (NULL, 0) is refused. The

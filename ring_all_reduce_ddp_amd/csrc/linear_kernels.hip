@@ -70,41 +70,68 @@ constexpr bool b_along(int dir) { return dir == DDP_LINEAR_FORWARD; }
 
 // ---------------------------------------------------------------- activations
 
-// x / y by the reciprocal instruction (1 ulp): the outputs' last step takes
-// the vector units while the matrix units wait, so its length counts.
-__device__ __forceinline__ float quotient(float x, float y) { return x * __builtin_amdgcn_rcpf(y); }
+// The outputs' last step takes the vector units while the matrix units wait, so
+// its length counts where the products are short, in bf16. There, quotients
+// come from the reciprocal instruction (1 ulp) and exponentials from the
+// exponential instruction (relative error 2^-24 times its argument and 2 ulp): errors
+// far below the outputs' rounding. fp32 data gets the library's functions.
+template <int DT>
+__device__ __forceinline__ float quotient(float x, float y) {
+  return DT == DDP_BF16 ? x * __builtin_amdgcn_rcpf(y) : x / y;
+}
+template <int DT>
+__device__ __forceinline__ float exponential(float x) {
+  return DT == DDP_BF16 ? __expf(x) : expf(x);
+}
 
 // 2 sqrt(2/pi) (z + 0.044715 z^3) = z (kTanh1 + kTanh3 z^2); 1 + tanh(u) = 2 / (1 + exp(-2u))
 constexpr float kTanh1 = 1.59576912f, kTanh3 = 0.0713548163f;
 
-// The normal distribution function (1 + erf(z / sqrt 2)) / 2 and exp(-z^2 / 2),
-// by formula 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical
+// The normal distribution function (1 + erf(z / sqrt 2)) / 2 and exp(-z^2 / 2).
+// With x = |z| / sqrt 2, it is erfc(x) / 2 or 1 less that: 1 + erf would cancel
+// for negative z.
+//
+// bf16: by formula 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical
 // Functions: erfc(x) = t (a1 + ... + a5 t^4) exp(-x^2), t = 1 / (1 + p x), off by
-// 1.5e-7 at most, near an fp32 rounding of 1. Taken as erfc, nothing cancels
-// for negative z. One exponential and one reciprocal serve value and slope;
-// the library's erff is several times as long (8192 x 8192 x 2048 forward
-// with z kept: 263 us against 286).
+// 1.5e-7 at most. That is 2e-4 of the function itself at z = -3.5 and 1.6e-3 at
+// -5, where it still rounds to bf16 about as well as the exact one, and 3e-2 at -10, of
+// values near 1e-23. One exponential and one reciprocal serve value and slope; the
+// library's erff is several times as long (8192 x 8192 x 2048 forward with z
+// kept: 263 us against 286).
+//
+// fp32: the library's erfc, good to 4 ulp, and x's rounding: 2^-24 (1.3 z^2 +
+// 9.3) of the function at most. Its length shows where little else is done (4096 x 4096
+// slopes alone 41 us against 29, a forward product of 64 terms 51 against 40) and
+// not in longer products (1037 x 1023 x 2049 60 us either way).
 struct Normal {
   float cdf, bell;
 };
+template <int DT>
 __device__ __forceinline__ Normal normal(float z) {
   const float x = fabsf(z) * 0.70710678f;
-  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.0f));
-  const float bell = __expf(-x * x);
-  float q = fmaf(1.061405429f, t, -1.453152027f);
-  q = fmaf(q, t, 1.421413741f);
-  q = fmaf(q, t, -0.284496736f);
-  q = fmaf(q, t, 0.254829592f);
-  q *= 0.5f * t * bell;
+  float q, bell;
+  if constexpr (DT == DDP_BF16) {
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.0f));
+    bell = __expf(-x * x);
+    q = fmaf(1.061405429f, t, -1.453152027f);
+    q = fmaf(q, t, 1.421413741f);
+    q = fmaf(q, t, -0.284496736f);
+    q = fmaf(q, t, 0.254829592f);
+    q *= 0.5f * t * bell;
+  } else {
+    q = 0.5f * erfcf(x);
+    bell = expf(-0.5f * z * z);
+  }
   return {z < 0.0f ? q : 1.0f - q, bell};
 }
 
-template <int ACT>
+template <int DT, int ACT>
 __device__ __forceinline__ float act_value(float z) {
   if constexpr (ACT == DDP_ACT_RELU) return z < 0.0f ? 0.0f : z;  // a NaN stays
-  if constexpr (ACT == DDP_ACT_GELU) return z * normal(z).cdf;
-  if constexpr (ACT == DDP_ACT_GELU_TANH) return quotient(z, 1.0f + __expf(-z * fmaf(kTanh3, z * z, kTanh1)));
-  if constexpr (ACT == DDP_ACT_SILU) return quotient(z, 1.0f + __expf(-z));
+  if constexpr (ACT == DDP_ACT_GELU) return z * normal<DT>(z).cdf;
+  if constexpr (ACT == DDP_ACT_GELU_TANH)
+    return quotient<DT>(z, 1.0f + exponential<DT>(-z * fmaf(kTanh3, z * z, kTanh1)));
+  if constexpr (ACT == DDP_ACT_SILU) return quotient<DT>(z, 1.0f + exponential<DT>(-z));
   return z;
 }
 
@@ -112,23 +139,23 @@ __device__ __forceinline__ float act_value(float z) {
 // factors would become infinity times zero. A NaN stays.
 __device__ __forceinline__ float within(float z, float most) { return z > most ? most : z < -most ? -most : z; }
 
-template <int ACT>
+template <int DT, int ACT>
 __device__ __forceinline__ float act_slope(float z) {
   if constexpr (ACT == DDP_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
   if constexpr (ACT == DDP_ACT_GELU) {
     z = within(z, 16.0f);
-    const Normal d = normal(z);
+    const Normal d = normal<DT>(z);
     return fmaf(z * 0.39894228f, d.bell, d.cdf);
   }
   if constexpr (ACT == DDP_ACT_GELU_TANH) {
     z = within(z, 16.0f);
     const float z2 = z * z;
-    const float s = quotient(1.0f, 1.0f + __expf(-z * fmaf(kTanh3, z2, kTanh1)));  // (1 + tanh u) / 2
-    return fmaf(z * s * (1.0f - s), fmaf(3.0f * kTanh3, z2, kTanh1), s);             // s + z s (1 - s) 2u'
+    const float s = quotient<DT>(1.0f, 1.0f + exponential<DT>(-z * fmaf(kTanh3, z2, kTanh1)));  // (1 + tanh u) / 2
+    return fmaf(z * s * (1.0f - s), fmaf(3.0f * kTanh3, z2, kTanh1), s);                          // s + z s (1 - s) 2u'
   }
   if constexpr (ACT == DDP_ACT_SILU) {
     z = within(z, 104.0f);
-    const float s = quotient(1.0f, 1.0f + __expf(-z));
+    const float s = quotient<DT>(1.0f, 1.0f + exponential<DT>(-z));
     return s * fmaf(z, 1.0f - s, 1.0f);
   }
   return 1.0f;
@@ -241,11 +268,12 @@ __device__ __forceinline__ void before_store(const LinearArgs& g, int64_t i, int
     if constexpr (DIR == DDP_LINEAR_FORWARD) {
       for (int k = 0; k < 8; ++k) v[k] += bias[k];  // zeros without a bias
       if (g.z != nullptr) store8<DT>(g.z, i * g.ldz + j, n, v, g.stream_z != 0);
-      for (int k = 0; k < 8; ++k) v[k] = act_value<ACT>(v[k]);
+      for (int k = 0; k < 8; ++k) v[k] = act_value<DT, ACT>(v[k]);
     } else if constexpr (ACT != DDP_ACT_NONE) {
       float z[8];
       unpack8<DT>(x.z, z);
-      for (int k = 0; k < 8; ++k) v[k] *= act_slope<ACT>(z[k]);
+#pragma unroll  // else z goes to scratch memory
+      for (int k = 0; k < 8; ++k) v[k] *= act_slope<DT, ACT>(z[k]);
     }
     if (g.e != nullptr) {
       unpack8<DT>(x.e, e);
@@ -954,16 +982,16 @@ __global__ __launch_bounds__(kThreads) void k_linear_few(LinearArgs g) {
   float y = z;
   switch (g.act) {
     case DDP_ACT_RELU:
-      y = act_value<DDP_ACT_RELU>(z);
+      y = act_value<DT, DDP_ACT_RELU>(z);
       break;
     case DDP_ACT_GELU:
-      y = act_value<DDP_ACT_GELU>(z);
+      y = act_value<DT, DDP_ACT_GELU>(z);
       break;
     case DDP_ACT_GELU_TANH:
-      y = act_value<DDP_ACT_GELU_TANH>(z);
+      y = act_value<DT, DDP_ACT_GELU_TANH>(z);
       break;
     case DDP_ACT_SILU:
-      y = act_value<DDP_ACT_SILU>(z);
+      y = act_value<DT, DDP_ACT_SILU>(z);
       break;
   }
   if (g.e != nullptr) y += Ops<DT>::load1(g.e, m * g.lde + j);
@@ -982,7 +1010,7 @@ __global__ __launch_bounds__(kThreads) void k_act_backward(const void* dy, int64
     float g[8], x[8];
     load8<DT>(dy, m * lddy + j, n, g);
     load8<DT>(z, m * ldz + j, n, x);
-    for (int k = 0; k < 8; ++k) g[k] *= act_slope<ACT>(x[k]);
+    for (int k = 0; k < 8; ++k) g[k] *= act_slope<DT, ACT>(x[k]);
     store8<DT>(dz, m * lddz + j, n, g);
   }
 }

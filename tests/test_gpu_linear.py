@@ -468,3 +468,49 @@ def test_column_blocks_of_one_buffer(m, n, k, dtype):
     tol = 4 * (n + 2) * U * (r.double().abs() @ w.double().abs())
     close(dx, want_dx.double(), tol + (B if dtype == "bf16" else U) * (want_dx.double().abs() + x.double().abs()), dtype, "dx")
     assert torch.equal(a, x) and torch.equal(dz, r)
+
+
+def act_and_bound(z, act):
+    """An activation in 64 bits, without sums that cancel for negative z, and
+    the most that its fp32 form may be off for exact z. The library's
+    erfc is taken as good to 8u (4 ulp), its exponential to 4u.
+    - gelu: x = |z| / sqrt 2 is off by 1.3u of itself, which erfc's condition
+      number takes up to z^2 + 1 times: q = erfc(x) / 2 to u (1.3 z^2 + 9.3). The
+      function is q, or 1 - q with u/2 more, and the product u.
+    - gelu_tanh: the exponent w = z (k1 + k3 z^2) is off by 4.5u of itself (two
+      constants, square, fma, product), which 1 / (1 + exp(-w)) takes 1 - s
+      times; sum and quotient u each.
+    - silu: the same without the exponent's errors.
+    The smallest subnormal times z comes to that."""
+    tiny = 2.0 ** -149 * (z.abs() + 1)
+    if act == "gelu":
+        y = z * torch.special.erfc(-z * math.sqrt(0.5)) / 2
+        q = torch.special.erfc(z.abs() * math.sqrt(0.5)) / 2
+        return y, z.abs() * U * (q * (1.3 * z * z + 9.3) + 0.5 * (z > 0)) + U * y.abs() + tiny
+    w = z * (math.sqrt(8 / math.pi) * (1 + 0.044715 * z * z)) if act == "gelu_tanh" else z
+    y = z * torch.sigmoid(w)
+    return y, y.abs() * U * (torch.sigmoid(-w) * (4 + (4.5 * w.abs() if act == "gelu_tanh" else 0)) + 2) * 1.0001 + tiny
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+def test_activations_of_fp32_to_a_few_roundings(act, rows):
+    most = {"gelu": 12.0, "gelu_tanh": 8.0, "silu": 40.0}[act]
+    z = torch.linspace(-most, most, 100_003, device="cuda")
+    y = rar.linear_forward(torch.ones(rows, 1, device="cuda"), z.view(-1, 1), act=act)
+    want, lim = act_and_bound(z.double(), act)
+    bad = ~((y.double() - want).abs() <= lim)
+    assert not bool(bad.any()), f"{int(bad.sum())} of {bad.numel()} outside, first at z = {float(z[bad.nonzero()[0, 1]])}"
+
+
+def test_slope_of_fp32_gelu_to_a_few_roundings():
+    """cdf + z bell: the function as above, the bell's exponent u, its
+    exponential 4u, two products and the fma."""
+    z = torch.linspace(-12, 12, 100_003, device="cuda").view(1, -1)
+    s = rar.act_backward(torch.ones_like(z), z, "gelu")
+    z = z.double()
+    q, bell = torch.special.erfc(z.abs() * math.sqrt(0.5)) / 2, torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    want = torch.special.erfc(-z * math.sqrt(0.5)) / 2 + z * bell
+    lim = U * (q * (1.3 * z * z + 9.3) + 0.5 * (z > 0) + z.abs() * bell * (z * z / 2 + 7) + want.abs()) + 2.0 ** -145
+    bad = ~((s.double() - want).abs() <= lim)
+    assert not bool(bad.any()), f"{int(bad.sum())} outside, first at z = {float(z[0, bad.nonzero()[0, 1]])}"
