@@ -142,6 +142,14 @@ int ddp_adamw_step(ddp_adamw* opt, double lr, double beta1, double beta2, double
 #define DDP_LINEAR_BACKWARD_WEIGHT 2
 int ddp_linear_workspace(int32_t direction, int64_t M, int64_t N, int64_t K, int32_t dtype, int64_t* bytes);
 
+/* ddp_linear_tiling: how a product of these sizes is cut, for whoever wants to
+ * understand its time or to test a form: *tile is the side of its square tiles
+ * (0: a few rows, without tiles), *parts the number of parts of the sum.
+ * direct = 1: every operand's rows begin on 16 bytes and hold whole 16-byte
+ * chunks; 0: any other alignment. */
+int ddp_linear_tiling(int32_t direction, int64_t M, int64_t N, int64_t K, int32_t dtype, int32_t direct, int32_t* tile,
+                      int32_t* parts);
+
 /* y = act(x w^T + bias) + residual; z (NULL: not kept) receives
  * rnd(x w^T + bias), which the backward pass takes. bias[N] and
  * residual may be NULL. The activation is applied to the unrounded sum.

@@ -103,6 +103,7 @@ def _load():
         "ddp_adamw_free": (None, [vp]),
         "ddp_adamw_step": (ctypes.c_int, [vp, f64, f64, f64, f64, f64, f64, vp, vp]),
         "ddp_linear_workspace": (ctypes.c_int, [i32, i64, i64, i64, i32, ctypes.POINTER(i64)]),
+        "ddp_linear_tiling": (ctypes.c_int, [i32, i64, i64, i64, i32, i32, ctypes.POINTER(i32), ctypes.POINTER(i32)]),
         "ddp_linear_forward": (ctypes.c_int, [vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, i64, i64, i64, i64,
                                               i32, i32, vp, i64, vp]),
         "ddp_linear_backward_input": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64,
@@ -653,6 +654,17 @@ LINEAR_FORWARD, LINEAR_BACKWARD_INPUT, LINEAR_BACKWARD_WEIGHT = 0, 1, 2
 def linear_workspace(direction, m, n, k, dtype):
     """Bytes of scratch that a linear call of these sizes needs."""
     return _linear_workspace(int(direction), int(m), int(n), int(k), dtype_code(dtype))
+
+
+def linear_tiling(direction, m, n, k, dtype, direct=True):
+    """(tile, parts): the side of the square tiles that a product of these
+    sizes is cut into (0: a few rows, without tiles) and the parts of its sum;
+    direct: the operands' rows are whole, aligned 16-byte chunks (see
+    ddp_linear_tiling in include/ddp_train.h)."""
+    tile, parts = ctypes.c_int32(), ctypes.c_int32()
+    _check(_get_lib().ddp_linear_tiling(int(direction), int(m), int(n), int(k), dtype_code(dtype), 1 if direct else 0,
+                                        ctypes.byref(tile), ctypes.byref(parts)))
+    return tile.value, parts.value
 
 
 @functools.lru_cache(maxsize=4096)

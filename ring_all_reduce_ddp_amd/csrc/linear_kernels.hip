@@ -1315,6 +1315,24 @@ extern "C" int ddp_linear_workspace(int32_t direction, int64_t M, int64_t N, int
   return DDP_OK;
 }
 
+extern "C" int ddp_linear_tiling(int32_t direction, int64_t M, int64_t N, int64_t K, int32_t dtype, int32_t direct,
+                                 int32_t* tile, int32_t* parts) {
+  const char* fn = "ddp_linear_tiling";
+  if (tile == nullptr || parts == nullptr) return fail(DDP_EINVAL, std::string(fn) + ": an output is NULL");
+  *tile = *parts = 0;
+  if (direction < DDP_LINEAR_FORWARD || direction > DDP_LINEAR_BACKWARD_WEIGHT)
+    return fail(DDP_EINVAL, std::string(fn) + ": unknown direction");
+  if (direct != 0 && direct != 1) return fail(DDP_EINVAL, std::string(fn) + ": direct must be 0 or 1");
+  int st = check_common(fn, M, N, K, dtype, DDP_ACT_NONE);
+  if (st != DDP_OK) return st;
+  int64_t I, J, S;
+  product_sizes(direction, M, N, K, &I, &J, &S);
+  const Cut c = cut_of(direction, I, J, S, dtype, direct != 0);
+  *tile = c.few ? 0 : c.tile;
+  *parts = c.parts;
+  return DDP_OK;
+}
+
 extern "C" int ddp_linear_forward(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias,
                                   const void* residual, int64_t ldr, void* y, int64_t ldy, void* z, int64_t ldz,
                                   int64_t M, int64_t N, int64_t K, int32_t dtype, int32_t act, void* workspace,

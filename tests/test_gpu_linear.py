@@ -514,3 +514,38 @@ def test_slope_of_fp32_gelu_to_a_few_roundings():
     lim = U * (q * (1.3 * z * z + 9.3) + 0.5 * (z > 0) + z.abs() * bell * (z * z / 2 + 7) + want.abs()) + 2.0 ** -145
     bad = ~((s.double() - want).abs() <= lim)
     assert not bool(bad.any()), f"{int(bad.sum())} outside, first at z = {float(z[0, bad.nonzero()[0, 1]])}"
+
+
+# dtype, whether rows are whole aligned chunks, tile, the output's rows and
+# columns (with ragged edges), and sums whose steps of 128 bytes are: three
+# whole; four; eight; three, four and eight and a part of one; and one cut into
+# parts of several steps
+TILED = [("bf16", True, 256, (2312, 3336), (192, 256, 512, 200, 264, 520), (392, 2696, 5128)),
+         ("bf16", True, 128, (520, 3592), (192, 256, 512, 200, 264, 520), (136, 1800, 2056)),
+         ("bf16", False, 128, (713, 4105), (192, 256, 512, 201, 265, 521), (521, 1161, 2057)),
+         ("fp32", True, 128, (712, 4104), (96, 128, 256, 104, 136, 264), (392, 2312, 1032)),
+         ("fp32", False, 128, (713, 4105), (96, 128, 256, 105, 137, 265), (521, 1161, 1033))]
+TILED = [(dtype, direct, tile, (*out, terms), False) for dtype, direct, tile, out, sums, _ in TILED for terms in sums] + \
+        [(dtype, direct, tile, cut, True) for dtype, direct, tile, _, _, cut in TILED]
+
+
+@pytest.mark.parametrize("dtype, direct, tile, size, in_parts", TILED, ids=str)
+@pytest.mark.parametrize("what", ["forward", "input", "weight"])
+def test_every_tile_over_many_steps(what, dtype, direct, tile, size, in_parts):
+    """The main loop of every tile and loader runs its pairs of whole steps;
+    the sizes' cut is asked for, so that other cuts cannot take the cases away."""
+    i, j, terms = size
+    m, n, k = {"forward": (i, j, terms), "input": (i, terms, j), "weight": (terms, i, j)}[what]
+    direction = {"forward": rar.LINEAR_FORWARD, "input": rar.LINEAR_BACKWARD_INPUT, "weight": rar.LINEAR_BACKWARD_WEIGHT}[what]
+    got, parts = rar.linear_tiling(direction, m, n, k, dtype, direct)
+    assert got == tile and (parts > 1) == in_parts
+    step = 64 if dtype == "bf16" else 32
+    assert -(-(-(-terms // step)) // parts) >= 3
+    layout = (8, 0) if direct else (3, 1)
+    if what == "forward":
+        forward_case(m, n, k, dtype, "silu", True, True, True, *layout)
+    elif what == "input":
+        input_case(m, n, k, dtype, "gelu", True, *layout)
+    else:
+        weight_case(m, n, k, dtype, "fp32", True, True, *layout)
+        weight_case(m, n, k, dtype, dtype, False, False, *layout)

@@ -179,3 +179,19 @@ def test_column_blocks_of_one_buffer_do_not_overlap(change, overlaps):
     base = dict(x=A + 7 * FAR)
     status = rar.lib.ddp_linear_forward(*forward_args(**{**base, **change}))
     refused(status, "overlaps" if overlaps else "not inside a device allocation")
+
+
+def test_linear_tiling():
+    lib, tile, parts = rar.lib, ctypes.c_int32(7), ctypes.c_int32(7)
+    out = ctypes.byref(tile), ctypes.byref(parts)
+    refused(lib.ddp_linear_tiling(0, 1, 1, 1, 0, 0, None, out[1]), "output is NULL")
+    refused(lib.ddp_linear_tiling(0, 1, 1, 1, 0, 0, out[0], None), "output is NULL")
+    refused(lib.ddp_linear_tiling(-1, 1, 1, 1, 0, 0, *out), "direction")
+    refused(lib.ddp_linear_tiling(0, 1, 1, 1, 0, 2, *out), "direct must be")
+    refused(lib.ddp_linear_tiling(0, 1, -1, 1, 0, 1, *out), "M, N and K")
+    refused(lib.ddp_linear_tiling(0, 1, 1, 1, 3, 1, *out), "dtype")
+    assert (tile.value, parts.value) == (0, 0)
+    assert rar.linear_tiling(rar.LINEAR_FORWARD, 1, 4096, 4096, "bf16")[0] == 0
+    for dtype, direct, wide in (("bf16", True, 256), ("bf16", False, 128), ("fp32", True, 128), ("fp32", False, 128)):
+        for direction in range(3):
+            assert rar.linear_tiling(direction, 8192, 8192, 8192, dtype, direct) == (wide, 1)
