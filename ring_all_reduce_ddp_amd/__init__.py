@@ -701,6 +701,8 @@ def _scratch(nbytes, workspace, stream):
             return None, (0, None)
         workspace = _empty(nbytes, torch.uint8, stream)
         return workspace, (nbytes, workspace.data_ptr())
+    if not workspace.is_cuda or not workspace.is_contiguous():   # else it spans more, or less, than its elements
+        raise ValueError("workspace must be a contiguous tensor on the GPU")
     return workspace, (workspace.numel() * workspace.element_size(), workspace.data_ptr())
 
 

@@ -549,3 +549,18 @@ def test_every_tile_over_many_steps(what, dtype, direct, tile, size, in_parts):
     else:
         weight_case(m, n, k, dtype, "fp32", True, True, *layout)
         weight_case(m, n, k, dtype, dtype, False, False, *layout)
+
+
+def test_a_workspace_of_less_memory_than_elements_is_refused():
+    a, b = torch.ones(64, 8192, device="cuda"), torch.ones(64, 8192, device="cuda")
+    need = rar.linear_workspace(rar.LINEAR_FORWARD, 64, 64, 8192, "fp32")
+    whole = torch.zeros(2 * need, dtype=torch.uint8, device="cuda")
+    for bad in (whole[:1].expand(need), whole[::2], torch.empty(need, dtype=torch.uint8)):
+        with pytest.raises(ValueError, match="workspace must be"):
+            rar.linear_forward(a, b, workspace=bad)
+        with pytest.raises(ValueError, match="workspace must be"):
+            rar.linear_backward_input(a[:, :64].contiguous(), b, workspace=bad)
+        with pytest.raises(ValueError, match="workspace must be"):
+            rar.linear_backward_weight(a, b, torch.ones(8192, 8192, device="cuda"), workspace=bad)
+    assert not bool(whole.any())
+    assert bool((rar.linear_forward(a, b, workspace=whole[:need]) == 8192).all())
