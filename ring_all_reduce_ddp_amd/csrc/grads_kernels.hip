@@ -215,12 +215,11 @@ void launch_clip(const ddp_grads* g, const ddp_grads* into, float max_norm, cons
   // gradients that the norm has just read (25.6M fp32, 102 MB: both 51 us
   // against 62; whoever reads the result next pays 2 us of it back); loads, and
   // stores in place, from the Infinity Cache's size on.
-  if (g->total * (elem_bytes(SRC) + elem_bytes(DST)) > kInfinityCacheBytes)
-    launch(k_grads_clip<SRC, DST, true, true>);
-  else if (into != g)
-    launch(k_grads_clip<SRC, DST, false, true>);
-  else
-    launch(k_grads_clip<SRC, DST, false, false>);
+  if (g->total * (elem_bytes(SRC) + elem_bytes(DST)) > kInfinityCacheBytes) return launch(k_grads_clip<SRC, DST, true, true>);
+  if constexpr (SRC == DST) {
+    if (into == g) return launch(k_grads_clip<SRC, DST, false, false>);
+  }
+  launch(k_grads_clip<SRC, DST, false, true>);
 }
 
 // The sets' tensors against each other: at once if the sets lie apart as
