@@ -208,3 +208,16 @@ def test_a_norm_inside_the_state_is_refused():
     assert int(t) == 0 and bool((p == 1).all())
     opt.step(max_norm=1.0, norm=g[3], **OPT)   # the gradients are only read
     assert int(t) == 1
+
+
+@pytest.mark.parametrize("copy", [False, True])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_step_beyond_the_cache(dtype, copy):
+    """More than the Infinity Cache (256 MiB) of gradients and state: every access is streamed."""
+    numels = [20_000_003, 511, 3, 5_000_001]
+    decay = [True, False, True, False]
+    s, opt = make(numels, dtype, 1, steps=41, copy=copy, decay=decay)
+    want = step64(opt, OPT, min(1.0, 0.01 / (norm64(s.tensors) + 1e-6)), 42, decay)
+    opt.step(max_norm=0.01, norm=s.norm(), **OPT)
+    check(opt, want)
+    assert int(opt.steps) == 42

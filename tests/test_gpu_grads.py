@@ -279,3 +279,43 @@ def test_a_norm_inside_what_is_written_is_refused():
     s.clip(1.0, big[45], into=into)   # among the gradients, which are only read
     f = 1 / (1 + 1e-6)
     assert ((into.tensors[0].double() - f).abs() <= 5 * U).all() and ((into.tensors[1].double() - f).abs() <= 5 * U).all()
+
+
+# more than the Infinity Cache (256 MiB) in either type, with odd starts and ends
+BEYOND_THE_CACHE = [70_000_001, 8191, 70_000_003, 5]
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_norm_beyond_the_cache(dtype):
+    """Both norms' streamed loads."""
+    _, ts = tensors_of(BEYOND_THE_CACHE, dtype, 14, 1)
+    s = rar.GradSet(ts)
+    want = norm64(ts)
+    assert abs(float(s.norm()) - want) <= (U + 1e-12) * want
+    assert float(s.norm("max")) == max(float(t.abs().max()) for t in ts)
+
+
+@pytest.mark.parametrize("pair", [("fp32", "fp32"), ("fp32", "bf16"), ("bf16", "fp32"), ("bf16", "bf16")])
+def test_clip_into_beyond_the_cache(pair):
+    _, ts = tensors_of(BEYOND_THE_CACHE, pair[0], 15, 1)
+    arena, into = tensors_of(BEYOND_THE_CACHE, pair[1], 16, 2)
+    outside = [arena[:2].clone(), arena[2 + sum(BEYOND_THE_CACHE):].clone()]
+    s, d = rar.GradSet(ts), rar.GradSet(into)
+    norm = s.norm()
+    s.clip(0.01, norm, into=d)
+    check_clipped(into, ts, float(norm), 0.01, pair[1])
+    assert torch.equal(arena[:2], outside[0]) and torch.equal(arena[2 + sum(BEYOND_THE_CACHE):], outside[1])
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_clip_in_place_beyond_the_cache(dtype):
+    _, ts = tensors_of(BEYOND_THE_CACHE, dtype, 17, 1)
+    before = [t.clone() for t in ts]
+    s = rar.GradSet(ts)
+    norm = s.norm()
+    s.clip(0.01, norm)
+    check_clipped(ts, before, float(norm), 0.01, dtype)
+    for t, b in zip(ts, before):
+        t.copy_(b)
+    s.clip(1e4, norm)
+    assert all(torch.equal(t, b) for t, b in zip(ts, before))

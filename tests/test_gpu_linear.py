@@ -564,3 +564,13 @@ def test_a_workspace_of_less_memory_than_elements_is_refused():
             rar.linear_backward_weight(a, b, torch.ones(8192, 8192, device="cuda"), workspace=bad)
     assert not bool(whole.any())
     assert bool((rar.linear_forward(a, b, workspace=whole[:need]) == 8192).all())
+
+
+@pytest.mark.parametrize("grads", ["fp32", "bf16"])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_bias_gradient_of_a_layer_without_inputs(accumulate, grads):
+    """bf16 rows of dz summed without a product; whole numbers, so exact."""
+    dz = torch.randint(-3, 4, (37, 130), device="cuda").to(torch.bfloat16)
+    db = torch.full((130,), 2.0, device="cuda").to(DT[grads])
+    rar.linear_backward_weight(dz, dz[:, :0], torch.empty(130, 0, dtype=DT[grads], device="cuda"), db, accumulate=accumulate)
+    assert torch.equal(db.float(), dz.float().sum(0) + (2.0 if accumulate else 0.0))
