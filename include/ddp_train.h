@@ -44,7 +44,10 @@ extern "C" {
  *   elements (one entry at least per tensor that is not empty) and 17 KiB of scratch are
  *   allocated there. The tensors must stay allocated while the set exists.
  *   Calls on one set share its scratch: they must be ordered (one stream, or
- *   streams that wait for each other). */
+ *   streams that wait for each other). Creating a set asks the runtime about every
+ *   tensor, allocates and copies, and waits for it: some 100 us, which is more than the
+ *   calls of a step on a small set take. A set is made once, not every step; the same
+ *   goes for ddp_adamw_create. */
 typedef struct ddp_grads ddp_grads;
 int ddp_grads_create(void* const* grads, const int64_t* numels, int32_t n, int32_t dtype, ddp_grads** out);
 
@@ -69,7 +72,8 @@ int ddp_grads_norm(ddp_grads* grads, int32_t kind, float* norm_dev, void* stream
  * read when the launch runs: the value of ddp_grads_norm on the same stream, or one
  * combined from several sets' by the caller; it lies in none of the tensors that
  * are written. A NaN norm gives NaN gradients;
- * an infinite one gives f = 0. max_norm >= 0 (infinity: never clip a finite norm). */
+ * an infinite one gives f = 0 (NaN if max_norm is infinite too). max_norm >= 0
+ * (infinity: never clip a finite norm). */
 int ddp_grads_clip(const ddp_grads* grads, const ddp_grads* into, float max_norm, const float* norm_dev,
                    void* stream);
 

@@ -21,11 +21,13 @@
 // What bounds it: a 256 x 256 tile's step of bf16 is 2048 cycles of the matrix
 // instructions and, at 128 bytes a cycle, 2031 of LDS (196 KB read by 8 waves,
 // 64 KB written), so the two have to overlap throughout, and a wave's other
-// instructions have to fit between its products. Measured, 8192 x 2048 x 8192
-// on random data: forward 204 us (1350 TFLOP/s), weight gradient 210, input
-// gradient to 8192 x 2048 203; a 256 x 256 tile's outputs take 7 to 15 us more,
-// in which its CU multiplies nothing. Power takes part of it: on zeros the same
-// products run a fifth faster. fp32: 150 TFLOP/s, the instructions' rate.
+// instructions have to fit between its products. Measured, 8192 rows, 8192
+// inputs and 2048 outputs on random data: forward 202 us (1360 TFLOP/s), weight
+// gradient 208 (216 added to fp32 gradients, 221 with the bias's); input gradient of
+// the layer with inputs and outputs exchanged 202; a 256 x 256 tile's outputs take
+// 7 to 15 us more, in which its CU multiplies nothing. Power takes part of it: on
+// zeros the same products run a fifth faster. fp32: 148 TFLOP/s at 4096 x 4096 x
+// 4096 in all directions, the instructions' rate.
 #include <algorithm>
 #include <cmath>
 #include <new>
@@ -840,8 +842,8 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
 // Joins the parts of every sum, in their order, and finishes the outputs. What
 // the outputs need, and four parts at a time, are loaded before they are used: a
 // launch has two blocks per CU or fewer, which hide little latency (257 x 640
-// weight gradient: 4.0 us against 6.5 a part at a time; 1037 x 1023 forward, 38
-// MB with its outputs: 8.8, near the memory's rate either way).
+// weight gradient: 4.0 us against 6.5 a part at a time; 1037 x 1023 forward in 7
+// parts, 42 MB with residual and outputs: 9 either way).
 template <int DT, int DIR>
 __global__ __launch_bounds__(kThreads) void k_linear_join(LinearArgs g) {
   const int64_t jv = (g.J + 7) / 8;
@@ -896,8 +898,10 @@ __global__ __launch_bounds__(kThreads) void k_column_sums(const void* src, int64
 // is read once and each value meets every row's, so the bound is w's bytes. A
 // block takes 4 rows of w, its waves every fourth kilobyte of each; x stays in
 // the caches. (1 row, 8192 x 2048 bf16: 6 us, 5.6 TB/s with w in the Infinity
-// Cache, against 15 in 128 x 128 tiles; 8 rows took 40 this way and 19 in
-// tiles.)
+// Cache. The whole call, without and with tiles: 1 and 2 rows 7.0 us and 10.4
+// there, 7.0 and 10.8 at 4096 x 4096, fp32 12 and 26. 4 rows gain where outputs are
+// few, 9.9 and 14.0 at 2048 x 8192, fp32 16 and 26 at 4096 x 4096, and lose where
+// they are many, 16.5 and 10.5 at 8192 x 2048, 50 and 12.5 at 32000 x 1024.)
 constexpr int kFewRows = 4, kFewOuts = 4;
 
 // V = 16 / element size values of a row from k on, zeros past K.
@@ -1192,12 +1196,16 @@ int launch_product(LinearArgs& g, void* workspace, bool want_rows, hipStream_t s
     }
   }
   // z waits for the backward pass, the rest of what the call touches does not:
-  // where all of it is much for the Infinity Cache, z leaves it to y (a layer
-  // and the one after it, rows x inputs x outputs and back, with z cached and
-  // streamed: 8192 x 2048 x 8192 512 and 467 us, 8192 x 1536 x 6144, 244 MB, 327
-  // and 293, 4096 x 2048 x 8192, 184 MB, 275 and 257; 8192 x 1024 x 4096, 159
-  // MB, 143 and 144, with their backward pass 480 and 484; 4096 x 1024 x 4096
-  // 88.3 and 88.7). C streamed too is read back too slowly: 487, 325, 267.
+  // where all of it is much for the Infinity Cache, z leaves it to y. A layer and
+  // the one after it, rows x inputs x outputs and back, with z cached and streamed,
+  // forward and, in brackets, with the backward pass, which reads z from further away:
+  // 8192 x 2048 x 8192 512 and 467 us (1501 and 1485), 8192 x 1536 x 6144, 244 MB,
+  // 327 and 293 (1047 and 1025), 4096 x 2048 x 8192, 184 MB, 275 and 257 (830 and
+  // 818), 16384 x 1024 x 4096 284 and 267 (876 and 865). At 159 MB, 8192 x 1024 x
+  // 4096, nothing is gained: 144 and 144 (480 and 484). C streamed too is better
+  // for the whole step at some sizes (1464, 862; 476 at 159 MB) and worse at others
+  // (1044; 8 to 10 % at 4096 x 1024 x 4096 and 8192 x 512 x 2048), and the forward
+  // pass by itself is slower with it: 487, 325, 267, 281.
   if (DIR == DDP_LINEAR_FORWARD && g.z != nullptr)
     g.stream_z = (g.I * g.K + g.J * g.K + g.I * g.J * (g.e != nullptr ? 3 : 2)) * elem_bytes(DT) > kInfinityCacheBytes / 3 * 2;
   g.parts = c.parts;
