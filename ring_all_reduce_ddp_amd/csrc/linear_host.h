@@ -1,0 +1,183 @@
+// Host side of the products (linear_device.h): how they are cut and launched,
+// and the checks of their arguments.
+#pragma once
+
+#include <algorithm>
+#include <cmath>
+#include <string>
+
+#include "linear_device.h"
+
+namespace ddp {
+namespace {
+
+int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+
+// `blocks` blocks in launches of kMaxGrid at most: launch(first block, grid).
+template <class F>
+void launch_blocks(int64_t blocks, F&& launch) {
+  for (int64_t b = 0; b < blocks; b += kMaxGrid) launch(b, dim3(unsigned(std::min(blocks - b, kMaxGrid))));
+}
+
+// Up to so many rows a forward product goes without tiles (linear_kernels.hip).
+constexpr int kFewRows = 4;
+
+// How a product is cut: the tile's side (256 needs direct loads), and in how
+// many parts the sum. Up to kFewRows rows of a forward product go without
+// tiles.
+struct Cut {
+  bool few = false;
+  int tile = 128;
+  int32_t parts = 1;
+  int64_t part_k = 0;
+};
+
+// The cut with the least time by a rough model in cycles. Its constants were
+// fitted to the times of 250 products of 5 to 8192 rows, 64 to 8192 columns
+// and terms, odd and even, on MI355X, each cut in up to 27 ways: the cut it
+// picks takes 1.9 % longer than the best of them in the mean, 31 % at worst.
+// A tile's step (128 bytes of k) takes `step` cycles of a CU that its blocks
+// fill and `alone` of a block by itself, its outputs `ends`; parts cost a
+// launch, a round each, and their bytes.
+Cut cut_by_model(int dir, int32_t I, int32_t J, int32_t K, int dtype, bool direct) {
+  Cut best;
+  if (dir == DDP_LINEAR_FORWARD && I <= kFewRows) {
+    best.few = true;
+    return best;
+  }
+  struct Shape {
+    int32_t tile, fit;  // `fit` blocks share a CU
+    float step, alone, ends;
+  };
+  static const Shape shapes[2][2][3] = {
+      // fp32: loads at any alignment, direct loads
+      {{{64, 5, 1160, 1880, 1500}, {128, 2, 3840, 4670, 5400}, {}}, {{64, 5, 1050, 1140, 1230}, {128, 2, 3920, 3700, 2970}, {}}},
+      // bf16
+      {{{64, 5, 620, 1150, 1050}, {128, 2, 1850, 2040, 3350}, {}},
+       {{64, 5, 440, 850, 2190}, {128, 2, 920, 1010, 4340}, {256, 1, 2100, 2290, 10160}}}};
+  constexpr float kStart = 2000, kJoin = 13100, kPart = 320, kBytesPerCycle = 3160;
+  constexpr int32_t kCus = 256;
+  const auto up = [](int64_t a, int64_t b) { return int32_t((a + b - 1) / b); };
+  const int32_t row = std::min(a_along(dir) ? K : I, b_along(dir) ? K : J);  // the operands' shorter rows
+  const int n_shapes = row < 16 / elem_bytes(dtype) ? 1 : dtype == DDP_BF16 && direct ? 3 : 2;
+  const int32_t step = 128 / elem_bytes(dtype), steps = std::max(1, up(K, step));
+  float least = INFINITY;
+  for (int k = 0; k < n_shapes; ++k) {
+    const Shape& sh = shapes[dtype == DDP_BF16][direct][k];
+    const int64_t tiles = int64_t(up(I, sh.tile)) * up(J, sh.tile);
+    for (int32_t want : {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 28, 32}) {
+      if (want > 1 && (want > steps / 2 || tiles * want > 4 * kCus * sh.fit)) break;
+      const int32_t per = up(steps, want), parts = up(steps, per), on_cu = up(tiles * parts, kCus);
+      float t = std::max(float(up(on_cu, sh.fit)) * (kStart + float(per) * sh.alone),
+                         kStart + float(on_cu) * (float(per) * sh.step + sh.ends));
+      if (parts > 1) t += kJoin + float(parts) * kPart + float(parts + 2) * float(I) * float(J) * (4 / kBytesPerCycle);
+      if (t >= least) continue;
+      least = t;
+      best.tile = sh.tile;
+      best.parts = parts;
+      best.part_k = int64_t(per) * step;
+    }
+  }
+  return best;
+}
+
+// The same, remembered per thread for the sizes seen last: the model takes a
+// microsecond or two, and a call asks it three times.
+Cut cut_of(int dir, int64_t I, int64_t J, int64_t K, int dtype, bool direct) {
+  struct Seen {
+    int64_t key[4] = {-1, -1, -1, -1};
+    Cut cut;
+  };
+  static thread_local Seen seen[64];
+  const int64_t key[4] = {I, J, K, dir * 4 + dtype * 2 + int(direct)};
+  const uint64_t h = (uint64_t(I) * 31 + uint64_t(J) * 7 + uint64_t(K)) * 8 + uint64_t(key[3]);
+  Seen& s = seen[(h ^ (h >> 7)) % 64];
+  if (!std::equal(key, key + 4, s.key)) {
+    s.cut = cut_by_model(dir, int32_t(I), int32_t(J), int32_t(K), dtype, direct);
+    std::copy(key, key + 4, s.key);
+  }
+  return s.cut;
+}
+
+int64_t partial_bytes(const Cut& c, int64_t I, int64_t J) {
+  return c.parts > 1 ? round_up(int64_t(c.parts) * I * round_up(J, 8) * 4, 256) : 0;
+}
+
+// A matrix argument: rows x cols, leading dimension ld, NULL where allowed.
+struct Matrix {
+  const void* p;
+  int64_t rows, cols, ld;
+  int eb;
+  const char* what;
+  bool written;
+  bool may_be_null;
+  int64_t bytes() const { return rows > 0 && cols > 0 ? ((rows - 1) * ld + cols) * eb : 0; }
+};
+
+// Whether two matrices share a byte. Of one pitch (or one of them a single
+// row, which has none), they may lie side by side as column blocks.
+bool matrices_overlap(const Matrix& a, const Matrix& b) {
+  if (!spans_overlap(a.p, a.bytes(), b.p, b.bytes())) return false;
+  if (a.rows == 1 && b.rows == 1) return true;
+  const uint64_t pa = uint64_t(a.ld) * a.eb, pb = uint64_t(b.ld) * b.eb;
+  if (a.rows > 1 && b.rows > 1 && pa != pb) return true;
+  const uint64_t pitch = a.rows > 1 ? pa : pb;
+  const uint64_t wa = uint64_t(a.cols) * a.eb, wb = uint64_t(b.cols) * b.eb;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  const uint64_t ahead = y >= x ? (y - x) % pitch : (pitch - (x - y) % pitch) % pitch;  // of b's columns, before a's begin again
+  return ahead < wa || ahead + wb > pitch;
+}
+
+// Every matrix lies in its allocation, and what is written overlaps nothing
+// else, except that matrix `in_place` may be matrix `out` (the same place and rows).
+int check_matrices(const char* fn, const Matrix* m, int n, int in_place, int out) {
+  for (int k = 0; k < n; ++k) {
+    const Matrix& x = m[k];
+    if (x.p == nullptr && x.may_be_null) continue;
+    if (x.ld < x.cols) return fail(DDP_EINVAL, std::string(fn) + ": the leading dimension of " + x.what + " is less than its columns");
+    if (x.rows > 1 && x.ld > (int64_t(1) << 30))  // so that bytes() fits 63 bits
+      return fail(DDP_EINVAL, std::string(fn) + ": the leading dimension of " + x.what + " is over 2^22");
+    if (x.bytes() == 0) continue;
+    if (x.p == nullptr) return fail(DDP_EINVAL, std::string(fn) + ": " + x.what + " is NULL");
+    if (reinterpret_cast<uintptr_t>(x.p) % uintptr_t(x.eb) != 0)
+      return fail(DDP_EINVAL, std::string(fn) + ": " + x.what + " is not aligned to its element");
+  }
+  for (int k = 0; k < n; ++k) {
+    if (!m[k].written || m[k].p == nullptr) continue;
+    for (int o = 0; o < n; ++o) {
+      if (o == k || m[o].p == nullptr) continue;
+      if (k == out && o == in_place && m[o].p == m[k].p && m[o].ld == m[k].ld) continue;
+      if (matrices_overlap(m[k], m[o]))
+        return fail(DDP_EINVAL, std::string(fn) + ": " + m[k].what + " overlaps " + m[o].what);
+    }
+  }
+  for (int k = 0; k < n; ++k) {  // asks the runtime, so last
+    if (m[k].p == nullptr) continue;
+    int st = check_range(m[k].p, m[k].bytes(), fn, m[k].what);
+    if (st != DDP_OK) return st;
+    if (m[k].rows > 1 && m[k].ld > (int64_t(1) << 22))  // offsets within a tile are 32 bits wide
+      return fail(DDP_EINVAL, std::string(fn) + ": the leading dimension of " + m[k].what + " is over 2^22");
+  }
+  return DDP_OK;
+}
+
+int check_common(const char* fn, int64_t M, int64_t N, int64_t K, int32_t dtype, int32_t act) {
+  if (!valid_dtype(dtype)) return fail(DDP_EINVAL, std::string(fn) + ": unknown dtype");
+  if (act < DDP_ACT_NONE || act > DDP_ACT_SILU) return fail(DDP_EINVAL, std::string(fn) + ": unknown activation");
+  const int64_t most = int64_t(1) << 31;  // sums and rows are counted in 32 bits
+  if (M < 0 || N < 0 || K < 0 || M >= most || N >= most || K >= most)
+    return fail(DDP_EINVAL, std::string(fn) + ": M, N and K must lie in [0, 2^31)");
+  return DDP_OK;
+}
+
+int check_workspace(const char* fn, const void* p, int64_t have, int64_t need) {
+  if (need == 0) return DDP_OK;
+  if (p == nullptr || have < need)
+    return fail(DDP_EINVAL, std::string(fn) + ": the workspace needs " + std::to_string(need) + " bytes");
+  if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return fail(DDP_EINVAL, std::string(fn) + ": the workspace is not 16-byte aligned");
+  return DDP_OK;
+}
+
+}  // namespace
+}  // namespace ddp
