@@ -1,8 +1,9 @@
 /*
  * ddp_train.h -- C ABI of the operators around the gradient sync of
  * ddp_ring.h, on the same MI355X (gfx950): what makes the gradients where the
- * sync reads them (a linear layer and its gradients), and what reads them
- * after it (the global gradient norm, clipping, an AdamW step).
+ * sync reads them (linear layers, of experts too, and the losses of an output
+ * layer, with their gradients), and what reads them after it (the global
+ * gradient norm, clipping, an AdamW step).
  *
  * In the step of "DDP 与 Ring All-Reduce" (blog.vllbc.top), section 05, the
  * layer is step 2 (backward produces the gradients, whose hooks mark them
@@ -188,6 +189,45 @@ int ddp_linear_backward_weight(const void* dz, int64_t lddz, const void* x, int6
  * ddp_linear_backward_input. dz may be dy. */
 int ddp_act_backward(const void* dy, int64_t lddy, const void* z, int64_t ldz, void* dz, int64_t lddz,
                      int64_t M, int64_t N, int32_t dtype, int32_t act, void* stream);
+
+/* ---------------------------------------------------------------- experts
+ * Linear layers of E experts over T rows sorted by expert: expert e has the
+ * rows offsets[e] <= i < offsets[e + 1] of x, y, z, dz and dx, its weights are
+ * rows e N .. (e + 1) N - 1 of w[E * N][K], its bias is bias[e * N ..], its
+ * gradients lie likewise in dw and db. Matrices, types, activations and sums
+ * are those of the linear layer above.
+ * offsets[E + 1] are int64 on the device, read when the launch runs: nothing
+ * waits for the host. Each counts as the largest one up to it, within [0, T],
+ * so an expert whose offsets do not ascend has no rows, and no row has two
+ * experts. Rows before the first offset and from the last one on belong to
+ * nobody: they are neither read nor written. An expert without rows gets
+ * zero gradients.
+ * 1 <= E <= 65536, K >= 1, T, N and K below 2^31, E * N below 2^31.
+ *
+ * ddp_experts_workspace: bytes of scratch on the current device that a
+ * direction (DDP_LINEAR_*) needs: 0 but for the weight gradient, whose
+ * call takes it under the same conditions as ddp_linear_backward_weight. */
+int ddp_experts_workspace(int32_t direction, int64_t T, int64_t E, int64_t N, int64_t K, int32_t dtype, int64_t* bytes);
+
+/* y_i = act(x_i w_e^T + bias_e); z (NULL: not kept) receives the rounded
+ * argument of act. bias may be NULL. */
+int ddp_experts_forward(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias, const int64_t* offsets,
+                        void* y, int64_t ldy, void* z, int64_t ldz, int64_t T, int64_t E, int64_t N, int64_t K,
+                        int32_t dtype, int32_t act, void* stream);
+
+/* dx_i = (dz_i w_e) * act'(z_i), z[T][K] kept by the layer before (NULL: no
+ * activation, `act` must be DDP_ACT_NONE). */
+int ddp_experts_backward_input(const void* dz, int64_t lddz, const void* w, int64_t ldw, const int64_t* offsets,
+                               const void* z, int64_t ldz, void* dx, int64_t lddx, int64_t T, int64_t E, int64_t N,
+                               int64_t K, int32_t dtype, int32_t act, void* stream);
+
+/* dw_e = sum of dz_i^T x_i, db_e = sum of dz_i over the expert's rows (db
+ * NULL: not wanted), of grad_dtype (`dtype`, or fp32 gradients of bf16 data),
+ * overwriting or, with accumulate = 1, added to what is there. */
+int ddp_experts_backward_weight(const void* dz, int64_t lddz, const void* x, int64_t ldx, const int64_t* offsets, void* dw,
+                                int64_t lddw, void* db, int64_t T, int64_t E, int64_t N, int64_t K, int32_t dtype,
+                                int32_t grad_dtype, int32_t accumulate, void* workspace, int64_t workspace_bytes,
+                                void* stream);
 
 #ifdef __cplusplus
 }

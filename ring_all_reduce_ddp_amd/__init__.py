@@ -110,6 +110,11 @@ def _load():
                                                      i32, i32, vp, i64, vp]),
         "ddp_linear_backward_weight": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i32, i32, i32,
                                                       vp, i64, vp]),
+        "ddp_experts_workspace": (ctypes.c_int, [i32, i64, i64, i64, i64, i32, ctypes.POINTER(i64)]),
+        "ddp_experts_forward": (ctypes.c_int, [vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, i64, i64, i64, i64, i32, i32, vp]),
+        "ddp_experts_backward_input": (ctypes.c_int, [vp, i64, vp, i64, vp, vp, i64, vp, i64, i64, i64, i64, i64, i32, i32, vp]),
+        "ddp_experts_backward_weight": (ctypes.c_int, [vp, i64, vp, i64, vp, vp, i64, vp, i64, i64, i64, i64, i32, i32, i32,
+                                                       vp, i64, vp]),
         "ddp_act_backward": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, i64, i64, i32, i32, vp]),
     }
     for name, (res, args) in sig.items():
@@ -775,3 +780,90 @@ def act_backward(dy, z, act, out=None, stream=None):
     op, ldo = _matrix(dz, m, n, dt, "out")
     _check(_get_lib().ddp_act_backward(yp, ldy, zp, ldz, op, ldo, m, n, dtype_code(dt), ACTIVATIONS[act], _stream(stream)))
     return dz
+
+
+def _offsets(t, n, what="offsets"):
+    if not t.is_cuda or t.dtype != torch.int64 or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous vector of {n} int64 on the GPU")
+    return t.data_ptr()
+
+
+def _expert_matrices(t, e, n, k, dtype, what):
+    """(pointer, leading dimension) of e matrices n x k whose rows follow each other at one pitch."""
+    if t.dtype is not dtype or t.shape != (e, n, k) or not t.is_cuda:
+        raise ValueError(f"{what} must be {e} matrices {n} x {k} of {dtype} on the GPU")
+    group, ld, step = t.stride()
+    if (step != 1 and k > 1) or (e > 1 and n > 1 and group != n * ld):
+        raise ValueError(f"the rows of {what} must be contiguous and evenly spaced")
+    if n <= 1:
+        ld = group if e > 1 else max(k, 1)
+    return t.data_ptr(), ld
+
+
+def _expert_vectors(t, e, n, dtype, what):
+    if t is None:
+        return None
+    if not t.is_cuda or t.shape != (e, n) or not t.is_contiguous() or t.dtype != dtype:
+        raise ValueError(f"{what} must be a contiguous {e} x {n} matrix of {dtype} on the GPU")
+    return t.data_ptr()
+
+
+@functools.lru_cache(maxsize=4096)
+def _experts_workspace(direction, t, e, n, k, code):
+    b = ctypes.c_int64()
+    _check(_get_lib().ddp_experts_workspace(direction, t, e, n, k, code, ctypes.byref(b)))
+    return b.value
+
+
+def experts_forward(x, w, offsets, bias=None, act="none", keep=False, out=None, z=None, stream=None):
+    """act(x_i w_e^T + bias_e) over rows sorted by expert: expert e has the rows
+    offsets[e] to offsets[e + 1] (int64, on the GPU) of x and the matrix w[e].
+    With keep=True (or a matrix z to fill) the pair (y, z). Rows of no expert
+    stay as they are in out and z, and are undefined in new ones (see
+    ddp_experts_forward in include/ddp_train.h)."""
+    t, k = x.shape
+    e, n = w.shape[0], w.shape[1]
+    dt = x.dtype
+    code = dtype_code(dt)
+    y = _result(out, t, n, dt, stream)
+    if keep and z is None:
+        z = _result(None, t, n, dt, stream)
+    xp, ldx = _matrix(x, t, k, dt, "x")
+    wp, ldw = _expert_matrices(w, e, n, k, dt, "w")
+    yp, ldy = _matrix(y, t, n, dt, "out")
+    zp, ldz = _matrix(z, t, n, dt, "z")
+    _check(_get_lib().ddp_experts_forward(xp, ldx, wp, ldw, _expert_vectors(bias, e, n, dt, "bias"), _offsets(offsets, e + 1),
+                                          yp, ldy, zp, ldz, t, e, n, k, code, ACTIVATIONS[act], _stream(stream)))
+    return y if z is None else (y, z)
+
+
+def experts_backward_input(dz, w, offsets, act="none", z=None, out=None, stream=None):
+    """(dz_i w_e) * act'(z_i) (see ddp_experts_backward_input)."""
+    t, n = dz.shape
+    e, k = w.shape[0], w.shape[2]
+    dt = dz.dtype
+    dx = _result(out, t, k, dt, stream)
+    gp, ldg = _matrix(dz, t, n, dt, "dz")
+    wp, ldw = _expert_matrices(w, e, n, k, dt, "w")
+    zp, ldz = _matrix(z, t, k, dt, "z")
+    op, ldo = _matrix(dx, t, k, dt, "out")
+    _check(_get_lib().ddp_experts_backward_input(gp, ldg, wp, ldw, _offsets(offsets, e + 1), zp, ldz, op, ldo, t, e, n, k,
+                                                 dtype_code(dt), ACTIVATIONS[act], _stream(stream)))
+    return dx
+
+
+def experts_backward_weight(dz, x, offsets, dw, db=None, accumulate=False, workspace=None, stream=None):
+    """dw[e] (+)= dz_i^T x_i and db[e] (+)= dz_i, summed over each expert's
+    rows, into tensors of the data's dtype or float32, e.g. views of a gradient
+    arena (see ddp_experts_backward_weight)."""
+    t, n = dz.shape
+    e, k = dw.shape[0], x.shape[1]
+    dt, gt = dz.dtype, dw.dtype
+    code = dtype_code(dt)
+    gp, ldg = _matrix(dz, t, n, dt, "dz")
+    xp, ldx = _matrix(x, t, k, dt, "x")
+    wp, ldw = _expert_matrices(dw, e, n, k, gt, "dw")
+    bp = _expert_vectors(db, e, n, gt, "db")
+    ws, (nbytes, p) = _scratch(_experts_workspace(LINEAR_BACKWARD_WEIGHT, t, e, n, k, code), workspace, stream)
+    _check(_get_lib().ddp_experts_backward_weight(gp, ldg, xp, ldx, _offsets(offsets, e + 1), wp, ldw, bp, t, e, n, k, code,
+                                                  dtype_code(gt), 1 if accumulate else 0, p, nbytes, _stream(stream)))

@@ -5,7 +5,16 @@
 //   input gradient   dx = (dz w) * act'(z) + add
 //   weight gradient  dw (+)= dz^T x,  db (+)= sum of dz's rows
 //
-// All three are C[i][j] = sum_k A(i, k) B(j, k). What differs is how an
+// and, of the other operators that are products,
+
+//   row statistics   of z = x w^T: each row's maximum and sum of exponentials (the losses of an output layer)
+//   row slopes       the loss's gradient with respect to z, from z made again
+//   input pieces     dx += dz w over a piece of dz's columns, kept in fp32 between pieces
+//   weight terms     dw (+)= (dz1 + dz2)^T x, dz in two terms of 16 bits
+//
+// each of the rows of one group or of several (experts) whose bounds are on the device.
+//
+// All are C[i][j] = sum_k A(i, k) B(j, k). What differs is how an
 // operand lies in memory: with the sum's index k contiguous ("along": x and w
 // in the forward product), or with k going from row to row ("across": w in
 // the input gradient, both operands of the weight gradient).
@@ -43,6 +52,26 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 #define DDP_LDS __attribute__((address_space(3)))
 
+// What the losses of an output layer need besides the product. Rows are those
+// of the caller; the product has only those that count.
+struct HeadArgs {
+  float scale;             // z = scale * x w^T
+  float slope;             // row slopes: dz = slope * dloss * (p - q)
+  int64_t vocabulary;
+  int64_t j_base;          // the piece's first column, a multiple of the tile
+  const int64_t* targets;  // a row's target; or NULL, and its entries:
+  int32_t top;             // as many a row at most (1 with targets)
+  int32_t tiles;           // column tiles of the vocabulary
+  const int32_t* ids;      // [row][top], ascending, each once
+  const float* weights;    // [row][top]
+  const uint16_t* starts;  // [row][tiles + 1], the first entry of a column tile or a later one
+  const float* own_terms;  // [row], NaN where an entry is not valid
+  float* stats;            // row statistics: [column tile][2][compact row]: maximum, sum of exp(z - maximum)
+  float* picked;           // row statistics: [row][top], z of the entries
+  const float* lse;        // row slopes: [row]
+  const float* dloss;      // row slopes: [row]
+};
+
 struct LinearArgs {
   const void* a;    // operand of the rows of C
   const void* b;    // operand of the columns of C
@@ -65,10 +94,30 @@ struct LinearArgs {
   float* row_sums;     // weight gradient: [part * tiles_j + tile_j][I], sums of A's rows (NULL: not wanted)
   int32_t tiles_i, tiles_j;
   int32_t begin;    // the launch's first block
+
+  // Groups: group e has the rows bounds[e] .. bounds[e + 1] of x and dz, and
+  // its own w, bias, dw and db, one after the other's.
+  const int64_t* bounds;  // groups + 1, on the device
+  int32_t groups;
+  int64_t rows;           // of x and dz: no bound counts beyond them
+  int64_t b_group;        // elements from one group's w to the next one's
+
+  // Operands with room behind their rows, which holds zeros.
+  int32_t a_room, b_room;  // elements of it that belong to the last chunk
+  int32_t terms;           // weight terms: 1 or 2
+  int64_t term;            // bytes from A's first term to its second, or elements of C (row slopes)
+  float* sums;             // input pieces: the sum over pieces, fp32 (NULL: one piece)
+  int32_t first, last;     // input pieces: whether this is the first, the last piece
+  const int32_t* row_of;   // where the compact rows come from
+  HeadArgs head;
 };
 
-constexpr bool a_along(int dir) { return dir != DDP_LINEAR_BACKWARD_WEIGHT; }
-constexpr bool b_along(int dir) { return dir == DDP_LINEAR_FORWARD; }
+// Products beside the linear layer's three directions.
+constexpr int kRowStats = 3, kRowSlopes = 4, kInputPiece = 5, kWeightTerms = 6;
+constexpr bool is_weight(int dir) { return dir == DDP_LINEAR_BACKWARD_WEIGHT || dir == kWeightTerms; }
+constexpr bool is_head(int dir) { return dir == kRowStats || dir == kRowSlopes; }
+constexpr bool a_along(int dir) { return !is_weight(dir); }
+constexpr bool b_along(int dir) { return dir == DDP_LINEAR_FORWARD || is_head(dir); }
 
 // ---------------------------------------------------------------- activations
 
@@ -244,7 +293,9 @@ struct Extra {
 
 template <int DT, int DIR>
 __device__ __forceinline__ void load_extra(const LinearArgs& g, int64_t i, int64_t j, int n, Extra& x) {
-  if constexpr (DIR == DDP_LINEAR_BACKWARD_WEIGHT) {
+  if constexpr (DIR == kInputPiece) {
+    if (!g.first) x.e = load_raw8<DDP_FP32>(g.sums, i * g.J + j, n);
+  } else if constexpr (is_weight(DIR)) {
     if (g.accumulate) x.e = g.grad32 ? load_raw8<DDP_FP32>(g.c, i * g.ldc + j, n) : load_raw8<DT>(g.c, i * g.ldc + j, n);
   } else {
     if (g.e != nullptr) x.e = load_raw8<DT>(g.e, i * g.lde + j, n);
@@ -258,7 +309,12 @@ template <int DT, int DIR, int ACT>
 __device__ __forceinline__ void before_store(const LinearArgs& g, int64_t i, int64_t j, int n, float v[8], const Extra& x,
                                              const float bias[8]) {
   float e[8];
-  if constexpr (DIR == DDP_LINEAR_BACKWARD_WEIGHT) {
+  if constexpr (DIR == kInputPiece) {
+    if (!g.first) {
+      unpack8<DDP_FP32>(x.e, e);
+      for (int k = 0; k < 8; ++k) v[k] += e[k];
+    }
+  } else if constexpr (is_weight(DIR)) {
     if (g.accumulate) {
       if (g.grad32)
         unpack8<DDP_FP32>(x.e, e);
@@ -286,7 +342,11 @@ __device__ __forceinline__ void before_store(const LinearArgs& g, int64_t i, int
 // ... and the store.
 template <int DT, int DIR>
 __device__ __forceinline__ void store_output(const LinearArgs& g, int64_t i, int64_t j, int n, const float v[8]) {
-  if (DIR == DDP_LINEAR_BACKWARD_WEIGHT && g.grad32)
+  if (DIR == kInputPiece && !g.last)
+    store8<DDP_FP32>(g.sums, i * g.J + j, n, v);
+  else if (DIR == kInputPiece)
+    store8<DT>(g.c, g.row_of[i] * g.ldc + j, n, v);
+  else if (is_weight(DIR) && g.grad32)
     store8<DDP_FP32>(g.c, i * g.ldc + j, n, v);
   else
     store8<DT>(g.c, i * g.ldc + j, n, v);
@@ -399,8 +459,8 @@ constexpr uint32_t kFar = 0xfffffff0u;     // an offset outside every descriptor
 constexpr int32_t kMostRange = 0x0f000000; // of a descriptor, in 16-byte chunks
 
 // Direct loads to LDS, for operands whose every chunk is 16-byte aligned and
-// whole. The descriptor ends with the operand, so a chunk past it reads as
-// zeros; a row of C's side past the operand repeats the last one (its
+// whole (`room` elements behind the last row make its last chunk whole). The
+// descriptor ends with the operand, so a chunk past it reads as zeros; a row of C's side past the operand repeats the last one (its
 // products are not stored).
 template <class TL, bool ALONG, int THREADS>
 struct DirectLoader {
@@ -417,13 +477,13 @@ struct DirectLoader {
     const int q = (n * (THREADS / 64) + wave) * 64 + (int(threadIdx.x) & 63);
     return ALONG ? TL::col_of(q) * TL::V : TL::row_of(q);
   }
-  __device__ __forceinline__ void init(const void* base, int64_t ld, int64_t side, int64_t K, int64_t s0, int64_t k0, int64_t k1) {
+  __device__ __forceinline__ void init(const void* base, int64_t ld, int64_t side, int64_t K, int64_t s0, int64_t k0, int64_t k1, int32_t room) {
     const int lane = int(threadIdx.x) & 63;
     wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const int64_t rows = ALONG ? side : K, cols = ALONG ? K : side;
     const int64_t start = ALONG ? s0 * ld + k0 : k0 * ld + s0;
     p = static_cast<const char*>(base) + start * TL::ES;
-    left = int32_t(((rows - 1) * ld + cols - start) / TL::V);
+    left = int32_t(((rows - 1) * ld + cols + room - start) / TL::V);
     advance = ALONG ? TL::ROW : TL::STEP * ld * TL::ES;
     k_left = int32_t(k1 - k0);
 #pragma unroll
@@ -487,7 +547,7 @@ struct AnyLoader {
   u32x4 x[TL::N];
 
   static __device__ __forceinline__ int chunk(int n) { return n * THREADS + int(threadIdx.x); }
-  __device__ __forceinline__ void init(const void* base, int64_t ld, int64_t side, int64_t, int64_t s0, int64_t k0, int64_t k1) {
+  __device__ __forceinline__ void init(const void* base, int64_t ld, int64_t side, int64_t, int64_t s0, int64_t k0, int64_t k1, int32_t) {
     row_bytes = ld * TL::ES;
     p = static_cast<const char*>(base) + (ALONG ? s0 * ld + k0 : k0 * ld + s0) * TL::ES;
     k_left = int32_t(k1 - k0);
@@ -545,7 +605,7 @@ struct ShortLoader {
   int64_t ld, side, s0, k, k1;
   u32x4 x[TL::N];
 
-  __device__ __forceinline__ void init(const void* b, int64_t ld_, int64_t side_, int64_t, int64_t s0_, int64_t k0, int64_t k1_) {
+  __device__ __forceinline__ void init(const void* b, int64_t ld_, int64_t side_, int64_t, int64_t s0_, int64_t k0, int64_t k1_, int32_t) {
     base = b, ld = ld_, side = side_, s0 = s0_, k = k0, k1 = k1_;
   }
   template <bool FULL>
@@ -576,10 +636,232 @@ using LoaderOf = std::conditional_t<LOAD == kDirect, DirectLoader<TL, ALONG, THR
                                     std::conditional_t<LOAD == kAny, AnyLoader<DT, TL, ALONG, THREADS>,
                                                        ShortLoader<DT, TL, ALONG, THREADS>>>;
 
+// ---------------------------------------------------------------- groups of rows
+
+// The bounds come from the device and are not trusted: each counts as the
+// largest one up to it, within [0, rows]. So groups never overlap, and their
+// tiles never outnumber a launch's blocks.
+__device__ __forceinline__ int32_t bound_at(const LinearArgs& g, int32_t e) {
+  const int64_t b = g.bounds[e];
+  return b < 0 ? 0 : b < g.rows ? int32_t(b) : int32_t(g.rows);
+}
+
+// 64 groups from e0 on, one a lane.
+struct GroupScan {
+  int32_t begin, rows;     // of this lane's group
+  int32_t tiles, until;    // its tiles of T rows; tiles up to and with it
+};
+template <int T>
+__device__ __forceinline__ GroupScan scan_groups(const LinearArgs& g, int32_t e0, int32_t& bound, int32_t& tiles) {
+  const int lane = int(threadIdx.x) & 63;
+  int32_t end = e0 + lane < g.groups ? bound_at(g, e0 + lane + 1) : 0;
+  if (end < bound) end = bound;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int32_t o = __shfl_up(end, d);
+    if (lane >= d && o > end) end = o;
+  }
+  GroupScan s;
+  s.begin = __shfl_up(end, 1);
+  if (lane == 0) s.begin = bound;
+  s.rows = e0 + lane < g.groups ? end - s.begin : 0;
+  s.tiles = (s.rows + T - 1) / T;
+  s.until = s.tiles;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int32_t o = __shfl_up(s.until, d);
+    if (lane >= d) s.until += o;
+  }
+  s.until += tiles;
+  bound = __builtin_amdgcn_readfirstlane(__shfl(end, 63));
+  tiles = __builtin_amdgcn_readfirstlane(__shfl(s.until, 63));
+  return s;
+}
+// Tiles of T rows in all groups.
+template <int T>
+__device__ __forceinline__ int32_t tiles_of_groups(const LinearArgs& g, GroupScan& first) {
+  int32_t bound = bound_at(g, 0), tiles = 0;
+  first = scan_groups<T>(g, 0, bound, tiles);
+  for (int32_t e0 = 64; e0 < g.groups; e0 += 64) scan_groups<T>(g, e0, bound, tiles);
+  return tiles;
+}
+struct Group {
+  int32_t index, begin, rows, tile;  // the group, its rows, and which of its tiles
+};
+// The group of tile number `tile` (below their number).
+template <int T>
+__device__ __forceinline__ Group group_of_tile(const LinearArgs& g, const GroupScan& first, int32_t tile) {
+  int32_t bound = 0, tiles = 0, e0 = 0;
+  GroupScan s = first;
+  uint64_t hit = __ballot(tile < s.until);
+  if (hit == 0) {
+    bound = bound_at(g, 0);
+    scan_groups<T>(g, 0, bound, tiles);
+    do {
+      e0 += 64;
+      s = scan_groups<T>(g, e0, bound, tiles);
+      hit = __ballot(tile < s.until);
+    } while (hit == 0 && e0 + 64 < g.groups);
+  }
+  const int from = hit != 0 ? __builtin_ctzll(hit) : 0;
+  return Group{e0 + from, __builtin_amdgcn_readlane(s.begin, from), __builtin_amdgcn_readlane(s.rows, from),
+               tile - (__builtin_amdgcn_readlane(s.until, from) - __builtin_amdgcn_readlane(s.tiles, from))};
+}
+// Group number e.
+__device__ __forceinline__ Group group_at(const LinearArgs& g, int32_t e) {
+  int32_t bound = bound_at(g, 0), tiles = 0;
+  for (int32_t e0 = 0;; e0 += 64) {
+    const GroupScan s = scan_groups<1>(g, e0, bound, tiles);
+    if (e >= e0 + 64) continue;
+    return Group{e, __builtin_amdgcn_readlane(s.begin, e - e0), __builtin_amdgcn_readlane(s.rows, e - e0), 0};
+  }
+}
+
+// ---------------------------------------------------------------- the losses' outputs
+
+// From a tile of x w^T in registers (lane l: row l & 31, columns 8 q + 4 (l >> 5)
+// + r of each 32 x 32 product), so a row's values lie in two lanes:
+//
+// row statistics: the maximum over the tile's columns and the sum of exp(z -
+// maximum), which need no exchange but with the other half and, in LDS, with
+// the waves beside this one; and z of the row's entries (its target, or the
+// teacher's logits), found through LDS where a wave's columns hold any.
+//
+// row slopes: dz = slope dloss (exp(z - lse) - q), by rows through LDS, where q
+// of the few entries is taken off. bf16: in one or two terms, the second what the
+// first's rounding left, which together are off by 2^-16 of dz at most.
+template <int DT, int DIR, int TI, int TJ, int WI, int WJ>
+__device__ __forceinline__ void head_outputs(const LinearArgs& g, f32x16 (&acc)[TI / WI / 32][TJ / WJ / 32], char* lds, int64_t i0,
+                                             int64_t j0, int wi, int wj, int wave, int lane, int tile_j) {
+  constexpr int FI = TI / WI / 32, FJ = TJ / WJ / 32, THREADS = WI * WJ * 64, PITCH = 32 * FJ + 4;
+  const HeadArgs& h = g.head;
+  const int half = lane >> 5, in = lane & 31;
+  const int width = g.J - j0 - wj < 32 * FJ ? int(g.J - j0 - wj) : 32 * FJ;  // of the wave's columns inside, or less than 0
+  float* const mine = reinterpret_cast<float*>(lds) + wave * 32 * PITCH;
+  float* const stats = reinterpret_cast<float*>(lds) + WI * WJ * 32 * PITCH;  // [WJ][2][TI]
+  const int64_t column = h.j_base + j0;                                       // of the vocabulary, the tile's first
+#pragma unroll
+  for (int a = 0; a < FI; ++a) {
+    const int64_t i = i0 + wi + 32 * a + in;
+    const bool counts = i < g.I;
+    const int64_t row = counts ? g.row_of[i] : 0;
+    // The row's entries in this tile; of a target, `place` is known at once.
+    int entry = 0, entries = 0, place = -1;
+    if (h.targets != nullptr) {
+      const int64_t t = counts ? h.targets[row] - column - wj : -1;
+      if (t >= 0 && t < width) place = int(t), entries = 1;
+    } else if (counts) {
+      const int64_t at = row * (h.tiles + 1) + column / TJ;
+      entry = h.starts[at];
+      entries = h.starts[at + 1] - entry;
+    }
+    const auto place_of = [&](int k) __attribute__((always_inline)) {
+      return h.targets != nullptr ? place : int(h.ids[row * h.top + k] - column - wj);
+    };
+    const auto to_lds = [&] __attribute__((always_inline)) {
+#pragma unroll
+      for (int b = 0; b < FJ; ++b)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<f32x4*>(mine + in * PITCH + 32 * b + 8 * q + 4 * half) =
+              f32x4{acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
+      __builtin_amdgcn_wave_barrier();
+    };
+    // f(value) for every value, `outside` in place of those outside C.
+    const auto each = [&](float outside, auto&& f) __attribute__((always_inline)) {
+      const bool whole = width == 32 * FJ;
+#pragma unroll
+      for (int b = 0; b < FJ; ++b)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float v = f(acc[a][b][e]);
+          acc[a][b][e] = whole || 32 * b + 8 * (e >> 2) + 4 * half + (e & 3) < width ? v : outside;
+        }
+    };
+    if constexpr (DIR == kRowStats) {
+      each(-INFINITY, [&](float v) { return v * h.scale; });
+      float most = -INFINITY, sum = 0.0f;
+#pragma unroll
+      for (int b = 0; b < FJ; ++b)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) most = fmaxf(most, acc[a][b][e]);
+      most = fmaxf(most, __shfl_xor(most, 32));
+      const float base = most == -INFINITY ? 0.0f : most;
+#pragma unroll
+      for (int b = 0; b < FJ; ++b)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sum += exponential<DT>(acc[a][b][e] - base);
+      sum += __shfl_xor(sum, 32);
+      if (half == 0) {
+        stats[(wj / (32 * FJ) * 2 + 0) * TI + wi + 32 * a + in] = most;
+        stats[(wj / (32 * FJ) * 2 + 1) * TI + wi + 32 * a + in] = sum;
+      }
+      if (__any(entries > 0)) {
+        to_lds();
+        for (int k = half; k < entries; k += 2) {
+          const int at = place_of(entry + k);
+          if (at >= 0 && at < width) h.picked[row * h.top + entry + k] = mine[in * PITCH + at];
+        }
+        __builtin_amdgcn_wave_barrier();
+      }
+    } else {
+      float lse = 0.0f, slope = 0.0f;
+      if (counts) {
+        lse = h.lse[row];
+        slope = h.slope * h.dloss[row];
+        // A target or entry outside the vocabulary makes the row NaN.
+        if (h.targets != nullptr ? h.targets[row] >= h.vocabulary : h.own_terms[row] != h.own_terms[row]) lse = NAN;
+      }
+      each(0.0f, [&](float v) { return slope * exponential<DT>(fmaf(v, h.scale, -lse)); });
+      to_lds();
+      for (int k = half; k < entries; k += 2) {
+        const int at = place_of(entry + k);
+        if (at < 0 || at >= width) continue;
+        const float q = h.targets != nullptr ? 1.0f : h.weights[row * h.top + entry + k];
+        mine[in * PITCH + at] = fmaf(-q, slope, mine[in * PITCH + at]);
+      }
+      __builtin_amdgcn_wave_barrier();
+      constexpr int LPR = 4 * FJ, RPP = 64 / LPR;  // lanes per row, rows per pass
+      const int c = lane % LPR * 8;
+#pragma unroll
+      for (int p = 0; p < 32 / RPP; ++p) {
+        const int r = p * RPP + lane / LPR;
+        const float* src = mine + r * PITCH + c;
+        const int64_t to = i0 + wi + 32 * a + r;
+        float v[8], rest[8];
+        for (int k = 0; k < 8; ++k) v[k] = src[k];
+        if (to >= g.I || c >= width) continue;  // a row's last chunk is written whole, with zeros
+        const int64_t at = to * g.ldc + j0 + wj + c;
+        store_all8<DT, false>(g.c, at, v);
+        if (DT == DDP_BF16 && g.terms > 1) {
+          for (int k = 0; k < 8; ++k) rest[k] = v[k] - round_bf16(v[k]);
+          store_all8<DT, false>(g.c, g.term + at, rest);
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+  if constexpr (DIR == kRowStats) {
+    __syncthreads();
+    for (int r = int(threadIdx.x); r < TI; r += THREADS) {
+      if (i0 + r >= g.I) continue;
+      float most = stats[r], sum = 0.0f;
+      for (int w = 1; w < WJ; ++w) most = fmaxf(most, stats[w * 2 * TI + r]);
+      const float base = most == -INFINITY ? 0.0f : most;
+      for (int w = 0; w < WJ; ++w) {
+        const float m = stats[w * 2 * TI + r];
+        sum += stats[(w * 2 + 1) * TI + r] * exponential<DT>((m == -INFINITY ? base : m) - base);
+      }
+      h.stats[int64_t(tile_j) * 2 * g.rows + i0 + r] = most;
+      h.stats[(int64_t(tile_j) * 2 + 1) * g.rows + i0 + r] = sum;
+    }
+  }
+}
+
 // ---------------------------------------------------------------- the product
 
-// Tile TI x TJ of C by WI x WJ waves.
-template <int DT, int DIR, int TI, int TJ, int WI, int WJ, int LOAD>
+// Tile TI x TJ of C by WI x WJ waves. GROUPS: of the rows of one group.
+template <int DT, int DIR, int TI, int TJ, int WI, int WJ, int LOAD, bool GROUPS = false>
 __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
   constexpr int THREADS = WI * WJ * 64;
   constexpr int FI = TI / WI / 32, FJ = TJ / WJ / 32;  // 32 x 32 products per wave
@@ -602,15 +884,63 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
   // groups of 4 tile rows, so that blocks that share operands share an L2
   // (8192 x 8192 x 2048 forward with z kept: 254 us; groups of 8, 258, of 1,
   // 283; tiles in the blocks' order, 299).
-  const int tiles = g.tiles_i * g.tiles_j;
-  const int at = g.begin + int(blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8);
+  // Of groups, the eighths are of the tiles that there are (rows grouped), or of
+  // every group's tiles, as groups differ in length (sums grouped).
+  int tiles_i = g.tiles_i;
+  GroupScan scan;
+  if constexpr (GROUPS && !is_weight(DIR)) tiles_i = tiles_of_groups<TI>(g, scan);
+  const int tiles = tiles_i * g.tiles_j;
+  int at = g.begin + int(blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8);
+  int group_index = 0;
+  if constexpr (GROUPS) {
+    const int eighth = (tiles * g.parts + 7) / 8, b = g.begin + int(blockIdx.x);
+    if (eighth == 0) return;
+    int n = b / 8;
+    if constexpr (is_weight(DIR)) {
+      group_index = n / eighth;
+      n -= group_index * eighth;
+      if (group_index >= g.groups) return;
+    } else if (n >= eighth) {
+      return;
+    }
+    at = b % 8 * eighth + n;
+  }
   if (at >= tiles * g.parts) return;
   const int part = at / tiles, tile = at % tiles;
   constexpr int GROUP = 4;
   const int group = tile / (GROUP * g.tiles_j), in_group = tile % (GROUP * g.tiles_j);
-  const int rows = g.tiles_i - GROUP * group < GROUP ? g.tiles_i - GROUP * group : GROUP;
-  const int64_t i0 = int64_t(GROUP * group + in_group % rows) * TI, j0 = int64_t(in_group / rows) * TJ;
-  const int64_t k0 = part * g.part_k, k1 = k0 + g.part_k < g.K ? k0 + g.part_k : g.K;
+  const int rows = tiles_i - GROUP * group < GROUP ? tiles_i - GROUP * group : GROUP;
+  int64_t i0 = int64_t(GROUP * group + in_group % rows) * TI, j0 = int64_t(in_group / rows) * TJ;
+  if constexpr (GROUPS) {
+    // From here on the operands are the group's.
+    Group e;
+    if constexpr (is_weight(DIR)) {
+      e = group_at(g, group_index);
+      g.a = static_cast<const char*>(g.a) + e.begin * g.lda * TA::ES;
+      g.b = static_cast<const char*>(g.b) + e.begin * g.ldb * TA::ES;
+      g.c = static_cast<char*>(g.c) + group_index * g.I * g.ldc * (g.grad32 ? 4 : TA::ES);
+      g.K = e.rows;
+      const int32_t steps = (e.rows + TA::STEP - 1) / TA::STEP;
+      g.part_k = int64_t((steps + g.parts - 1) / g.parts) * TA::STEP;
+    } else {
+      e = group_of_tile<TI>(g, scan, GROUP * group + in_group % rows);
+      i0 = int64_t(e.tile) * TI;
+      g.a = static_cast<const char*>(g.a) + e.begin * g.lda * TA::ES;
+      g.b = static_cast<const char*>(g.b) + e.index * g.b_group * TA::ES;
+      if (DIR == DDP_LINEAR_FORWARD && g.bias != nullptr) g.bias = static_cast<const char*>(g.bias) + e.index * g.J * TA::ES;
+      if constexpr (DIR == DDP_LINEAR_FORWARD || DIR == DDP_LINEAR_BACKWARD_INPUT) {
+        g.c = static_cast<char*>(g.c) + e.begin * g.ldc * TA::ES;
+        if (g.z != nullptr) g.z = static_cast<char*>(g.z) + e.begin * g.ldz * TA::ES;
+      }
+      g.I = e.rows;
+    }
+  }
+  const int64_t all_i = GROUPS && is_weight(DIR) ? g.I * g.groups : g.I;      // rows of all groups' C,
+  const int64_t first_i = GROUPS && is_weight(DIR) ? group_index * g.I : 0;   // and this one's first
+  int64_t k0 = part * g.part_k, k1 = k0 + g.part_k < g.K ? k0 + g.part_k : g.K;
+  if constexpr (GROUPS) {
+    if (k0 > k1) k0 = k1;  // a part of a short group
+  }
   const int steps = int((k1 - k0 + TA::STEP - 1) / TA::STEP);
 
   const int lane = int(threadIdx.x) & 63, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
@@ -628,11 +958,15 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
   const bool sum_rows = DIR == DDP_LINEAR_BACKWARD_WEIGHT && g.row_sums != nullptr && wave % WJ == 0;
   float row_sum[FI] = {};
 
-  if (steps > 0) {
+  const int terms = DIR == kWeightTerms ? g.terms : 1;
+#pragma unroll 1
+  for (int term = 0; term < (DIR == kWeightTerms ? terms : 1); ++term) {
+    if (steps <= 0) break;
+    if (DIR == kWeightTerms && term > 0) __syncthreads();  // every wave is done with the first term's operands
     LA la;
     LB lb;
-    la.init(g.a, g.lda, g.I, g.K, i0, k0, k1);
-    lb.init(g.b, g.ldb, g.J, g.K, j0, k0, k1);
+    la.init(static_cast<const char*>(g.a) + (DIR == kWeightTerms ? term * g.term : 0), g.lda, g.I, g.K, i0, k0, k1, g.a_room);
+    lb.init(g.b, g.ldb, g.J, g.K, j0, k0, k1, g.b_room);
     u32x4 fa[2][FI], fb[2][FJ];
     // Fragment m of quarter s: B's first, then A's.
     const auto read_one = [&](const char* stage, int s, int to, int m) {
@@ -744,8 +1078,14 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
     for (int a = 0; a < FI; ++a) {
       const float r = row_sum[a] + __shfl_xor(row_sum[a], 32);  // both halves of k
       const int64_t i = i0 + wi + 32 * a + lane;
-      if (lane < 32 && i < g.I) g.row_sums[(int64_t(part) * g.tiles_j + tile_j) * g.I + i] = r;
+      if (lane < 32 && i < g.I) g.row_sums[(int64_t(part) * g.tiles_j + tile_j) * all_i + first_i + i] = r;
     }
+  }
+
+  if constexpr (is_head(DIR)) {
+    if (steps > 0) __syncthreads();  // every wave is done with the operands in LDS
+    head_outputs<DT, DIR, TI, TJ, WI, WJ>(g, acc, lds, i0, j0, wi, wj, wave, lane, tile_j);
+    return;
   }
 
   // The outputs leave by rows: a wave writes 32 rows of its sums to LDS (a
@@ -800,7 +1140,7 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
     if (g.parts > 1) {
 #pragma unroll
       for (int p = 0; p < BATCH; ++p)
-        if (i + p * RPP < g.I && n > 0) store8<DDP_FP32>(g.partial, (part * g.I + i + p * RPP) * jp + j, 8, v[p]);
+        if (i + p * RPP < g.I && n > 0) store8<DDP_FP32>(g.partial, (part * all_i + first_i + i + p * RPP) * jp + j, 8, v[p]);
     } else if (whole) {
       const auto values = [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
@@ -844,8 +1184,9 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
 // launch has two blocks per CU or fewer, which hide little latency (257 x 640
 // weight gradient: 4.0 us against 6.5 a part at a time; 1037 x 1023 forward in 7
 // parts, 42 MB with residual and outputs: 9 either way).
-template <int DT, int DIR>
+template <int DT, int DIR, bool GROUPS = false>
 __global__ __launch_bounds__(kThreads) void k_linear_join(LinearArgs g) {
+  if constexpr (GROUPS) g.I = bound_at(g, 1);  // one group, of rows
   const int64_t jv = (g.J + 7) / 8;
   const int64_t at = int64_t(blockIdx.x) * kThreads + threadIdx.x;
   if (at >= g.I * jv) return;

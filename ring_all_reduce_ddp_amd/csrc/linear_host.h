@@ -39,10 +39,11 @@ struct Cut {
 // picks takes 1.9 % longer than the best of them in the mean, 31 % at worst.
 // A tile's step (128 bytes of k) takes `step` cycles of a CU that its blocks
 // fill and `alone` of a block by itself, its outputs `ends`; parts cost a
-// launch, a round each, and their bytes.
-Cut cut_by_model(int dir, int32_t I, int32_t J, int32_t K, int dtype, bool direct) {
+// launch, a round each, and their bytes. With `groups`, of I rows or K terms in all,
+// the groups count as equally long, a group of rows as half a tile longer.
+Cut cut_by_model(int dir, int32_t I, int32_t J, int32_t K, int dtype, bool direct, int32_t groups, int32_t most_parts) {
   Cut best;
-  if (dir == DDP_LINEAR_FORWARD && I <= kFewRows) {
+  if (dir == DDP_LINEAR_FORWARD && groups == 0 && I <= kFewRows) {
     best.few = true;
     return best;
   }
@@ -61,12 +62,19 @@ Cut cut_by_model(int dir, int32_t I, int32_t J, int32_t K, int dtype, bool direc
   const auto up = [](int64_t a, int64_t b) { return int32_t((a + b - 1) / b); };
   const int32_t row = std::min(a_along(dir) ? K : I, b_along(dir) ? K : J);  // the operands' shorter rows
   const int n_shapes = row < 16 / elem_bytes(dtype) ? 1 : dtype == DDP_BF16 && direct ? 3 : 2;
-  const int32_t step = 128 / elem_bytes(dtype), steps = std::max(1, up(K, step));
+  const bool sums = groups > 0 && is_weight(dir);  // the groups are of terms
+  const int32_t step = 128 / elem_bytes(dtype), steps = std::max(1, up(sums ? up(K, groups) : K, step));
+  const float busy = float(std::min(groups, I));   // groups that have rows
   float least = INFINITY;
   for (int k = 0; k < n_shapes; ++k) {
     const Shape& sh = shapes[dtype == DDP_BF16][direct][k];
-    const int64_t tiles = int64_t(up(I, sh.tile)) * up(J, sh.tile);
+    int64_t tiles = int64_t(up(I, sh.tile)) * up(J, sh.tile);
+    if (sums)
+      tiles *= groups;
+    else if (groups > 1)
+      tiles = int64_t(std::max(busy, float(I) / float(sh.tile) + 0.5f * busy)) * up(J, sh.tile);
     for (int32_t want : {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 28, 32}) {
+      if (want > most_parts) break;
       if (want > 1 && (want > steps / 2 || tiles * want > 4 * kCus * sh.fit)) break;
       const int32_t per = up(steps, want), parts = up(steps, per), on_cu = up(tiles * parts, kCus);
       float t = std::max(float(up(on_cu, sh.fit)) * (kStart + float(per) * sh.alone),
@@ -84,17 +92,17 @@ Cut cut_by_model(int dir, int32_t I, int32_t J, int32_t K, int dtype, bool direc
 
 // The same, remembered per thread for the sizes seen last: the model takes a
 // microsecond or two, and a call asks it three times.
-Cut cut_of(int dir, int64_t I, int64_t J, int64_t K, int dtype, bool direct) {
+Cut cut_of(int dir, int64_t I, int64_t J, int64_t K, int dtype, bool direct, int32_t groups = 0, int32_t most_parts = 32) {
   struct Seen {
     int64_t key[4] = {-1, -1, -1, -1};
     Cut cut;
   };
   static thread_local Seen seen[64];
-  const int64_t key[4] = {I, J, K, dir * 4 + dtype * 2 + int(direct)};
+  const int64_t key[4] = {I, J, K, (int64_t(groups) * 64 + most_parts) * 32 + dir * 4 + dtype * 2 + int(direct)};
   const uint64_t h = (uint64_t(I) * 31 + uint64_t(J) * 7 + uint64_t(K)) * 8 + uint64_t(key[3]);
   Seen& s = seen[(h ^ (h >> 7)) % 64];
   if (!std::equal(key, key + 4, s.key)) {
-    s.cut = cut_by_model(dir, int32_t(I), int32_t(J), int32_t(K), dtype, direct);
+    s.cut = cut_by_model(dir, int32_t(I), int32_t(J), int32_t(K), dtype, direct, groups, most_parts);
     std::copy(key, key + 4, s.key);
   }
   return s.cut;
@@ -102,6 +110,66 @@ Cut cut_of(int dir, int64_t I, int64_t J, int64_t K, int dtype, bool direct) {
 
 int64_t partial_bytes(const Cut& c, int64_t I, int64_t J) {
   return c.parts > 1 ? round_up(int64_t(c.parts) * I * round_up(J, 8) * 4, 256) : 0;
+}
+
+// The bias gradient's partial rows, one per part and tile column.
+int64_t bias_bytes(const Cut& c, int64_t I, int64_t J) { return round_up(c.parts * div_up(J, c.tile) * I * 4, 256); }
+
+// Direct loads need whole, aligned chunks: the contiguous index of an
+// operand (with what lies behind it) a multiple of a chunk, offsets within a
+// tile below 2^32 bytes and the whole operand below 2^31 chunks.
+bool whole_chunks(const void* p, int64_t ld, int64_t rows, int64_t contiguous, int dtype) {
+  const int64_t V = 16 / elem_bytes(dtype);
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % V == 0 && contiguous % V == 0 && ld <= (int64_t(1) << 21) &&
+         rows * (ld / V) < (int64_t(1) << 31);
+}
+
+// The tiles of g's groups, in as many blocks as any bounds can ask for.
+template <int DT, int DIR, int T, int WI, int WJ, int LOAD>
+int launch_group_tiles(LinearArgs& g, const char* fn, hipStream_t s) {
+  const int64_t ti = div_up(g.I, T) + (is_weight(DIR) ? 0 : g.groups - 1), tj = div_up(g.J, T);
+  const int64_t blocks = is_weight(DIR) ? round_up(ti * tj * g.parts, 8) * g.groups : round_up(ti * tj * g.parts, 8);
+  if (blocks >= (int64_t(1) << 30)) return fail(DDP_EINVAL, std::string(fn) + ": too many tiles for one launch");
+  g.tiles_i = int32_t(ti);
+  g.tiles_j = int32_t(tj);
+  launch_blocks(blocks, [&](int64_t begin, dim3 grid) {
+    g.begin = int32_t(begin);
+    hipLaunchKernelGGL((k_linear<DT, DIR, T, T, WI, WJ, LOAD, true>), grid, dim3(WI * WJ * 64), 0, s, g);
+  });
+  DDP_HIP_TRY(hipGetLastError(), fn);
+  return DDP_OK;
+}
+
+// The same for a cut, and how its operands are loaded.
+template <int DT, int DIR>
+int launch_groups(LinearArgs& g, const Cut& c, bool direct, const char* fn, hipStream_t s) {
+  constexpr int V = 16 / (DT == DDP_BF16 ? 2 : 4);
+  g.parts = c.parts;
+  g.part_k = c.part_k;
+  if ((a_along(DIR) ? g.K : g.I) < V || (b_along(DIR) ? g.K : g.J) < V)  // rows shorter than a chunk
+    return launch_group_tiles<DT, DIR, 64, 2, 2, kShort>(g, fn, s);
+  if constexpr (DT == DDP_BF16) {
+    if (c.tile == 256) return launch_group_tiles<DT, DIR, 256, 2, 4, kDirect>(g, fn, s);
+  }
+  if (c.tile == 128)
+    return direct ? launch_group_tiles<DT, DIR, 128, 2, 2, kDirect>(g, fn, s) : launch_group_tiles<DT, DIR, 128, 2, 2, kAny>(g, fn, s);
+  return direct ? launch_group_tiles<DT, DIR, 64, 2, 2, kDirect>(g, fn, s) : launch_group_tiles<DT, DIR, 64, 2, 2, kAny>(g, fn, s);
+}
+
+// db (+)= the column sums of `rows` rows of `from` (fp32, or the data).
+int launch_column_sums(const void* from, int32_t from_dtype, int64_t ld, int64_t rows, int64_t N, void* db, int32_t grad_dtype,
+                       int32_t accumulate, const char* fn, hipStream_t s) {
+  launch_blocks(div_up(N, 64), [&](int64_t begin, dim3 grid) {
+    const auto launch = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, s, from, ld, rows, N, db, accumulate, begin * 64);
+    };
+    if (grad_dtype == DDP_BF16)
+      from_dtype == DDP_BF16 ? launch(k_column_sums<DDP_BF16, DDP_BF16>) : launch(k_column_sums<DDP_FP32, DDP_BF16>);
+    else
+      from_dtype == DDP_BF16 ? launch(k_column_sums<DDP_BF16, DDP_FP32>) : launch(k_column_sums<DDP_FP32, DDP_FP32>);
+  });
+  DDP_HIP_TRY(hipGetLastError(), fn);
+  return DDP_OK;
 }
 
 // A matrix argument: rows x cols, leading dimension ld, NULL where allowed.

@@ -153,8 +153,6 @@ void launch_act_backward(const void* dy, int64_t lddy, const void* z, int64_t ld
   }
 }
 
-// The bias gradient's partial rows, one per part and tile column.
-int64_t bias_bytes(const Cut& c, int64_t I, int64_t J) { return round_up(c.parts * div_up(J, c.tile) * I * 4, 256); }
 
 // Scratch of a product: for either loader, as the sizes alone do not tell which.
 int64_t scratch_bytes(int dir, int64_t I, int64_t J, int64_t K, int dtype, bool bias) {
@@ -195,15 +193,8 @@ int launch_tiles(LinearArgs& g, hipStream_t s) {
 template <int DT, int DIR>
 int launch_product(LinearArgs& g, void* workspace, bool want_rows, hipStream_t s) {
   constexpr int V = 16 / (DT == DDP_BF16 ? 2 : 4);
-  // Direct loads need whole, aligned chunks: the contiguous index of each
-  // operand a multiple of a chunk, offsets within a tile below 2^32 bytes and
-  // the whole operand below 2^31 chunks.
-  const auto aligned = [&](const void* p, int64_t ld, int64_t rows, int64_t contiguous) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % V == 0 && contiguous % V == 0 && ld <= (int64_t(1) << 21) &&
-           rows * (ld / V) < (int64_t(1) << 31);
-  };
-  const bool direct = aligned(g.a, g.lda, a_along(DIR) ? g.I : g.K, a_along(DIR) ? g.K : g.I) &&
-                      aligned(g.b, g.ldb, b_along(DIR) ? g.J : g.K, b_along(DIR) ? g.K : g.J);
+  const bool direct = whole_chunks(g.a, g.lda, a_along(DIR) ? g.I : g.K, a_along(DIR) ? g.K : g.I, DT) &&
+                      whole_chunks(g.b, g.ldb, b_along(DIR) ? g.J : g.K, b_along(DIR) ? g.K : g.J, DT);
   const Cut c = cut_of(DIR, g.I, g.J, g.K, DT, direct);
   const bool shorter = (a_along(DIR) ? g.K : g.I) < V || (b_along(DIR) ? g.K : g.J) < V;  // rows than a chunk
   if constexpr (DIR == DDP_LINEAR_FORWARD) {
@@ -382,18 +373,8 @@ extern "C" int ddp_linear_backward_weight(const void* dz, int64_t lddz, const vo
     sums = g.row_sums, sums_ld = N, sums_rows = int64_t(g.parts) * g.tiles_j;
   }
   if (db == nullptr) return DDP_OK;
-  const bool from16 = K == 0 && dtype == DDP_BF16;
-  launch_blocks(div_up(N, 64), [&](int64_t begin, dim3 grid) {
-    const auto launch = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, s, sums, sums_ld, sums_rows, N, db, accumulate, begin * 64);
-    };
-    if (grad_dtype == DDP_BF16)
-      from16 ? launch(k_column_sums<DDP_BF16, DDP_BF16>) : launch(k_column_sums<DDP_FP32, DDP_BF16>);
-    else
-      from16 ? launch(k_column_sums<DDP_BF16, DDP_FP32>) : launch(k_column_sums<DDP_FP32, DDP_FP32>);
-  });
-  DDP_HIP_TRY(hipGetLastError(), "ddp_linear_backward_weight: bias launch");
-  return DDP_OK;
+  return launch_column_sums(sums, K == 0 ? dtype : DDP_FP32, sums_ld, sums_rows, N, db, grad_dtype, accumulate,
+                            "ddp_linear_backward_weight: bias launch", s);
 }
 
 extern "C" int ddp_act_backward(const void* dy, int64_t lddy, const void* z, int64_t ldz, void* dz, int64_t lddz,
