@@ -229,6 +229,75 @@ int ddp_experts_backward_weight(const void* dz, int64_t lddz, const void* x, int
                                 int32_t grad_dtype, int32_t accumulate, void* workspace, int64_t workspace_bytes,
                                 void* stream);
 
+/* ---------------------------------------------------------------- losses of an output layer
+ * z = x w^T, x[M][K] and w[V][K] as in the linear layer, V the vocabulary. Its
+ * M x V values are made where they are used and not kept: neither call needs
+ * room for them, and the backward pass makes them again, a piece of the
+ * vocabulary at a time. p_ij = exp(z_ij - lse_i), lse_i = log sum_j exp(z_ij).
+ *
+ * Cross entropy: row i has a target t_i (int64 on the device) and
+ *   loss_i = lse_i - z_it,   dz_ij = dloss_i (p_ij - [j = t_i]).
+ *
+ * Distillation: row i has C entries of a teacher, ids and logits, and with
+ * q = softmax of logits / T over the row's entries, and z = x w^T / T,
+ *   loss_i = T^2 sum_k q_k (log q_k - z_i,id_k + lse_i),
+ *   the gradient of x w^T is dloss_i T (p_ij - sum of q_k with id_k = j).
+ * An entry whose id is negative or whose logit is -infinity is left out.
+ * lse is that of x w^T / T. An id may occur more than once.
+ *
+ * In both, dx = dz w and dw (+)= dz^T x. Rows with a negative target, or
+ * with no entry, do not count: their loss, lse and dx are 0, they cost
+ * next to nothing, and whatever x, lse and dloss hold there reaches nothing. A
+ * target or id from V on, or an entry's logit that is +infinity or NaN, makes
+ * the row's loss and gradients NaN, and with them dw.
+ *
+ * loss, lse and dloss are float[M]; the gradient is that of sum_i dloss_i
+ * loss_i, so a mean's is dloss = 1 / its count. lse is as the forward call left it. dx and dw may be NULL (not
+ * wanted); dw is of grad_dtype (`dtype`, or fp32 gradients of bf16 data),
+ * overwritten or, with accumulate = 1, added to with one rounding, and may lie in a gradient
+ * arena. Sums and statistics are fp32. The products of a bf16 gradient take dz
+ * rounded to bf16; those of an fp32 dw of bf16 data take it as two bf16 terms,
+ * which are off by 2^-16 of it at most.
+ *
+ * 1 <= V < 2^31, 0 <= M <= 2^21, 1 <= K <= 2^21, M K <= 2^33, 1 <= C <= 1024, T > 0 and finite.
+ *
+ * ddp_cross_entropy_workspace: bytes of scratch for a direction and sizes on
+ * the current device, under the conditions of ddp_linear_workspace; grad_dtype
+ * counts for the backward direction. */
+#define DDP_LOSS_FORWARD 0
+#define DDP_LOSS_BACKWARD 1
+int ddp_cross_entropy_workspace(int32_t direction, int64_t M, int64_t V, int64_t K, int32_t dtype, int32_t grad_dtype,
+                                int64_t* bytes);
+
+/* loss and lse of every row. */
+int ddp_cross_entropy_forward(const void* x, int64_t ldx, const void* w, int64_t ldw, const int64_t* targets, float* loss,
+                              float* lse, int64_t M, int64_t V, int64_t K, int32_t dtype, void* workspace,
+                              int64_t workspace_bytes, void* stream);
+
+/* dx and dw. */
+int ddp_cross_entropy_backward(const void* x, int64_t ldx, const void* w, int64_t ldw, const int64_t* targets,
+                               const float* lse, const float* dloss, void* dx, int64_t lddx, void* dw, int64_t lddw,
+                               int64_t M, int64_t V, int64_t K, int32_t dtype, int32_t grad_dtype, int32_t accumulate,
+                               void* workspace, int64_t workspace_bytes, void* stream);
+
+/* The same for distillation: ids[M][C] int64 with leading dimension ld_ids,
+ * teacher[M][C] the logits, of teacher_dtype (DDP_FP32 or DDP_BF16). */
+int ddp_distill_workspace(int32_t direction, int64_t M, int64_t V, int64_t K, int32_t C, int32_t dtype,
+                          int32_t grad_dtype, int64_t* bytes);
+
+/* loss and lse of every row. */
+int ddp_distill_forward(const void* x, int64_t ldx, const void* w, int64_t ldw, const int64_t* ids, int64_t ld_ids,
+                        const void* teacher, int64_t ld_teacher, int32_t teacher_dtype, float temperature, float* loss,
+                        float* lse, int64_t M, int64_t V, int64_t K, int32_t C, int32_t dtype, void* workspace,
+                        int64_t workspace_bytes, void* stream);
+
+/* dx and dw. */
+int ddp_distill_backward(const void* x, int64_t ldx, const void* w, int64_t ldw, const int64_t* ids, int64_t ld_ids,
+                         const void* teacher, int64_t ld_teacher, int32_t teacher_dtype, float temperature,
+                         const float* lse, const float* dloss, void* dx, int64_t lddx, void* dw, int64_t lddw, int64_t M,
+                         int64_t V, int64_t K, int32_t C, int32_t dtype, int32_t grad_dtype, int32_t accumulate,
+                         void* workspace, int64_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

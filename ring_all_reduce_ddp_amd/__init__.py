@@ -115,6 +115,15 @@ def _load():
         "ddp_experts_backward_input": (ctypes.c_int, [vp, i64, vp, i64, vp, vp, i64, vp, i64, i64, i64, i64, i64, i32, i32, vp]),
         "ddp_experts_backward_weight": (ctypes.c_int, [vp, i64, vp, i64, vp, vp, i64, vp, i64, i64, i64, i64, i32, i32, i32,
                                                        vp, i64, vp]),
+        "ddp_cross_entropy_workspace": (ctypes.c_int, [i32, i64, i64, i64, i32, i32, ctypes.POINTER(i64)]),
+        "ddp_cross_entropy_forward": (ctypes.c_int, [vp, i64, vp, i64, vp, vp, vp, i64, i64, i64, i32, vp, i64, vp]),
+        "ddp_cross_entropy_backward": (ctypes.c_int, [vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, i64, i64, i64, i32, i32, i32,
+                                                      vp, i64, vp]),
+        "ddp_distill_workspace": (ctypes.c_int, [i32, i64, i64, i64, i32, i32, i32, ctypes.POINTER(i64)]),
+        "ddp_distill_forward": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, vp, i64, i32, f32, vp, vp, i64, i64, i64, i32, i32,
+                                               vp, i64, vp]),
+        "ddp_distill_backward": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, vp, i64, i32, f32, vp, vp, vp, i64, vp, i64, i64, i64, i64,
+                                                i32, i32, i32, i32, vp, i64, vp]),
         "ddp_act_backward": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, i64, i64, i32, i32, vp]),
     }
     for name, (res, args) in sig.items():
@@ -867,3 +876,123 @@ def experts_backward_weight(dz, x, offsets, dw, db=None, accumulate=False, works
     ws, (nbytes, p) = _scratch(_experts_workspace(LINEAR_BACKWARD_WEIGHT, t, e, n, k, code), workspace, stream)
     _check(_get_lib().ddp_experts_backward_weight(gp, ldg, xp, ldx, _offsets(offsets, e + 1), wp, ldw, bp, t, e, n, k, code,
                                                   dtype_code(gt), 1 if accumulate else 0, p, nbytes, _stream(stream)))
+
+
+LOSS_FORWARD, LOSS_BACKWARD = 0, 1
+
+
+@functools.lru_cache(maxsize=4096)
+def _loss_workspace(direction, m, v, k, top, code, grad_code):
+    b = ctypes.c_int64()
+    if top:
+        _check(_get_lib().ddp_distill_workspace(direction, m, v, k, top, code, grad_code, ctypes.byref(b)))
+    else:
+        _check(_get_lib().ddp_cross_entropy_workspace(direction, m, v, k, code, grad_code, ctypes.byref(b)))
+    return b.value
+
+
+def cross_entropy_workspace(direction, m, v, k, dtype, grad_dtype=None):
+    """Bytes of scratch that a cross entropy call of these sizes needs
+    (direction LOSS_FORWARD or LOSS_BACKWARD)."""
+    code = dtype_code(dtype)
+    return _loss_workspace(int(direction), int(m), int(v), int(k), 0, code, code if grad_dtype is None else dtype_code(grad_dtype))
+
+
+def distill_workspace(direction, m, v, k, top, dtype, grad_dtype=None):
+    """Bytes of scratch that a distillation call of these sizes needs."""
+    code = dtype_code(dtype)
+    if int(top) < 1:
+        raise ValueError("a row has at least one entry")
+    return _loss_workspace(int(direction), int(m), int(v), int(k), int(top), code,
+                           code if grad_dtype is None else dtype_code(grad_dtype))
+
+
+def _row_values(t, m, what, stream):
+    """A float32 vector of m elements, made if it is None."""
+    t = _empty((m,), torch.float32, stream) if t is None else t
+    return t, _vector(t, m, torch.float32, what)
+
+
+def _entries(ids, teacher, m):
+    """Arguments of a teacher's entries: (ids, ld, logits, ld, logits' dtype, entries a row)."""
+    c = ids.shape[1] if ids.dim() == 2 else 0
+    if c < 1:
+        raise ValueError("ids must be a matrix with at least one entry a row")
+    ip, ldi = _matrix(ids, m, c, torch.int64, "ids")
+    tp, ldt = _matrix(teacher, m, c, teacher.dtype, "teacher")
+    return ip, ldi, tp, ldt, dtype_code(teacher.dtype), c
+
+
+def _loss_shapes(x, w):
+    """(m, v, k, dtype, its code, x's and w's arguments)."""
+    m, k = x.shape
+    v, dt = w.shape[0], x.dtype
+    xp, ldx = _matrix(x, m, k, dt, "x")
+    wp, ldw = _matrix(w, v, k, dt, "w")
+    return m, v, k, dt, dtype_code(dt), (xp, ldx, wp, ldw)
+
+
+def _gradients(dx, dw, m, v, k, dt):
+    """Arguments of dx and dw (None: not wanted), and the code of dw's dtype."""
+    op, ldo = _matrix(dx, m, k, dt, "out")
+    gt = dt if dw is None else dw.dtype
+    gp, ldg = _matrix(dw, v, k, gt, "dw")
+    return (op, ldo, gp, ldg), dtype_code(gt)
+
+
+def cross_entropy_forward(x, w, targets, loss=None, lse=None, workspace=None, stream=None):
+    """(loss, lse) of every row of z = x w^T with an int64 target a row
+    (negative: the row does not count), float32, without a matrix of z (see
+    ddp_cross_entropy_forward in include/ddp_train.h)."""
+    m, v, k, dt, code, xw = _loss_shapes(x, w)
+    loss, lossp = _row_values(loss, m, "loss", stream)
+    lse, lsep = _row_values(lse, m, "lse", stream)
+    ws, (nbytes, p) = _scratch(_loss_workspace(LOSS_FORWARD, m, v, k, 0, code, code), workspace, stream)
+    _check(_get_lib().ddp_cross_entropy_forward(*xw, _vector(targets, m, torch.int64, "targets"), lossp, lsep, m, v, k, code,
+                                                p, nbytes, _stream(stream)))
+    return loss, lse
+
+
+def cross_entropy_backward(x, w, targets, lse, dloss, dw=None, accumulate=False, out=None, need_dx=True, workspace=None, stream=None):
+    """dx (None with need_dx=False), with dw (+)= the gradient of w where a
+    tensor is given: the gradients of sum(dloss * loss); lse as
+    cross_entropy_forward gave it (see ddp_cross_entropy_backward)."""
+    m, v, k, dt, code, xw = _loss_shapes(x, w)
+    dx = _result(out, m, k, dt, stream) if need_dx else None
+    grads, grad_code = _gradients(dx, dw, m, v, k, dt)
+    ws, (nbytes, p) = _scratch(_loss_workspace(LOSS_BACKWARD, m, v, k, 0, code, grad_code), workspace, stream)
+    _check(_get_lib().ddp_cross_entropy_backward(*xw, _vector(targets, m, torch.int64, "targets"),
+                                                 _vector(lse, m, torch.float32, "lse"), _vector(dloss, m, torch.float32, "dloss"),
+                                                 *grads, m, v, k, code, grad_code, 1 if accumulate else 0, p, nbytes,
+                                                 _stream(stream)))
+    return dx
+
+
+def distill_forward(x, w, ids, teacher, temperature=1.0, loss=None, lse=None, workspace=None, stream=None):
+    """(loss, lse) of every row: temperature^2 times the divergence of
+    softmax(x w^T / temperature) from the softmax of a teacher's logits /
+    temperature at `ids` (int64; negative, or a logit of -inf: left out). See
+    ddp_distill_forward in include/ddp_train.h."""
+    m, v, k, dt, code, xw = _loss_shapes(x, w)
+    entries = _entries(ids, teacher, m)
+    loss, lossp = _row_values(loss, m, "loss", stream)
+    lse, lsep = _row_values(lse, m, "lse", stream)
+    ws, (nbytes, p) = _scratch(_loss_workspace(LOSS_FORWARD, m, v, k, entries[5], code, code), workspace, stream)
+    _check(_get_lib().ddp_distill_forward(*xw, *entries[:5], float(temperature), lossp, lsep, m, v, k, entries[5], code, p, nbytes,
+                                          _stream(stream)))
+    return loss, lse
+
+
+def distill_backward(x, w, ids, teacher, lse, dloss, temperature=1.0, dw=None, accumulate=False, out=None, need_dx=True,
+                     workspace=None, stream=None):
+    """The gradients of sum(dloss * loss), as cross_entropy_backward gives
+    them (see ddp_distill_backward)."""
+    m, v, k, dt, code, xw = _loss_shapes(x, w)
+    entries = _entries(ids, teacher, m)
+    dx = _result(out, m, k, dt, stream) if need_dx else None
+    grads, grad_code = _gradients(dx, dw, m, v, k, dt)
+    ws, (nbytes, p) = _scratch(_loss_workspace(LOSS_BACKWARD, m, v, k, entries[5], code, grad_code), workspace, stream)
+    _check(_get_lib().ddp_distill_backward(*xw, *entries[:5], float(temperature), _vector(lse, m, torch.float32, "lse"),
+                                           _vector(dloss, m, torch.float32, "dloss"), *grads, m, v, k, entries[5], code, grad_code,
+                                           1 if accumulate else 0, p, nbytes, _stream(stream)))
+    return dx

@@ -21,7 +21,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libddp_ring.so")
 
 HIP_SOURCES = ["fused_kernels.hip", "ring_kernels.hip", "pack_kernels.hip", "view_kernels.hip", "scatter_kernels.hip", "reducer.hip", "runtime.hip",
-               "grads_kernels.hip", "adamw_kernels.hip", "linear_kernels.hip", "experts_kernels.hip"]
+               "grads_kernels.hip", "adamw_kernels.hip", "linear_kernels.hip", "experts_kernels.hip", "head_kernels.hip"]
 HOST_SOURCES = ["plan.cpp"]
 ARCH = "gfx950"
 

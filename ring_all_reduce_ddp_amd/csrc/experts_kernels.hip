@@ -52,7 +52,7 @@ int launch_weight(LinearArgs& g, void* db, int32_t grad_dtype, void* workspace, 
     DDP_HIP_TRY(hipGetLastError(), fn);
   }
   if (db == nullptr) return DDP_OK;
-  return launch_column_sums(g.row_sums, DDP_FP32, N, int64_t(g.parts) * g.tiles_j, N, db, grad_dtype, g.accumulate, fn, s);
+  return launch_column_sums<DDP_FP32>(g.row_sums, N, int64_t(g.parts) * g.tiles_j, N, db, grad_dtype, g.accumulate, fn, s);
 }
 
 }  // namespace

@@ -1,0 +1,673 @@
+// Losses of an output layer z = x w^T over a large vocabulary, without a
+// matrix of z (ddp_train.h): cross entropy with a target a row, and the
+// divergence from a teacher's top logits.
+//
+//   forward    lse = log sum exp(z), loss from lse and z of the row's entries
+//   backward   dz = dloss (exp(z - lse) - q), dx = dz w, dw (+)= dz^T x
+//
+// The rows that count are gathered first, by index and by value: rows that do
+// not (padding, a prompt) cost nothing, and what they hold, NaN too, reaches
+// nothing. The products then have one group of rows, whose length is on the
+// device (linear_device.h). Forward is one product whose tiles leave a maximum
+// and a sum a row. Backward makes z again, a piece of the vocabulary at a time:
+// dz of the piece, then its part of dx, kept in fp32 from piece to piece, and
+// its rows of dw.
+#include <climits>
+
+#include "linear_host.h"
+
+namespace ddp {
+namespace {
+
+constexpr int32_t kMostTop = 1024;
+// Operands of direct loads have leading dimensions up to 2^21 and fewer than
+// 2^31 chunks, and those in the scratch are always loaded so.
+constexpr int64_t kMostRows = int64_t(1) << 21, kMostIns = int64_t(1) << 21;
+
+// ---------------------------------------------------------------- a teacher's top logits
+
+// One wave takes a row: the softmax of its logits / T over the entries that are
+// kept, then each id once, in ascending order, with the weights of its entries
+// added, and where each column tile's entries start.
+struct TopArgs {
+  const int64_t* ids;
+  const void* logits;
+  int64_t ld_ids, ld_logits, vocabulary;
+  int32_t top, width, tiles;  // column tiles
+  float inverse;              // 1 / T
+  int32_t* out_ids;
+  float* out_weights;
+  uint16_t* out_starts;
+  float* own_terms;           // sum of q log q, NaN where an entry is not valid
+  int32_t* counted;
+};
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+  return v;
+}
+
+template <int DT>
+__global__ __launch_bounds__(64) void k_top(TopArgs g) {
+  extern __shared__ int32_t lds[];
+  int32_t* const ids = lds;                                    // of the kept entries, else -1
+  float* const weights = reinterpret_cast<float*>(lds + g.top);
+  int32_t* const once = lds + 2 * g.top;                       // an id's first entry, else INT_MAX
+  int32_t* const sorted = lds + 3 * g.top;
+  const int lane = int(threadIdx.x);
+  const int64_t row = blockIdx.x;
+  const int64_t* const id_row = g.ids + row * g.ld_ids;
+  bool bad = false, any = false;
+  float most = -INFINITY;
+  for (int k = lane; k < g.top; k += 64) {
+    const int64_t id = id_row[k];
+    const float t = Ops<DT>::load1(g.logits, row * g.ld_logits + k);
+    const bool kept = id >= 0 && t != -INFINITY;
+    if (kept) {
+      any = true;
+      bad |= id >= g.vocabulary || !(t < INFINITY);
+      most = fmaxf(most, t);
+    }
+    ids[k] = !kept ? -1 : id < g.vocabulary ? int32_t(id) : INT_MAX - 1;
+    weights[k] = t;
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor(most, d));
+  bad = __any(bad);
+  any = __any(any);
+  __syncthreads();
+  float sum = 0.0f;
+  for (int k = lane; k < g.top; k += 64) sum += ids[k] >= 0 ? expf((weights[k] - most) * g.inverse) : 0.0f;
+  sum = wave_sum(sum);
+  const float log_sum = logf(sum);
+  float own = 0.0f;
+  for (int k = lane; k < g.top; k += 64) {
+    const float log_q = (weights[k] - most) * g.inverse - log_sum;
+    const float q = ids[k] >= 0 ? expf((weights[k] - most) * g.inverse) / sum : 0.0f;
+    if (q > 0.0f) own += q * log_q;
+    weights[k] = q;
+  }
+  own = wave_sum(own);
+  if (lane == 0) {
+    g.own_terms[row] = bad ? NAN : own;
+    g.counted[row] = any;
+  }
+  if (!any) return;
+  __syncthreads();
+  for (int k = lane; k < g.top; k += 64) {
+    bool first = ids[k] >= 0;
+    for (int o = 0; o < k; ++o) first &= ids[o] != ids[k];
+    once[k] = first ? ids[k] : INT_MAX;
+  }
+  __syncthreads();
+  int count = 0;
+  for (int k0 = 0; k0 < g.top; k0 += 64) {
+    const int k = k0 + lane;
+    const bool first = k < g.top && once[k] != INT_MAX;
+    count += int(__popcll(__ballot(first)));
+    if (!first) continue;
+    float q = 0.0f;
+    int rank = 0;
+    for (int o = 0; o < g.top; ++o) {
+      if (ids[o] == ids[k]) q += weights[o];
+      rank += once[o] < ids[k] ? 1 : 0;
+    }
+    sorted[rank] = ids[k];
+    g.out_ids[row * g.top + rank] = ids[k];
+    g.out_weights[row * g.top + rank] = q;
+  }
+  __syncthreads();
+  for (int t = lane; t <= g.tiles; t += 64) {
+    const int64_t column = int64_t(t) * g.width;
+    int lo = 0, hi = count;   // the first entry not below the tile's first column
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (sorted[mid] < column)
+        lo = mid + 1;
+      else
+        hi = mid;
+    }
+    g.out_starts[row * (g.tiles + 1) + t] = uint16_t(lo);
+  }
+}
+
+// ---------------------------------------------------------------- the rows that count
+
+struct RowsArgs {
+  const int64_t* targets;  // a row counts if its target is not negative,
+  const int32_t* counted;  // or (targets NULL) where this is not 0
+  const void* x;
+  int64_t ldx, M, K, ld_out;
+  int32_t rows;            // of a block, at most kThreads
+  int64_t* bounds;         // receives 0 and the rows' number
+  int32_t* row_of;
+  void* out;               // [number][ld_out], zeros from K on
+  float* loss;             // forward: zeros where rows do not count
+  float* lse;
+  void* dx;                // backward: likewise (NULL: not wanted)
+  int64_t lddx;
+  __device__ __forceinline__ bool counts(int64_t i) const { return targets != nullptr ? targets[i] >= 0 : counted[i] != 0; }
+};
+
+// A block counts the rows before its own by itself: reading a flag each costs
+// less than a launch that would sum them.
+template <int DT>
+__global__ __launch_bounds__(kThreads) void k_rows(RowsArgs g) {
+  __shared__ int32_t waves[2][4];
+  __shared__ int32_t here[kThreads];
+  const int lane = int(threadIdx.x) & 63, wave = int(threadIdx.x) >> 6;
+  const int64_t first = int64_t(blockIdx.x) * g.rows, end = first + g.rows < g.M ? first + g.rows : g.M;
+  int32_t before = 0;
+#pragma unroll 4
+  for (int64_t i = threadIdx.x; i < first; i += kThreads) before += g.counts(i) ? 1 : 0;
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) before += __shfl_xor(before, d);
+  const int64_t row = first + threadIdx.x;
+  const bool inside = row < end, mine = inside && g.counts(row);
+  const uint64_t votes = __ballot(mine);
+  if (lane == 0) {
+    waves[0][wave] = before;
+    waves[1][wave] = int32_t(__popcll(votes));
+  }
+  __syncthreads();
+  before = waves[0][0] + waves[0][1] + waves[0][2] + waves[0][3];
+  int32_t place = int32_t(__popcll(votes & ((uint64_t(1) << lane) - 1))), number = 0;
+  for (int w = 0; w < 4; ++w) {
+    if (w < wave) place += waves[1][w];
+    number += waves[1][w];
+  }
+  if (mine) {
+    here[place] = int32_t(row);
+    g.row_of[before + place] = int32_t(row);
+  } else if (inside) {
+    if (g.loss != nullptr) g.loss[row] = g.lse[row] = 0.0f;
+  }
+  if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) {
+    g.bounds[0] = 0;
+    g.bounds[1] = before + number;
+  }
+  __syncthreads();
+  constexpr int ES = DT == DDP_BF16 ? 2 : 4;
+  for (int32_t r = wave; r < number; r += 4) {
+    const int64_t from = here[r] * g.ldx;
+    char* const to = static_cast<char*>(g.out) + (before + r) * g.ld_out * ES;
+    for (int64_t j = lane * 8; j < g.ld_out; j += 512) {
+      const Raw8 v = load_raw8<DT>(g.x, from + j, g.K - j >= 8 ? 8 : g.K > j ? int(g.K - j) : 0);
+      u32x4* const p = reinterpret_cast<u32x4*>(to + j * ES);
+      p[0] = v.a;
+      if (DT == DDP_FP32) p[1] = v.b;
+    }
+  }
+  if (g.dx == nullptr || number == end - first) return;
+  const float zeros[8] = {};
+  for (int64_t i = first + wave; i < end; i += 4) {
+    if (g.counts(i)) continue;
+    for (int64_t j = lane * 8; j < g.K; j += 512) store8<DT>(g.dx, i * g.lddx + j, g.K - j >= 8 ? 8 : int(g.K - j), zeros);
+  }
+}
+
+// ---------------------------------------------------------------- the rows' losses
+
+struct JoinArgs {
+  const int64_t* bounds;
+  const int32_t* row_of;
+  int64_t M;
+  int32_t column_tiles;
+  HeadArgs head;
+  float factor;   // of the loss
+  float* loss;
+  float* lse;
+};
+
+constexpr int kJoinRows = 32, kJoinSlices = kThreads / kJoinRows;
+
+// 32 rows a block, eight threads a row: each an eighth of the column tiles, then
+// of the row's entries, joined in a fixed order.
+__global__ __launch_bounds__(kThreads) void k_loss_join(JoinArgs g) {
+  __shared__ float part[kJoinSlices][kJoinRows];
+  const HeadArgs& h = g.head;
+  const int in = int(threadIdx.x) % kJoinRows, slice = int(threadIdx.x) / kJoinRows;
+  const int64_t number = g.bounds[1], i = int64_t(blockIdx.x) * kJoinRows + in;
+  if (int64_t(blockIdx.x) * kJoinRows >= number) return;
+  const bool counts = i < number;
+  const auto joined = [&](float mine, auto&& join) {
+    part[slice][in] = mine;
+    __syncthreads();
+    float v = part[0][in];
+#pragma unroll
+    for (int s = 1; s < kJoinSlices; ++s) v = join(v, part[s][in]);
+    __syncthreads();
+    return v;
+  };
+  const auto add = [](float a, float b) { return a + b; };
+  float most = -INFINITY;
+  if (counts) {
+#pragma unroll 4
+    for (int t = slice; t < g.column_tiles; t += kJoinSlices) most = fmaxf(most, h.stats[int64_t(t) * 2 * g.M + i]);
+  }
+  most = joined(most, [](float a, float b) { return fmaxf(a, b); });
+  const float base = most == -INFINITY ? 0.0f : most;
+  float sum = 0.0f;
+  if (counts) {
+#pragma unroll 4
+    for (int t = slice; t < g.column_tiles; t += kJoinSlices) {
+      const float m = h.stats[int64_t(t) * 2 * g.M + i], s = h.stats[(int64_t(t) * 2 + 1) * g.M + i];
+      sum += s * expf((m == -INFINITY ? base : m) - base);
+    }
+  }
+  const float lse = base + logf(joined(sum, add));
+  const int64_t row = counts ? g.row_of[i] : 0;
+  float loss = 0.0f;
+  if (h.targets != nullptr) {
+    if (counts) loss = h.targets[row] < h.vocabulary ? lse - h.picked[row] : NAN;
+  } else {
+    if (counts) {
+      const int entries = h.starts[row * (h.tiles + 1) + h.tiles];
+      for (int k = slice; k < entries; k += kJoinSlices) {
+        const float q = h.weights[row * h.top + k];
+        if (q > 0.0f) loss += q * (lse - h.picked[row * h.top + k]);
+      }
+    }
+    loss = joined(loss, add);
+    if (counts) loss = g.factor * (loss + h.own_terms[row]);
+  }
+  if (!counts || slice != 0) return;
+  g.loss[row] = loss;
+  g.lse[row] = lse;
+}
+
+// ---------------------------------------------------------------- host side
+
+// What a call works on: sizes, types and the rows' targets or entries.
+struct Head {
+  int64_t M, V, K;
+  int32_t top;           // 0: targets
+  int32_t dtype, grad_dtype;
+  bool backward;
+  const void* x;
+  int64_t ldx;
+  const void* w;
+  int64_t ldw;
+  const int64_t* targets;
+  const int64_t* ids;
+  int64_t ld_ids;
+  const void* teacher;
+  int64_t ld_teacher;
+  int32_t teacher_dtype;
+  float temperature;
+
+  int64_t ldg() const { return round_up(K, 8); }   // of the gathered rows
+  // fp32 gradients of bf16 data: dz in two terms.
+  int32_t terms() const { return dtype == DDP_BF16 && grad_dtype == DDP_FP32 ? 2 : 1; }
+  bool w_whole() const { return whole_chunks(w, ldw, V, K, dtype); }
+};
+
+// The tile of the products that make z.
+int tile_of(const Head& h, int64_t columns, bool direct) {
+  return cut_of(kRowStats, h.M, columns, h.K, h.dtype, direct, 0, 1).tile;
+}
+
+// Columns of a piece, and pieces. A piece of dz should lie in the Infinity Cache
+// for the two products that read it, but be long enough that dx's sum over it
+// is worth the pass over dx in fp32 that each piece costs.
+struct Pieces {
+  int64_t columns, number;
+};
+Pieces pieces_of(const Head& h) {
+  const int64_t most = std::min<int64_t>(1 << 20, std::max<int64_t>(4096, (int64_t(1) << 27) / std::max<int64_t>(h.M, 1)));
+  const int64_t columns = round_up(div_up(h.V, div_up(h.V, most)), 256);
+  return {columns, div_up(h.V, columns)};
+}
+
+// Where a call's scratch lies; with base NULL, only its size.
+struct Scratch {
+  int64_t* bounds;
+  int32_t* row_of;
+  char* rows;
+  int32_t* counted;
+  float* own_terms;
+  int32_t* ids;
+  float* weights;
+  uint16_t* starts;
+  float* stats;
+  float* picked;
+  char* dz;
+  int64_t lddz;
+  float* sums;
+  float* partial;
+  int64_t bytes;
+};
+Scratch scratch_of(const Head& h, void* base) {
+  Scratch s{};
+  int64_t at = 0;
+  const auto take = [&](auto*& p, int64_t bytes) {
+    p = base == nullptr ? nullptr : reinterpret_cast<std::remove_reference_t<decltype(p)>>(static_cast<char*>(base) + at);
+    at += round_up(bytes, 256);
+  };
+  const int64_t eb = elem_bytes(h.dtype), tiles = div_up(h.V, 64);  // of any width
+  take(s.bounds, 16);
+  take(s.row_of, h.M * 4);
+  take(s.rows, h.M * h.ldg() * eb);
+  if (h.top > 0) {
+    take(s.counted, h.M * 4);
+    take(s.own_terms, h.M * 4);
+    take(s.ids, h.M * h.top * 4);
+    take(s.weights, h.M * h.top * 4);
+    take(s.starts, h.M * (tiles + 1) * 2);
+  }
+  if (!h.backward) {
+    take(s.stats, tiles * 2 * h.M * 4);
+    take(s.picked, h.M * std::max(h.top, 1) * 4);
+  } else {
+    const Pieces p = pieces_of(h);
+    s.lddz = std::min(p.columns, round_up(h.V, 8));
+    take(s.dz, h.terms() * h.M * s.lddz * eb);
+    if (p.number > 1) take(s.sums, h.M * h.K * 4);
+    int64_t most = 0;
+    for (int64_t v0 = 0; v0 < h.V; v0 += p.columns) {
+      const int64_t n = std::min(p.columns, h.V - v0);
+      for (bool direct : {false, true})
+        most = std::max(most, partial_bytes(cut_of(kInputPiece, h.M, h.K, n, h.dtype, direct), h.M, h.K));
+      most = std::max(most, partial_bytes(cut_of(kWeightTerms, n, h.K, h.M * h.terms(), h.dtype, true), n, h.K));
+    }
+    take(s.partial, most);
+  }
+  s.bytes = at;
+  return s;
+}
+
+int check_head(const char* fn, const Head& h) {
+  int st = check_common(fn, h.M, h.V, h.K, h.dtype, DDP_ACT_NONE);
+  if (st != DDP_OK) return st;
+  if (h.V < 1 || h.K < 1) return fail(DDP_EINVAL, std::string(fn) + ": V and K must be at least 1");
+  if (h.M > kMostRows || h.K > kMostIns || h.M * h.K > kMostRows * 4096)
+    return fail(DDP_EINVAL, std::string(fn) + ": M and K may be 2^21 at most, M * K 2^33");
+  if (h.grad_dtype != h.dtype && h.grad_dtype != DDP_FP32)
+    return fail(DDP_EINVAL, std::string(fn) + ": grad_dtype must be the data's or fp32");
+  return DDP_OK;
+}
+int check_top(const char* fn, const Head& h) {
+  if (h.top < 1 || h.top > kMostTop) return fail(DDP_EINVAL, std::string(fn) + ": C must lie in [1, 1024]");
+  return DDP_OK;
+}
+
+// The rows that count, and a teacher's entries; g: the products' arguments that
+// all have in common.
+template <int DT>
+int launch_rows_that_count(const Head& h, const Scratch& w, int width, RowsArgs r, LinearArgs& g, const char* fn, hipStream_t s) {
+  const int32_t tiles = int32_t(div_up(h.V, width));
+  if (h.top > 0 && h.M > 0) {
+    TopArgs t{h.ids, h.teacher, h.ld_ids, h.ld_teacher, h.V, h.top, width, tiles, 1.0f / h.temperature,
+              w.ids, w.weights, w.starts, w.own_terms, w.counted};
+    const size_t lds = size_t(h.top) * 16;
+    if (h.teacher_dtype == DDP_BF16)
+      hipLaunchKernelGGL((k_top<DDP_BF16>), dim3(unsigned(h.M)), dim3(64), lds, s, t);
+    else
+      hipLaunchKernelGGL((k_top<DDP_FP32>), dim3(unsigned(h.M)), dim3(64), lds, s, t);
+    DDP_HIP_TRY(hipGetLastError(), fn);
+  }
+  r.targets = h.targets, r.counted = w.counted;
+  r.x = h.x, r.ldx = h.ldx, r.M = h.M, r.K = h.K, r.ld_out = h.ldg();
+  r.rows = int32_t(std::min<int64_t>(kThreads, std::max<int64_t>(8, div_up(h.M, 1024))));
+  r.bounds = w.bounds, r.row_of = w.row_of, r.out = w.rows;
+  hipLaunchKernelGGL((k_rows<DT>), dim3(unsigned(std::max<int64_t>(1, div_up(h.M, r.rows)))), dim3(kThreads), 0, s, r);
+  DDP_HIP_TRY(hipGetLastError(), fn);
+  g.a = w.rows, g.lda = h.ldg(), g.a_room = int32_t(h.ldg() - h.K);
+  g.ldb = h.ldw;
+  g.I = h.M, g.K = h.K;
+  g.bounds = w.bounds, g.groups = 1, g.rows = h.M;
+  g.row_of = w.row_of;
+  HeadArgs& a = g.head;
+  a.scale = 1.0f / h.temperature;
+  a.slope = h.temperature;
+  a.vocabulary = h.V;
+  a.targets = h.targets;
+  a.top = std::max(h.top, 1), a.tiles = tiles;
+  a.ids = w.ids, a.weights = w.weights, a.starts = w.starts, a.own_terms = w.own_terms;
+  return DDP_OK;
+}
+
+template <int DT>
+int loss_forward(const Head& h, float* loss, float* lse, void* workspace, const char* fn, hipStream_t s) {
+  const Scratch w = scratch_of(h, workspace);
+  const bool direct = h.w_whole();
+  const Cut c = cut_of(kRowStats, h.M, h.V, h.K, DT, direct, 0, 1);
+  LinearArgs g{};
+  RowsArgs r{};
+  r.loss = loss, r.lse = lse;
+  int st = launch_rows_that_count<DT>(h, w, c.tile, r, g, fn, s);
+  if (st != DDP_OK) return st;
+  g.b = h.w, g.J = h.V;
+  g.head.stats = w.stats, g.head.picked = w.picked;
+  st = launch_groups<DT, kRowStats>(g, c, direct, fn, s);
+  if (st != DDP_OK) return st;
+  const JoinArgs j{w.bounds, w.row_of, h.M, g.tiles_j, g.head, h.temperature * h.temperature, loss, lse};
+  hipLaunchKernelGGL(k_loss_join, dim3(unsigned(div_up(h.M, kJoinRows))), dim3(kThreads), 0, s, j);
+  DDP_HIP_TRY(hipGetLastError(), fn);
+  return DDP_OK;
+}
+
+// The product of g cut like c, its parts joined.
+template <int DT, int DIR>
+int launch_joined(LinearArgs& g, const Cut& c, bool direct, const char* fn, hipStream_t s) {
+  int st = launch_groups<DT, DIR>(g, c, direct, fn, s);
+  if (st != DDP_OK || g.parts == 1) return st;
+  hipLaunchKernelGGL((k_linear_join<DT, DIR, !is_weight(DIR)>), dim3(unsigned(div_up(g.I * div_up(g.J, 8), kThreads))), dim3(kThreads),
+                     0, s, g);
+  DDP_HIP_TRY(hipGetLastError(), fn);
+  return DDP_OK;
+}
+
+template <int DT>
+int loss_backward(const Head& h, const float* lse, const float* dloss, void* dx, int64_t lddx, void* dw, int64_t lddw,
+                  int32_t accumulate, void* workspace, const char* fn, hipStream_t s) {
+  const Scratch w = scratch_of(h, workspace);
+  const Pieces p = pieces_of(h);
+  const bool w_whole = h.w_whole();
+  const int width = tile_of(h, std::min(p.columns, h.V), w_whole);
+  constexpr int64_t ES = DT == DDP_BF16 ? 2 : 4;
+  LinearArgs all{};
+  RowsArgs r{};
+  r.dx = dx, r.lddx = lddx;
+  int st = launch_rows_that_count<DT>(h, w, width, r, all, fn, s);
+  if (st != DDP_OK) return st;
+  all.head.lse = lse, all.head.dloss = dloss;
+  all.terms = dw != nullptr ? h.terms() : 1;
+  if (h.M == 0) dx = nullptr;
+  for (int64_t v0 = 0; v0 < h.V; v0 += p.columns) {
+    const int64_t n = std::min(p.columns, h.V - v0);
+    const char* const weights = static_cast<const char*>(h.w) + v0 * h.ldw * ES;
+    // dz of the piece
+    LinearArgs g = all;
+    g.b = weights, g.J = n;
+    g.c = w.dz, g.ldc = w.lddz, g.term = h.M * w.lddz;
+    g.head.j_base = v0;
+    Cut c;
+    c.tile = width, c.part_k = h.K;
+    st = launch_groups<DT, kRowSlopes>(g, c, w_whole, fn, s);
+    if (st != DDP_OK) return st;
+    const int32_t room = int32_t(round_up(n, 8) - n);
+    if (dx != nullptr) {
+      g = all;
+      g.a = w.dz, g.lda = w.lddz, g.a_room = room;
+      g.b = weights;
+      g.J = h.K, g.K = n;
+      g.c = dx, g.ldc = lddx;
+      g.sums = w.sums, g.first = v0 == 0, g.last = v0 + n == h.V;
+      g.partial = w.partial;
+      st = launch_joined<DT, kInputPiece>(g, cut_of(kInputPiece, h.M, h.K, n, DT, w_whole), w_whole, fn, s);
+      if (st != DDP_OK) return st;
+    }
+    if (dw != nullptr) {
+      g = all;
+      g.a = w.dz, g.lda = w.lddz, g.a_room = room, g.term = h.M * w.lddz * ES;
+      g.b = w.rows, g.ldb = h.ldg(), g.b_room = int32_t(h.ldg() - h.K);
+      g.I = n, g.J = h.K, g.K = h.M;
+      g.c = static_cast<char*>(dw) + v0 * lddw * elem_bytes(h.grad_dtype), g.ldc = lddw;
+      g.grad32 = h.grad_dtype == DDP_FP32, g.accumulate = accumulate;
+      g.partial = w.partial;
+      st = launch_joined<DT, kWeightTerms>(g, cut_of(kWeightTerms, n, h.K, h.M * all.terms, DT, true), true, fn, s);
+      if (st != DDP_OK) return st;
+    }
+  }
+  return DDP_OK;
+}
+
+// The matrices that every call reads, and its scratch.
+struct Checked {
+  Matrix m[12];
+  int n = 0;
+  void add(const Matrix& x) { m[n++] = x; }
+};
+Checked common_matrices(const Head& h) {
+  Checked c;
+  const int eb = elem_bytes(h.dtype);
+  c.add({h.x, h.M, h.K, h.ldx, eb, "x", false, false});
+  c.add({h.w, h.V, h.K, h.ldw, eb, "w", false, false});
+  if (h.top > 0) {
+    c.add({h.ids, h.M, h.top, h.ld_ids, 8, "ids", false, false});
+    c.add({h.teacher, h.M, h.top, h.ld_teacher, elem_bytes(h.teacher_dtype), "teacher", false, false});
+  } else {
+    c.add({h.targets, 1, h.M, h.M, 8, "targets", false, false});
+  }
+  return c;
+}
+
+int forward_call(const char* fn, const Head& h, float* loss, float* lse, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (h.M == 0) return DDP_OK;
+  const int64_t need = scratch_of(h, nullptr).bytes;
+  int st = check_workspace(fn, workspace, workspace_bytes, need);
+  if (st != DDP_OK) return st;
+  Checked c = common_matrices(h);
+  c.add({loss, 1, h.M, h.M, 4, "loss", true, false});
+  c.add({lse, 1, h.M, h.M, 4, "lse", true, false});
+  c.add({workspace, 1, need, need, 1, "workspace", true, false});
+  st = check_matrices(fn, c.m, c.n, -1, -1);
+  if (st != DDP_OK) return st;
+  return h.dtype == DDP_BF16 ? loss_forward<DDP_BF16>(h, loss, lse, workspace, fn, as_stream(stream))
+                             : loss_forward<DDP_FP32>(h, loss, lse, workspace, fn, as_stream(stream));
+}
+
+int backward_call(const char* fn, const Head& h, const float* lse, const float* dloss, void* dx, int64_t lddx, void* dw, int64_t lddw,
+                  int32_t accumulate, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (accumulate != 0 && accumulate != 1) return fail(DDP_EINVAL, std::string(fn) + ": accumulate must be 0 or 1");
+  if (dx == nullptr && dw == nullptr) return DDP_OK;
+  const int64_t need = scratch_of(h, nullptr).bytes;
+  int st = check_workspace(fn, workspace, workspace_bytes, need);
+  if (st != DDP_OK) return st;
+  Checked c = common_matrices(h);
+  c.add({lse, 1, h.M, h.M, 4, "lse", false, false});
+  c.add({dloss, 1, h.M, h.M, 4, "dloss", false, false});
+  c.add({dx, h.M, h.K, lddx, elem_bytes(h.dtype), "dx", true, true});
+  c.add({dw, h.V, h.K, lddw, elem_bytes(h.grad_dtype), "dw", true, true});
+  c.add({workspace, 1, need, need, 1, "workspace", true, false});
+  st = check_matrices(fn, c.m, c.n, -1, -1);
+  if (st != DDP_OK) return st;
+  return h.dtype == DDP_BF16 ? loss_backward<DDP_BF16>(h, lse, dloss, dx, lddx, dw, lddw, accumulate, workspace, fn, as_stream(stream))
+                             : loss_backward<DDP_FP32>(h, lse, dloss, dx, lddx, dw, lddw, accumulate, workspace, fn, as_stream(stream));
+}
+
+Head head_of(int64_t M, int64_t V, int64_t K, int32_t C, int32_t dtype, int32_t grad_dtype, bool backward) {
+  Head h{};
+  h.M = M, h.V = V, h.K = K, h.top = C;
+  h.dtype = dtype, h.grad_dtype = grad_dtype;
+  h.backward = backward;
+  h.temperature = 1.0f;
+  return h;
+}
+
+int workspace_call(const char* fn, int32_t direction, const Head& h, int64_t* bytes) {
+  if (bytes == nullptr) return fail(DDP_EINVAL, std::string(fn) + ": bytes is NULL");
+  *bytes = 0;
+  if (direction != DDP_LOSS_FORWARD && direction != DDP_LOSS_BACKWARD) return fail(DDP_EINVAL, std::string(fn) + ": unknown direction");
+  int st = check_head(fn, h);
+  if (st != DDP_OK) return st;
+  *bytes = scratch_of(h, nullptr).bytes;
+  return DDP_OK;
+}
+
+}  // namespace
+}  // namespace ddp
+
+using namespace ddp;
+
+extern "C" int ddp_cross_entropy_workspace(int32_t direction, int64_t M, int64_t V, int64_t K, int32_t dtype, int32_t grad_dtype,
+                                           int64_t* bytes) {
+  return workspace_call("ddp_cross_entropy_workspace", direction,
+                        head_of(M, V, K, 0, dtype, grad_dtype, direction == DDP_LOSS_BACKWARD), bytes);
+}
+
+extern "C" int ddp_cross_entropy_forward(const void* x, int64_t ldx, const void* w, int64_t ldw, const int64_t* targets, float* loss,
+                                         float* lse, int64_t M, int64_t V, int64_t K, int32_t dtype, void* workspace,
+                                         int64_t workspace_bytes, void* stream) {
+  const char* fn = "ddp_cross_entropy_forward";
+  Head h = head_of(M, V, K, 0, dtype, dtype, false);
+  h.x = x, h.ldx = ldx, h.w = w, h.ldw = ldw, h.targets = targets;
+  int st = check_head(fn, h);
+  if (st != DDP_OK) return st;
+  return forward_call(fn, h, loss, lse, workspace, workspace_bytes, stream);
+}
+
+extern "C" int ddp_cross_entropy_backward(const void* x, int64_t ldx, const void* w, int64_t ldw, const int64_t* targets,
+                                          const float* lse, const float* dloss, void* dx, int64_t lddx, void* dw, int64_t lddw,
+                                          int64_t M, int64_t V, int64_t K, int32_t dtype, int32_t grad_dtype, int32_t accumulate,
+                                          void* workspace, int64_t workspace_bytes, void* stream) {
+  const char* fn = "ddp_cross_entropy_backward";
+  Head h = head_of(M, V, K, 0, dtype, grad_dtype, true);
+  h.x = x, h.ldx = ldx, h.w = w, h.ldw = ldw, h.targets = targets;
+  int st = check_head(fn, h);
+  if (st != DDP_OK) return st;
+  return backward_call(fn, h, lse, dloss, dx, lddx, dw, lddw, accumulate, workspace, workspace_bytes, stream);
+}
+
+extern "C" int ddp_distill_workspace(int32_t direction, int64_t M, int64_t V, int64_t K, int32_t C, int32_t dtype,
+                                     int32_t grad_dtype, int64_t* bytes) {
+  const char* fn = "ddp_distill_workspace";
+  const Head h = head_of(M, V, K, C, dtype, grad_dtype, direction == DDP_LOSS_BACKWARD);
+  if (bytes != nullptr) *bytes = 0;
+  int st = check_top(fn, h);
+  if (st != DDP_OK) return st;
+  return workspace_call(fn, direction, h, bytes);
+}
+
+namespace ddp {
+namespace {
+int distill_head(const char* fn, Head& h, const void* x, int64_t ldx, const void* w, int64_t ldw, const int64_t* ids, int64_t ld_ids,
+                 const void* teacher, int64_t ld_teacher, int32_t teacher_dtype, float temperature) {
+  h.x = x, h.ldx = ldx, h.w = w, h.ldw = ldw;
+  h.ids = ids, h.ld_ids = ld_ids, h.teacher = teacher, h.ld_teacher = ld_teacher, h.teacher_dtype = teacher_dtype;
+  h.temperature = temperature;
+  int st = check_top(fn, h);
+  if (st == DDP_OK) st = check_head(fn, h);
+  if (st != DDP_OK) return st;
+  if (!valid_dtype(teacher_dtype)) return fail(DDP_EINVAL, std::string(fn) + ": unknown teacher_dtype");
+  if (!(temperature > 0.0f) || !(1.0f / temperature > 0.0f) || !(1.0f / temperature < INFINITY))
+    return fail(DDP_EINVAL, std::string(fn) + ": temperature must be positive and finite");
+  return DDP_OK;
+}
+}  // namespace
+}  // namespace ddp
+
+extern "C" int ddp_distill_forward(const void* x, int64_t ldx, const void* w, int64_t ldw, const int64_t* ids, int64_t ld_ids,
+                                   const void* teacher, int64_t ld_teacher, int32_t teacher_dtype, float temperature, float* loss,
+                                   float* lse, int64_t M, int64_t V, int64_t K, int32_t C, int32_t dtype, void* workspace,
+                                   int64_t workspace_bytes, void* stream) {
+  const char* fn = "ddp_distill_forward";
+  Head h = head_of(M, V, K, C, dtype, dtype, false);
+  int st = distill_head(fn, h, x, ldx, w, ldw, ids, ld_ids, teacher, ld_teacher, teacher_dtype, temperature);
+  if (st != DDP_OK) return st;
+  return forward_call(fn, h, loss, lse, workspace, workspace_bytes, stream);
+}
+
+extern "C" int ddp_distill_backward(const void* x, int64_t ldx, const void* w, int64_t ldw, const int64_t* ids, int64_t ld_ids,
+                                    const void* teacher, int64_t ld_teacher, int32_t teacher_dtype, float temperature,
+                                    const float* lse, const float* dloss, void* dx, int64_t lddx, void* dw, int64_t lddw, int64_t M,
+                                    int64_t V, int64_t K, int32_t C, int32_t dtype, int32_t grad_dtype, int32_t accumulate,
+                                    void* workspace, int64_t workspace_bytes, void* stream) {
+  const char* fn = "ddp_distill_backward";
+  Head h = head_of(M, V, K, C, dtype, grad_dtype, true);
+  int st = distill_head(fn, h, x, ldx, w, ldw, ids, ld_ids, teacher, ld_teacher, teacher_dtype, temperature);
+  if (st != DDP_OK) return st;
+  return backward_call(fn, h, lse, dloss, dx, lddx, dw, lddw, accumulate, workspace, workspace_bytes, stream);
+}

@@ -734,6 +734,7 @@ template <int DT, int DIR, int TI, int TJ, int WI, int WJ>
 __device__ __forceinline__ void head_outputs(const LinearArgs& g, f32x16 (&acc)[TI / WI / 32][TJ / WJ / 32], char* lds, int64_t i0,
                                              int64_t j0, int wi, int wj, int wave, int lane, int tile_j) {
   constexpr int FI = TI / WI / 32, FJ = TJ / WJ / 32, THREADS = WI * WJ * 64, PITCH = 32 * FJ + 4;
+  static_assert((WI * WJ * 32 * PITCH + WJ * 2 * TI) * 4 <= (TI + TJ) * 256, "the outputs' rows and statistics fit in LDS");
   const HeadArgs& h = g.head;
   const int half = lane >> 5, in = lane & 31;
   const int width = g.J - j0 - wj < 32 * FJ ? int(g.J - j0 - wj) : 32 * FJ;  // of the wave's columns inside, or less than 0

@@ -146,27 +146,33 @@ int launch_groups(LinearArgs& g, const Cut& c, bool direct, const char* fn, hipS
   constexpr int V = 16 / (DT == DDP_BF16 ? 2 : 4);
   g.parts = c.parts;
   g.part_k = c.part_k;
-  if ((a_along(DIR) ? g.K : g.I) < V || (b_along(DIR) ? g.K : g.J) < V)  // rows shorter than a chunk
-    return launch_group_tiles<DT, DIR, 64, 2, 2, kShort>(g, fn, s);
-  if constexpr (DT == DDP_BF16) {
-    if (c.tile == 256) return launch_group_tiles<DT, DIR, 256, 2, 4, kDirect>(g, fn, s);
+  if constexpr (DIR == kWeightTerms) {  // operands in the library's own room: always whole chunks
+    if (c.tile == 128) return launch_group_tiles<DT, DIR, 128, 2, 2, kDirect>(g, fn, s);
+    if constexpr (DT == DDP_BF16) {
+      if (c.tile == 256) return launch_group_tiles<DT, DIR, 256, 2, 4, kDirect>(g, fn, s);
+    }
+    return launch_group_tiles<DT, DIR, 64, 2, 2, kDirect>(g, fn, s);
+  } else {
+    if ((a_along(DIR) ? g.K : g.I) < V || (b_along(DIR) ? g.K : g.J) < V)  // rows shorter than a chunk
+      return launch_group_tiles<DT, DIR, 64, 2, 2, kShort>(g, fn, s);
+    if constexpr (DT == DDP_BF16) {
+      if (c.tile == 256) return launch_group_tiles<DT, DIR, 256, 2, 4, kDirect>(g, fn, s);
+    }
+    if (c.tile == 128)
+      return direct ? launch_group_tiles<DT, DIR, 128, 2, 2, kDirect>(g, fn, s) : launch_group_tiles<DT, DIR, 128, 2, 2, kAny>(g, fn, s);
+    return direct ? launch_group_tiles<DT, DIR, 64, 2, 2, kDirect>(g, fn, s) : launch_group_tiles<DT, DIR, 64, 2, 2, kAny>(g, fn, s);
   }
-  if (c.tile == 128)
-    return direct ? launch_group_tiles<DT, DIR, 128, 2, 2, kDirect>(g, fn, s) : launch_group_tiles<DT, DIR, 128, 2, 2, kAny>(g, fn, s);
-  return direct ? launch_group_tiles<DT, DIR, 64, 2, 2, kDirect>(g, fn, s) : launch_group_tiles<DT, DIR, 64, 2, 2, kAny>(g, fn, s);
 }
 
-// db (+)= the column sums of `rows` rows of `from` (fp32, or the data).
-int launch_column_sums(const void* from, int32_t from_dtype, int64_t ld, int64_t rows, int64_t N, void* db, int32_t grad_dtype,
-                       int32_t accumulate, const char* fn, hipStream_t s) {
+// db (+)= the column sums of `rows` rows of `from`.
+template <int SRC>
+int launch_column_sums(const void* from, int64_t ld, int64_t rows, int64_t N, void* db, int32_t grad_dtype, int32_t accumulate,
+                       const char* fn, hipStream_t s) {
   launch_blocks(div_up(N, 64), [&](int64_t begin, dim3 grid) {
     const auto launch = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, s, from, ld, rows, N, db, accumulate, begin * 64);
     };
-    if (grad_dtype == DDP_BF16)
-      from_dtype == DDP_BF16 ? launch(k_column_sums<DDP_BF16, DDP_BF16>) : launch(k_column_sums<DDP_FP32, DDP_BF16>);
-    else
-      from_dtype == DDP_BF16 ? launch(k_column_sums<DDP_BF16, DDP_FP32>) : launch(k_column_sums<DDP_FP32, DDP_FP32>);
+    grad_dtype == DDP_BF16 ? launch(k_column_sums<SRC, DDP_BF16>) : launch(k_column_sums<SRC, DDP_FP32>);
   });
   DDP_HIP_TRY(hipGetLastError(), fn);
   return DDP_OK;

@@ -373,8 +373,9 @@ extern "C" int ddp_linear_backward_weight(const void* dz, int64_t lddz, const vo
     sums = g.row_sums, sums_ld = N, sums_rows = int64_t(g.parts) * g.tiles_j;
   }
   if (db == nullptr) return DDP_OK;
-  return launch_column_sums(sums, K == 0 ? dtype : DDP_FP32, sums_ld, sums_rows, N, db, grad_dtype, accumulate,
-                            "ddp_linear_backward_weight: bias launch", s);
+  const char* where = "ddp_linear_backward_weight: bias launch";
+  return K == 0 && dtype == DDP_BF16 ? launch_column_sums<DDP_BF16>(sums, sums_ld, sums_rows, N, db, grad_dtype, accumulate, where, s)
+                                     : launch_column_sums<DDP_FP32>(sums, sums_ld, sums_rows, N, db, grad_dtype, accumulate, where, s);
 }
 
 extern "C" int ddp_act_backward(const void* dy, int64_t lddy, const void* z, int64_t ldz, void* dz, int64_t lddz,

@@ -1,0 +1,365 @@
+"""The losses of an output layer (include/ddp_train.h) against 64-bit formulas
+of the same inputs.
+
+Tolerances, with u = 2^-24, b = 2^-8 and A_ij = sum_k |x w|:
+- z: an fp32 sum of K terms, and the factor 1 / T: e_z = (2 (K + 2) + 2) u A / T;
+- lse: the largest e_z of the row, and relative errors of the sum of exp(z -
+  maximum): each exponential's u times its argument and 4 u, of which the sum takes
+  the mean with weights p (at most ln V), and the additions, 32 in a lane, 4
+  beside, then the tiles': (ln V + 4 + 36 + V / 64) u, and 2 u |lse|;
+- loss: those of lse and z, the sums over entries and 3 u of its terms;
+- p: p (e_z + e_lse + 2 u (|z| + |lse|) + u |z - lse| + 5 u);
+- q of the teacher: (|argument| + C + 8) u of it;
+- dz: |slope| (the errors of p and q, and 3 u (p + q)), and its rounding, b
+  of it in one term and b^2 in two (fp32: none);
+- dx, dw: dz's errors times |w|, |x|, and the fp32 sums, 2 (n + 2) u of the terms'
+  absolute values.
+"""
+
+import math
+
+import pytest
+import torch
+
+import ring_all_reduce_ddp_amd as rar
+from test_gpu_linear import B, DT, U, close, gen, matrix, untouched
+
+pytestmark = pytest.mark.gpu
+
+TINY = 2.0 ** -133
+
+
+class Case:
+    """Inputs of a call: the caller's tensors, and (ids, q) of every row in 64 bits, q's own terms and which rows count."""
+
+    def __init__(self, m, v, k, dtype, top=0, temperature=1.0, ignored=0.2, pad=0, shift=0, seed=1, scale=2.0, teacher="fp32"):
+        g = gen(seed)
+        self.m, self.v, self.k, self.dtype, self.top, self.t = m, v, k, dtype, top, temperature
+        self.x = matrix(g, m, k, dtype, pad, shift=shift)
+        self.w = matrix(g, v, k, dtype, pad, std=scale / math.sqrt(k), shift=shift)
+        self.counts = torch.rand(m, generator=g, device="cuda") >= ignored
+        right = torch.randint(0, v, (m,), generator=g, device="cuda")
+        if top == 0:
+            self.targets = torch.where(self.counts, right, -1 - right)
+            self.ids, self.q = right[:, None], self.counts.double()[:, None]
+            self.own = torch.zeros(m, device="cuda", dtype=torch.float64)
+            self.eq = torch.zeros_like(self.q)
+        else:
+            ids = torch.randint(0, v, (m, top), generator=g, device="cuda")   # some of them twice
+            logits = torch.randn(m, top, generator=g, device="cuda") * 3
+            kept = torch.rand(m, top, generator=g, device="cuda") < 0.8
+            kept[:, 0] = True
+            kept &= self.counts[:, None]
+            by_id = torch.rand(m, top, generator=g, device="cuda") < 0.5      # left out by either
+            pick = lambda t, dt: torch.cat([t, torch.zeros(m, 3, device="cuda", dtype=t.dtype)], 1).to(dt)[:, :top]  # noqa: E731
+            self.ids_in = pick(torch.where(kept | ~by_id, ids, -1 - ids), torch.int64)
+            self.teacher = pick(torch.where(kept | by_id, logits, -math.inf), DT[teacher])
+            t = torch.where(kept, self.teacher.double() / temperature, -math.inf)
+            most = t.amax(1, keepdim=True).clamp(min=-1e30)
+            e = torch.where(kept, torch.exp(t - most), 0.0)
+            self.q = e / e.sum(1, keepdim=True).clamp(min=1e-300)
+            self.own = torch.special.xlogy(self.q, self.q).sum(1)
+            self.eq = self.q * torch.where(kept, (t - most).abs() + top + 8, 0.0) * U
+            self.ids = ids
+        # what rows that do not count hold reaches nothing
+        self.x[~self.counts] = math.nan
+        self.dloss = torch.randn(m, generator=g, device="cuda")
+        self.dloss[~self.counts] = math.nan
+
+    def forward(self, **more):
+        if self.top:
+            return rar.distill_forward(self.x, self.w, self.ids_in, self.teacher, temperature=self.t, **more)
+        return rar.cross_entropy_forward(self.x, self.w, self.targets, **more)
+
+    def backward(self, lse, **more):
+        if self.top:
+            return rar.distill_backward(self.x, self.w, self.ids_in, self.teacher, lse, self.dloss, temperature=self.t, **more)
+        return rar.cross_entropy_backward(self.x, self.w, self.targets, lse, self.dloss, **more)
+
+    def formulas(self):
+        x = torch.where(self.counts[:, None], self.x.double(), 0.0)
+        w = self.w.double()
+        self.x64, self.w64 = x, w
+        c = self.counts
+        z = x @ w.t() / self.t
+        ez = (2 * (self.k + 2) + 2) * U * (x.abs() @ w.abs().t()) / self.t
+        lse = torch.logsumexp(z, 1)
+        self.e_lse = ez.amax(1) + (math.log(self.v) + 40 + self.v / 64 + 2) * U + 2 * U * lse.abs()
+        zt, ezt = z.gather(1, self.ids), ez.gather(1, self.ids)
+        terms = self.q * (lse[:, None] - zt)
+        self.loss = torch.where(c, self.t ** 2 * (self.own + terms.sum(1)), 0.0)
+        self.e_loss = self.t ** 2 * (self.e_lse + (self.q * ezt + self.eq * (lse[:, None] - zt).abs()).sum(1) + (self.top + 4) * U *
+                                     (self.own.abs() + terms.abs().sum(1)) + (self.eq * (1 + self.q.clamp(min=1e-300).log().abs())).sum(1))
+        self.lse = torch.where(c, lse, 0.0)
+        p = torch.exp(z - lse[:, None])
+        ep = p * (ez + self.e_lse[:, None] + 2 * U * (z.abs() + lse.abs()[:, None]) + U * (z - lse[:, None]).abs() + 5 * U)
+        q = torch.zeros_like(p).scatter_add_(1, self.ids, self.q)
+        eq = torch.zeros_like(p).scatter_add_(1, self.ids, self.eq)
+        s = torch.where(c, self.dloss.double() * self.t, 0.0)[:, None]
+        self.dz = s * (p - q)
+        self.e_dz = s.abs() * (ep + eq + 3 * U * (p + q))
+
+    def check_forward(self, loss, lse):
+        close(lse, self.lse, torch.where(self.counts, self.e_lse, 0.0), "fp32", "lse")
+        close(loss, self.loss, torch.where(self.counts, self.e_loss, 0.0), "fp32", "loss")
+
+    def check_backward(self, dx, dw, grads, old=None):
+        wide = self.dtype == "fp32"
+        e_dz = self.e_dz + (0 if wide else B * self.dz.abs() + TINY)
+        e_dz *= self.counts[:, None]
+        if dx is not None:
+            tol = e_dz @ self.w64.abs() + 2 * (self.v + 8) * U * (self.dz.abs() @ self.w64.abs())
+            close(dx, self.dz @ self.w64, tol, self.dtype, "dx")
+        if dw is not None:
+            r = 0 if wide else B * B if grads == "fp32" else B
+            e_dz = (self.e_dz + r * self.dz.abs() + (0 if wide else TINY)) * self.counts[:, None]
+            want = self.dz.t() @ self.x64
+            tol = e_dz.t() @ self.x64.abs() + 2 * (2 * self.m + 2) * U * (self.dz.abs().t() @ self.x64.abs())
+            if old is not None:
+                want = want + old
+                tol = tol + U * want.abs()
+            close(dw, want, tol, grads, "dw")
+
+
+# M, V, K: single elements, odd sizes, rows shorter than 16 bytes, sums cut into parts, tiles' edges
+SIZES = [(1, 1, 1), (1, 700, 64), (3, 7, 5), (2, 5, 72), (64, 1009, 96), (130, 257, 264), (65, 3, 40), (33, 4100, 71), (257, 1000, 520),
+         (40, 30, 2049), (700, 90, 3)]
+LAYOUTS = [(0, 0), (8, 0), (3, 1)]
+
+
+def run_case(c, grads, accumulate, pad, shift, out_given=True):
+    loss, lse = c.forward()
+    c.formulas()
+    c.check_forward(loss, lse)
+    g = gen(9)
+    dw = matrix(g, c.v, c.k, grads, pad, shift=shift)
+    old = dw.double() if accumulate else None
+    if not accumulate:
+        dw.fill_(math.nan)
+    dx = matrix(g, c.m, c.k, c.dtype, pad, shift=shift) if out_given else None
+    lse[~c.counts] = math.nan
+    dx = c.backward(lse, dw=dw, accumulate=accumulate, out=dx)
+    c.check_backward(dx, dw, grads, old)
+    assert bool((dx[~c.counts] == 0).all())
+    if out_given:
+        assert untouched(dx) and untouched(dw)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS, ids=["dense", "aligned rows", "odd rows"])
+@pytest.mark.parametrize("types", [("fp32", "fp32"), ("bf16", "fp32"), ("bf16", "bf16")], ids=str)
+@pytest.mark.parametrize("size", SIZES, ids=str)
+def test_cross_entropy(size, types, layout):
+    i = SIZES.index(size)
+    c = Case(*size, types[0], ignored=[0.0, 0.3, 0.7][i % 3], pad=layout[0], shift=layout[1])
+    run_case(c, types[1], i % 2 == 0, *layout)
+
+
+@pytest.mark.parametrize("layout", [(0, 0), (3, 1)], ids=["dense", "odd rows"])
+@pytest.mark.parametrize("types", [("fp32", "fp32"), ("bf16", "fp32"), ("bf16", "bf16")], ids=str)
+@pytest.mark.parametrize("size", SIZES, ids=str)
+def test_distill(size, types, layout):
+    i = SIZES.index(size)
+    c = Case(*size, types[0], top=[1, 8, 65, 200, 3][i % 5], temperature=[1.0, 2.0, 0.5][i % 3], ignored=[0.0, 0.3, 0.7][i % 3],
+             pad=layout[0], shift=layout[1], teacher=["fp32", "bf16"][i % 2])
+    run_case(c, types[1], i % 2 == 1, *layout)
+
+
+@pytest.mark.parametrize("top", [0, 1024])
+def test_wide_tiles(top):
+    """Enough 256 x 256 tiles for the widest form of every product, with ragged edges."""
+    for m, v, k in ((3000, 9001, 136), (2999, 9000, 3592)):
+        for grads in ("fp32", "bf16"):
+            run_case(Case(m, v, k, "bf16", top=top, ignored=0.1, pad=8), grads, grads == "fp32", 8, 0)
+
+
+@pytest.mark.parametrize("dtype, grads", [("fp32", "fp32"), ("bf16", "fp32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("top", [0, 5])
+def test_pieces_of_the_vocabulary(dtype, grads, top):
+    run_case(Case(40000, 9003, 24, dtype, top=top, ignored=0.05), grads, True, 0, 0)
+
+
+@pytest.mark.parametrize("which", ["dx", "dw"])
+def test_one_gradient_alone(which):
+    c = Case(100, 300, 72, "bf16", ignored=0.2)
+    _, lse = c.forward()
+    c.formulas()
+    dw = torch.empty(300, 72, device="cuda") if which == "dw" else None
+    dx = c.backward(lse, dw=dw, need_dx=which == "dx")
+    assert (dx is None) == (which == "dw")
+    c.check_backward(dx, dw, "fp32")
+
+
+def test_no_row_counts():
+    for top in (0, 4):
+        c = Case(70, 300, 40, "bf16", top=top, ignored=2.0)
+        loss, lse = c.forward()
+        assert bool((loss == 0).all()) and bool((lse == 0).all())
+        dw = torch.full((300, 40), 3.0, device="cuda")
+        dx = c.backward(lse, dw=dw, accumulate=True)
+        assert bool((dx == 0).all()) and bool((dw == 3).all())
+        c.backward(lse, dw=dw)
+        assert bool((dw == 0).all())
+
+
+def test_no_rows():
+    x, w = torch.empty(0, 8, device="cuda"), torch.ones(5, 8, device="cuda")
+    t, f = torch.empty(0, dtype=torch.int64, device="cuda"), torch.empty(0, device="cuda")
+    loss, lse = rar.cross_entropy_forward(x, w, t)
+    assert loss.shape == lse.shape == (0,)
+    dw = torch.ones(5, 8, device="cuda")
+    assert rar.cross_entropy_backward(x, w, t, f, f, dw=dw, accumulate=True).shape == (0, 8)
+    assert bool((dw == 1).all())
+    rar.cross_entropy_backward(x, w, t, f, f, dw=dw)
+    assert bool((dw == 0).all())
+    ids, logits = torch.empty(0, 3, dtype=torch.int64, device="cuda"), torch.empty(0, 3, device="cuda")
+    assert rar.distill_forward(x, w, ids, logits)[0].shape == (0,)
+    rar.distill_backward(x, w, ids, logits, f, f, dw=dw)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_large_and_equal_logits(dtype):
+    """Logits near +-1e4 (an exponential of them overflows), and a vocabulary of equal ones."""
+    x = torch.full((3, 8), 36.0, device="cuda").to(DT[dtype])
+    x[1] = -36.0
+    w = torch.zeros(300, 8, device="cuda").to(DT[dtype])
+    w[7] = 36.0
+    t = torch.tensor([7, 7, 9], device="cuda")
+    loss, lse = rar.cross_entropy_forward(x, w, t)
+    big = 36.0 * 36.0 * 8
+    want = torch.tensor([0.0, math.log(299) + big, big])
+    assert bool(((loss.cpu() - want).abs() <= 1e-6 * want + 1e-6).all()), loss
+    dw = torch.empty(300, 8, device="cuda")
+    dx = rar.cross_entropy_backward(x, w, t, lse, torch.ones(3, device="cuda"), dw=dw)
+    assert bool(torch.isfinite(dx).all()) and bool(torch.isfinite(dw).all())
+    zero = torch.zeros_like(x)
+    loss, lse = rar.cross_entropy_forward(zero, w, t)
+    assert bool(((loss.cpu() - math.log(300)).abs() <= 20 * U * math.log(300)).all())
+
+
+def test_entries_that_are_not_valid_make_their_row_nan():
+    g = gen(3)
+    m, v, k = 70, 300, 40
+    x, w = matrix(g, m, k, "bf16"), matrix(g, v, k, "bf16")
+    t = torch.randint(0, v, (m,), generator=g, device="cuda")
+    t[3], t[60], t[61] = v, 1 << 40, v + 63
+    loss, lse = rar.cross_entropy_forward(x, w, t)
+    dx = rar.cross_entropy_backward(x, w, t, lse, torch.ones(m, device="cuda"))
+    bad = torch.zeros(m, dtype=torch.bool, device="cuda")
+    bad[[3, 60, 61]] = True
+    assert torch.equal(torch.isnan(loss), bad) and torch.equal(torch.isnan(dx).all(1), bad) and torch.equal(torch.isnan(dx).any(1), bad)
+    ids = torch.randint(0, v, (m, 6), generator=g, device="cuda")
+    logits = torch.randn(m, 6, generator=g, device="cuda")
+    ids[3, 2], ids[60, 0] = v, (1 << 32) + 5
+    logits[61, 5] = math.inf
+    logits[5, 1], bad[5] = math.nan, True
+    loss, lse = rar.distill_forward(x, w, ids, logits)
+    dx = rar.distill_backward(x, w, ids, logits, lse, torch.ones(m, device="cuda"))
+    assert torch.equal(torch.isnan(loss), bad) and torch.equal(torch.isnan(dx).all(1), bad) and torch.equal(torch.isnan(dx).any(1), bad)
+
+
+def test_infinities_and_nan_stay_in_their_rows():
+    g = gen(4)
+    x, w = matrix(g, 200, 96, "bf16"), matrix(g, 136, 96, "bf16")
+    x[7, 3], x[150, 90] = math.inf, math.nan
+    t = torch.arange(200, device="cuda") % 136
+    loss, lse = rar.cross_entropy_forward(x, w, t)
+    dx = rar.cross_entropy_backward(x, w, t, lse, torch.ones(200, device="cuda"))
+    want = [i not in (7, 150) for i in range(200)]
+    assert torch.isfinite(loss).tolist() == want and torch.isfinite(dx).all(1).tolist() == want
+
+
+@pytest.mark.parametrize("top", [0, 6])
+def test_gradients_against_differences(top):
+    """Central differences along random directions of x and w, fp32. L = sum(dloss loss) over 5 rows; each loss is off by
+    less than 2e-6 (e_z below 1e-6), so the quotient by 2e-6 sum|dloss| / h; the third derivative of lse along a direction whose
+    effect on z is D is below 2 max|D|^3 / T^3, times T^2."""
+    m, v, k, h = 5, 37, 8, 0.02
+    c = Case(m, v, k, "fp32", top=top, temperature=2.0 if top else 1.0, ignored=0.0, scale=1.0)
+    _, lse = c.forward()
+    dw = torch.empty(v, k, device="cuda")
+    dx = c.backward(lse, dw=dw)
+    g = gen(6)
+    for name, grad in (("x", dx), ("w", dw)):
+        p = getattr(c, name)
+        d = torch.randn(p.shape, generator=g, device="cuda")
+        saved = p.clone()
+
+        def loss(t):
+            setattr(c, name, (saved + t * d).contiguous())
+            return float((c.dloss.double() * c.forward()[0].double()).sum())
+
+        effect = d.double() @ c.w.double().t() if name == "x" else c.x.double() @ d.double().t()
+        tol = 2e-6 * float(c.dloss.abs().sum()) / h + h * h / 3 * float((c.dloss.double().abs() * effect.abs().amax(1) ** 3).sum()) / c.t
+        got = (loss(h) - loss(-h)) / (2 * h)
+        setattr(c, name, saved)
+        assert abs(got - float((grad.double() * d.double()).sum())) <= tol, name
+
+
+@pytest.mark.parametrize("top", [0, 9])
+def test_repeated_calls_streams_and_graphs_give_the_same_bits(top):
+    c = Case(240, 1500, 264, "bf16", top=top, ignored=0.2)
+    c.dloss.nan_to_num_()
+    dw = torch.zeros(1500, 264, device="cuda")
+    dx = torch.zeros(240, 264, device="cuda", dtype=torch.bfloat16)
+    loss, lse = torch.zeros(240, device="cuda"), torch.zeros(240, device="cuda")
+    outs = (loss, lse, dx, dw)
+
+    def step(stream=None):
+        c.forward(loss=loss, lse=lse, stream=stream)
+        c.backward(lse, dw=dw, out=dx, stream=stream)
+        return [a.clone() for a in outs] if stream is None else None
+
+    want = step()
+    assert all(torch.equal(a, b) for a, b in zip(want, step()))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    step(side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, outs))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    which = c.ids_in if top else c.targets
+    for r in range(4):   # the rows that count are found at the replay
+        which[r * 10:r * 10 + 5] = -7
+        want = step()
+        for a in outs:
+            a.fill_(5.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, outs)), r
+
+
+def test_workspaces_and_arguments():
+    c = Case(40, 300, 64, "bf16")
+    need = rar.cross_entropy_workspace(rar.LOSS_FORWARD, 40, 300, 64, torch.bfloat16)
+    ws = torch.full((need + 256,), 7, dtype=torch.uint8, device="cuda")
+    loss, lse = c.forward(workspace=ws[:need])
+    assert bool((ws[need:] == 7).all())
+    assert all(torch.equal(a, b) for a, b in zip((loss, lse), c.forward()))
+    with pytest.raises(rar.DDPError, match="workspace"):
+        c.forward(workspace=ws[:need - 256])
+    need = rar.cross_entropy_workspace(rar.LOSS_BACKWARD, 40, 300, 64, torch.bfloat16, torch.float32)
+    dw = torch.empty(300, 64, device="cuda")
+    ws = torch.full((need + 256,), 7, dtype=torch.uint8, device="cuda")
+    dx = c.backward(lse, dw=dw, workspace=ws[:need])
+    assert bool((ws[need:] == 7).all()) and bool(torch.isfinite(dx).all())
+    with pytest.raises(rar.DDPError, match="workspace"):
+        c.backward(lse, dw=dw, workspace=ws[:need - 256])
+    with pytest.raises(rar.DDPError, match="overlaps"):
+        c.backward(lse, out=c.x)
+    with pytest.raises(ValueError, match="targets"):
+        rar.cross_entropy_forward(c.x, c.w, c.targets.int())
+    with pytest.raises(ValueError, match="dloss"):
+        rar.cross_entropy_backward(c.x, c.w, c.targets, lse, c.dloss[:3])
+    with pytest.raises(ValueError, match="dw"):
+        c.backward(lse, dw=dw[:20])
+    d = Case(40, 300, 64, "bf16", top=4)
+    with pytest.raises(ValueError, match="ids"):
+        rar.distill_forward(d.x, d.w, d.ids_in[:, :0], d.teacher[:, :0])
+    with pytest.raises(ValueError, match="teacher"):
+        rar.distill_forward(d.x, d.w, d.ids_in, d.teacher[:, :3])
+    with pytest.raises(rar.DDPError, match="temperature"):
+        rar.distill_forward(d.x, d.w, d.ids_in, d.teacher, temperature=0.0)
+    with pytest.raises(rar.DDPError, match="C must"):
+        rar.distill_forward(d.x, d.w, d.ids_in.repeat(1, 300), d.teacher.repeat(1, 300))
