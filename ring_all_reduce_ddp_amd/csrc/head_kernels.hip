@@ -27,8 +27,7 @@ constexpr int64_t kMostRows = int64_t(1) << 21, kMostIns = int64_t(1) << 21;
 // ---------------------------------------------------------------- a teacher's top logits
 
 // One wave takes a row: the softmax of its logits / T over the entries that are
-// kept, then each id once, in ascending order, with the weights of its entries
-// added, and where each column tile's entries start.
+// kept, then these in ascending order, and where each column tile's start.
 struct TopArgs {
   const int64_t* ids;
   const void* logits;
@@ -50,11 +49,11 @@ __device__ __forceinline__ float wave_sum(float v) {
 
 template <int DT>
 __global__ __launch_bounds__(64) void k_top(TopArgs g) {
-  extern __shared__ int32_t lds[];
-  int32_t* const ids = lds;                                    // of the kept entries, else -1
-  float* const weights = reinterpret_cast<float*>(lds + g.top);
-  int32_t* const once = lds + 2 * g.top;                       // an id's first entry, else INT_MAX
-  int32_t* const sorted = lds + 3 * g.top;
+  extern __shared__ __attribute__((aligned(16))) int32_t lds[];
+  const int padded = (g.top + 3) / 4 * 4;
+  int32_t* const ids = lds;                                    // of the kept entries, else INT_MAX
+  float* const weights = reinterpret_cast<float*>(lds + padded);
+  int32_t* const sorted = lds + 2 * padded;
   const int lane = int(threadIdx.x);
   const int64_t row = blockIdx.x;
   const int64_t* const id_row = g.ids + row * g.ld_ids;
@@ -69,22 +68,23 @@ __global__ __launch_bounds__(64) void k_top(TopArgs g) {
       bad |= id >= g.vocabulary || !(t < INFINITY);
       most = fmaxf(most, t);
     }
-    ids[k] = !kept ? -1 : id < g.vocabulary ? int32_t(id) : INT_MAX - 1;
+    ids[k] = !kept ? INT_MAX : id < g.vocabulary ? int32_t(id) : INT_MAX - 1;
     weights[k] = t;
   }
+  if (lane < padded - g.top) ids[g.top + lane] = INT_MAX;
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor(most, d));
   bad = __any(bad);
   any = __any(any);
   __syncthreads();
   float sum = 0.0f;
-  for (int k = lane; k < g.top; k += 64) sum += ids[k] >= 0 ? expf((weights[k] - most) * g.inverse) : 0.0f;
+  for (int k = lane; k < g.top; k += 64) sum += ids[k] < INT_MAX ? expf((weights[k] - most) * g.inverse) : 0.0f;
   sum = wave_sum(sum);
   const float log_sum = logf(sum);
   float own = 0.0f;
   for (int k = lane; k < g.top; k += 64) {
     const float log_q = (weights[k] - most) * g.inverse - log_sum;
-    const float q = ids[k] >= 0 ? expf((weights[k] - most) * g.inverse) / sum : 0.0f;
+    const float q = ids[k] < INT_MAX ? expf((weights[k] - most) * g.inverse) / sum : 0.0f;
     if (q > 0.0f) own += q * log_q;
     weights[k] = q;
   }
@@ -95,27 +95,25 @@ __global__ __launch_bounds__(64) void k_top(TopArgs g) {
   }
   if (!any) return;
   __syncthreads();
-  for (int k = lane; k < g.top; k += 64) {
-    bool first = ids[k] >= 0;
-    for (int o = 0; o < k; ++o) first &= ids[o] != ids[k];
-    once[k] = first ? ids[k] : INT_MAX;
-  }
-  __syncthreads();
+  // The kept entries in ascending order of their ids, by counting for each those
+  // before it, four at a time.
   int count = 0;
-  for (int k0 = 0; k0 < g.top; k0 += 64) {
+  for (int k0 = 0; k0 < padded; k0 += 64) {
     const int k = k0 + lane;
-    const bool first = k < g.top && once[k] != INT_MAX;
-    count += int(__popcll(__ballot(first)));
-    if (!first) continue;
-    float q = 0.0f;
+    const int id = k < padded ? ids[k] : INT_MAX;
+    const bool kept = id < INT_MAX;
+    count += int(__popcll(__ballot(kept)));
     int rank = 0;
-    for (int o = 0; o < g.top; ++o) {
-      if (ids[o] == ids[k]) q += weights[o];
-      rank += once[o] < ids[k] ? 1 : 0;
+#pragma unroll 4
+    for (int o = 0; o < padded; o += 4) {
+      const int4 v = *reinterpret_cast<const int4*>(ids + o);
+      rank += (v.x < id || (v.x == id && o < k)) + (v.y < id || (v.y == id && o + 1 < k)) + (v.z < id || (v.z == id && o + 2 < k)) +
+              (v.w < id || (v.w == id && o + 3 < k));
     }
-    sorted[rank] = ids[k];
-    g.out_ids[row * g.top + rank] = ids[k];
-    g.out_weights[row * g.top + rank] = q;
+    if (!kept) continue;
+    sorted[rank] = id;
+    g.out_ids[row * g.top + rank] = id;
+    g.out_weights[row * g.top + rank] = weights[k];
   }
   __syncthreads();
   for (int t = lane; t <= g.tiles; t += 64) {
@@ -147,6 +145,8 @@ struct RowsArgs {
   float* lse;
   void* dx;                // backward: likewise (NULL: not wanted)
   int64_t lddx;
+  const float* dloss;      // backward: of every row
+  float* factor;           // receives the largest magnitude of those that count (1 if that is 0 or not finite)
   __device__ __forceinline__ bool counts(int64_t i) const { return targets != nullptr ? targets[i] >= 0 : counted[i] != 0; }
 };
 
@@ -158,6 +158,22 @@ __global__ __launch_bounds__(kThreads) void k_rows(RowsArgs g) {
   __shared__ int32_t here[kThreads];
   const int lane = int(threadIdx.x) & 63, wave = int(threadIdx.x) >> 6;
   const int64_t first = int64_t(blockIdx.x) * g.rows, end = first + g.rows < g.M ? first + g.rows : g.M;
+  const bool last = blockIdx.x == gridDim.x - 1;
+  if (last && g.factor != nullptr) {
+    __shared__ float most[4];
+    float m = 0.0f;
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < g.M; i += kThreads) {
+      const float d = fabsf(g.dloss[i]);
+      if (g.counts(i)) m = fmaxf(m, d);
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+    if (lane == 0) most[wave] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+    if (threadIdx.x == 0) *g.factor = m > 0.0f && m < INFINITY ? m : 1.0f;
+  }
   int32_t before = 0;
 #pragma unroll 4
   for (int64_t i = threadIdx.x; i < first; i += kThreads) before += g.counts(i) ? 1 : 0;
@@ -183,7 +199,7 @@ __global__ __launch_bounds__(kThreads) void k_rows(RowsArgs g) {
   } else if (inside) {
     if (g.loss != nullptr) g.loss[row] = g.lse[row] = 0.0f;
   }
-  if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) {
+  if (last && threadIdx.x == 0) {
     g.bounds[0] = 0;
     g.bounds[1] = before + number;
   }
@@ -220,12 +236,12 @@ struct JoinArgs {
   float* lse;
 };
 
-constexpr int kJoinRows = 32, kJoinSlices = kThreads / kJoinRows;
+constexpr int kJoinRows = 8, kJoinSlices = kThreads / kJoinRows;
 
-// 32 rows a block, eight threads a row: each an eighth of the column tiles, then
-// of the row's entries, joined in a fixed order.
+// 8 rows a block, 32 threads a row: each a share of the column tiles, then of
+// the row's entries, joined in a fixed order.
 __global__ __launch_bounds__(kThreads) void k_loss_join(JoinArgs g) {
-  __shared__ float part[kJoinSlices][kJoinRows];
+  __shared__ float part[kJoinSlices][kJoinRows + 1];
   const HeadArgs& h = g.head;
   const int in = int(threadIdx.x) % kJoinRows, slice = int(threadIdx.x) / kJoinRows;
   const int64_t number = g.bounds[1], i = int64_t(blockIdx.x) * kJoinRows + in;
@@ -234,28 +250,38 @@ __global__ __launch_bounds__(kThreads) void k_loss_join(JoinArgs g) {
   const auto joined = [&](float mine, auto&& join) {
     part[slice][in] = mine;
     __syncthreads();
-    float v = part[0][in];
 #pragma unroll
-    for (int s = 1; s < kJoinSlices; ++s) v = join(v, part[s][in]);
+    for (int n = kJoinSlices / 2; n > 0; n /= 2) {
+      if (slice < n) part[slice][in] = join(part[slice][in], part[slice + n][in]);
+      __syncthreads();
+    }
+    const float v = part[0][in];
     __syncthreads();
     return v;
   };
   const auto add = [](float a, float b) { return a + b; };
-  float most = -INFINITY;
+  float mine = -INFINITY, sum = 0.0f;
   if (counts) {
-#pragma unroll 4
-    for (int t = slice; t < g.column_tiles; t += kJoinSlices) most = fmaxf(most, h.stats[int64_t(t) * 2 * g.M + i]);
-  }
-  most = joined(most, [](float a, float b) { return fmaxf(a, b); });
-  const float base = most == -INFINITY ? 0.0f : most;
-  float sum = 0.0f;
-  if (counts) {
-#pragma unroll 4
-    for (int t = slice; t < g.column_tiles; t += kJoinSlices) {
-      const float m = h.stats[int64_t(t) * 2 * g.M + i], s = h.stats[(int64_t(t) * 2 + 1) * g.M + i];
-      sum += s * expf((m == -INFINITY ? base : m) - base);
+    for (int t = slice; t < g.column_tiles; t += 4 * kJoinSlices) {
+      float m[4], s[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {  // past the last tile: the last again, unused
+        const int at = t + u * kJoinSlices < g.column_tiles ? t + u * kJoinSlices : g.column_tiles - 1;
+        m[u] = h.stats[int64_t(at) * 2 * g.M + i];
+        s[u] = h.stats[(int64_t(at) * 2 + 1) * g.M + i];
+        if (t + u * kJoinSlices >= g.column_tiles) m[u] = -INFINITY, s[u] = 0.0f;
+      }
+      const float most = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), mine);
+      const float base = most == -INFINITY ? 0.0f : most;
+      sum *= expf((mine == -INFINITY ? base : mine) - base);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) sum += s[u] * expf((m[u] == -INFINITY ? base : m[u]) - base);
+      mine = most;
     }
   }
+  const float most = joined(mine, [](float a, float b) { return fmaxf(a, b); });
+  const float base = most == -INFINITY ? 0.0f : most;
+  sum *= expf((mine == -INFINITY ? base : mine) - base);
   const float lse = base + logf(joined(sum, add));
   const int64_t row = counts ? g.row_of[i] : 0;
   float loss = 0.0f;
@@ -322,7 +348,7 @@ Pieces pieces_of(const Head& h) {
 
 // Where a call's scratch lies; with base NULL, only its size.
 struct Scratch {
-  int64_t* bounds;
+  int64_t* bounds;   // of the one group, then the gradients' factor
   int32_t* row_of;
   char* rows;
   int32_t* counted;
@@ -346,7 +372,7 @@ Scratch scratch_of(const Head& h, void* base) {
     at += round_up(bytes, 256);
   };
   const int64_t eb = elem_bytes(h.dtype), tiles = div_up(h.V, 64);  // of any width
-  take(s.bounds, 16);
+  take(s.bounds, 24);
   take(s.row_of, h.M * 4);
   take(s.rows, h.M * h.ldg() * eb);
   if (h.top > 0) {
@@ -400,7 +426,7 @@ int launch_rows_that_count(const Head& h, const Scratch& w, int width, RowsArgs 
   if (h.top > 0 && h.M > 0) {
     TopArgs t{h.ids, h.teacher, h.ld_ids, h.ld_teacher, h.V, h.top, width, tiles, 1.0f / h.temperature,
               w.ids, w.weights, w.starts, w.own_terms, w.counted};
-    const size_t lds = size_t(h.top) * 16;
+    const size_t lds = size_t(round_up(h.top, 4)) * 12;
     if (h.teacher_dtype == DDP_BF16)
       hipLaunchKernelGGL((k_top<DDP_BF16>), dim3(unsigned(h.M)), dim3(64), lds, s, t);
     else
@@ -470,9 +496,11 @@ int loss_backward(const Head& h, const float* lse, const float* dloss, void* dx,
   LinearArgs all{};
   RowsArgs r{};
   r.dx = dx, r.lddx = lddx;
+  r.dloss = dloss, r.factor = reinterpret_cast<float*>(w.bounds + 2);
   int st = launch_rows_that_count<DT>(h, w, width, r, all, fn, s);
   if (st != DDP_OK) return st;
   all.head.lse = lse, all.head.dloss = dloss;
+  all.factor = r.factor;
   all.terms = dw != nullptr ? h.terms() : 1;
   if (h.M == 0) dx = nullptr;
   for (int64_t v0 = 0; v0 < h.V; v0 += p.columns) {

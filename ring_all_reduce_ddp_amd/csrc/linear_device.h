@@ -62,14 +62,14 @@ struct HeadArgs {
   const int64_t* targets;  // a row's target; or NULL, and its entries:
   int32_t top;             // as many a row at most (1 with targets)
   int32_t tiles;           // column tiles of the vocabulary
-  const int32_t* ids;      // [row][top], ascending, each once
+  const int32_t* ids;      // [row][top], ascending
   const float* weights;    // [row][top]
   const uint16_t* starts;  // [row][tiles + 1], the first entry of a column tile or a later one
   const float* own_terms;  // [row], NaN where an entry is not valid
   float* stats;            // row statistics: [column tile][2][compact row]: maximum, sum of exp(z - maximum)
   float* picked;           // row statistics: [row][top], z of the entries
   const float* lse;        // row slopes: [row]
-  const float* dloss;      // row slopes: [row]
+  const float* dloss;      // row slopes: [row]; dz is relative to the largest of them, `factor`
 };
 
 struct LinearArgs {
@@ -109,11 +109,13 @@ struct LinearArgs {
   float* sums;             // input pieces: the sum over pieces, fp32 (NULL: one piece)
   int32_t first, last;     // input pieces: whether this is the first, the last piece
   const int32_t* row_of;   // where the compact rows come from
+  const float* factor;     // input pieces, weight terms: the sums' factor, on the device
   HeadArgs head;
 };
 
 // Products beside the linear layer's three directions.
 constexpr int kRowStats = 3, kRowSlopes = 4, kInputPiece = 5, kWeightTerms = 6;
+constexpr bool one_group(int dir) { return dir >= kRowStats; }  // of grouped products, those that have only one
 constexpr bool is_weight(int dir) { return dir == DDP_LINEAR_BACKWARD_WEIGHT || dir == kWeightTerms; }
 constexpr bool is_head(int dir) { return dir == kRowStats || dir == kRowSlopes; }
 constexpr bool a_along(int dir) { return !is_weight(dir); }
@@ -314,7 +316,15 @@ __device__ __forceinline__ void before_store(const LinearArgs& g, int64_t i, int
       unpack8<DDP_FP32>(x.e, e);
       for (int k = 0; k < 8; ++k) v[k] += e[k];
     }
+    if (g.last) {
+      const float factor = *g.factor;
+      for (int k = 0; k < 8; ++k) v[k] *= factor;
+    }
   } else if constexpr (is_weight(DIR)) {
+    if constexpr (DIR == kWeightTerms) {
+      const float factor = *g.factor;
+      for (int k = 0; k < 8; ++k) v[k] *= factor;
+    }
     if (g.accumulate) {
       if (g.grad32)
         unpack8<DDP_FP32>(x.e, e);
@@ -809,13 +819,13 @@ __device__ __forceinline__ void head_outputs(const LinearArgs& g, f32x16 (&acc)[
       float lse = 0.0f, slope = 0.0f;
       if (counts) {
         lse = h.lse[row];
-        slope = h.slope * h.dloss[row];
+        slope = h.slope * (h.dloss[row] / *g.factor);
         // A target or entry outside the vocabulary makes the row NaN.
         if (h.targets != nullptr ? h.targets[row] >= h.vocabulary : h.own_terms[row] != h.own_terms[row]) lse = NAN;
       }
       each(0.0f, [&](float v) { return slope * exponential<DT>(fmaf(v, h.scale, -lse)); });
       to_lds();
-      for (int k = half; k < entries; k += 2) {
+      for (int k = 0; half == 0 && k < entries; ++k) {  // an id may come again: one lane a row, in order
         const int at = place_of(entry + k);
         if (at < 0 || at >= width) continue;
         const float q = h.targets != nullptr ? 1.0f : h.weights[row * h.top + entry + k];
@@ -889,7 +899,12 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
   // every group's tiles, as groups differ in length (sums grouped).
   int tiles_i = g.tiles_i;
   GroupScan scan;
-  if constexpr (GROUPS && !is_weight(DIR)) tiles_i = tiles_of_groups<TI>(g, scan);
+  if constexpr (GROUPS && one_group(DIR)) {
+    (is_weight(DIR) ? g.K : g.I) = bound_at(g, 1);
+    if (!is_weight(DIR)) tiles_i = int(g.I + TI - 1) / TI;
+  } else if constexpr (GROUPS && !is_weight(DIR)) {
+    tiles_i = tiles_of_groups<TI>(g, scan);
+  }
   const int tiles = tiles_i * g.tiles_j;
   int at = g.begin + int(blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8);
   int group_index = 0;
@@ -897,7 +912,7 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
     const int eighth = (tiles * g.parts + 7) / 8, b = g.begin + int(blockIdx.x);
     if (eighth == 0) return;
     int n = b / 8;
-    if constexpr (is_weight(DIR)) {
+    if constexpr (is_weight(DIR) && !one_group(DIR)) {
       group_index = n / eighth;
       n -= group_index * eighth;
       if (group_index >= g.groups) return;
@@ -912,7 +927,9 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
   const int group = tile / (GROUP * g.tiles_j), in_group = tile % (GROUP * g.tiles_j);
   const int rows = tiles_i - GROUP * group < GROUP ? tiles_i - GROUP * group : GROUP;
   int64_t i0 = int64_t(GROUP * group + in_group % rows) * TI, j0 = int64_t(in_group / rows) * TJ;
-  if constexpr (GROUPS) {
+  if constexpr (GROUPS && one_group(DIR)) {
+    if (is_weight(DIR)) g.part_k = ((g.K + TA::STEP - 1) / TA::STEP + g.parts - 1) / g.parts * TA::STEP;
+  } else if constexpr (GROUPS) {
     // From here on the operands are the group's.
     Group e;
     if constexpr (is_weight(DIR)) {
@@ -936,8 +953,9 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
       g.I = e.rows;
     }
   }
-  const int64_t all_i = GROUPS && is_weight(DIR) ? g.I * g.groups : g.I;      // rows of all groups' C,
-  const int64_t first_i = GROUPS && is_weight(DIR) ? group_index * g.I : 0;   // and this one's first
+  constexpr bool kMany = GROUPS && !one_group(DIR);
+  const int64_t all_i = kMany && is_weight(DIR) ? g.I * g.groups : g.I;      // rows of all groups' C,
+  const int64_t first_i = kMany && is_weight(DIR) ? group_index * g.I : 0;   // and this one's first
   int64_t k0 = part * g.part_k, k1 = k0 + g.part_k < g.K ? k0 + g.part_k : g.K;
   if constexpr (GROUPS) {
     if (k0 > k1) k0 = k1;  // a part of a short group
