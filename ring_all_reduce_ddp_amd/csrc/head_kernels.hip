@@ -329,11 +329,6 @@ struct Head {
   bool w_whole() const { return whole_chunks(w, ldw, V, K, dtype); }
 };
 
-// The tile of the products that make z.
-int tile_of(const Head& h, int64_t columns, bool direct) {
-  return cut_of(kRowStats, h.M, columns, h.K, h.dtype, direct, 0, 1).tile;
-}
-
 // Columns of a piece, and pieces. A piece of dz should lie in the Infinity Cache
 // for the two products that read it, but be long enough that dx's sum over it
 // is worth the pass over dx in fp32 that each piece costs.
@@ -491,13 +486,13 @@ int loss_backward(const Head& h, const float* lse, const float* dloss, void* dx,
   const Scratch w = scratch_of(h, workspace);
   const Pieces p = pieces_of(h);
   const bool w_whole = h.w_whole();
-  const int width = tile_of(h, std::min(p.columns, h.V), w_whole);
+  const Cut c = cut_of(kRowStats, h.M, std::min(p.columns, h.V), h.K, DT, w_whole, 0, 1);  // of the products that make z
   constexpr int64_t ES = DT == DDP_BF16 ? 2 : 4;
   LinearArgs all{};
   RowsArgs r{};
   r.dx = dx, r.lddx = lddx;
   r.dloss = dloss, r.factor = reinterpret_cast<float*>(w.bounds + 2);
-  int st = launch_rows_that_count<DT>(h, w, width, r, all, fn, s);
+  int st = launch_rows_that_count<DT>(h, w, c.tile, r, all, fn, s);
   if (st != DDP_OK) return st;
   all.head.lse = lse, all.head.dloss = dloss;
   all.factor = r.factor;
@@ -511,8 +506,6 @@ int loss_backward(const Head& h, const float* lse, const float* dloss, void* dx,
     g.b = weights, g.J = n;
     g.c = w.dz, g.ldc = w.lddz, g.term = h.M * w.lddz;
     g.head.j_base = v0;
-    Cut c;
-    c.tile = width, c.part_k = h.K;
     st = launch_groups<DT, kRowSlopes>(g, c, w_whole, fn, s);
     if (st != DDP_OK) return st;
     const int32_t room = int32_t(round_up(n, 8) - n);

@@ -101,6 +101,8 @@ struct LinearArgs {
   int32_t groups;
   int64_t rows;           // of x and dz: no bound counts beyond them
   int64_t b_group;        // elements from one group's w to the next one's
+  int32_t spread;         // begin the sums at different steps,
+  int32_t spread_from;    // from the group's on
 
   // Operands with room behind their rows, which holds zeros.
   int32_t a_room, b_room;  // elements of it that belong to the last chunk
@@ -472,12 +474,14 @@ constexpr int32_t kMostRange = 0x0f000000; // of a descriptor, in 16-byte chunks
 // whole (`room` elements behind the last row make its last chunk whole). The
 // descriptor ends with the operand, so a chunk past it reads as zeros; a row of C's side past the operand repeats the last one (its
 // products are not stored).
-template <class TL, bool ALONG, int THREADS>
+template <class TL, bool ALONG, int THREADS, bool TURNED>
 struct DirectLoader {
   const char* p;        // the tile at the current step
   int64_t advance;      // bytes per step
   int32_t left;         // chunks from p to the operand's end
   int32_t k_left;       // terms left
+  int32_t until;        // TURNED: steps to the operand's last one
+  int64_t back;         // and the way back from there
   uint32_t off[TL::N];  // of this lane's chunks, in bytes from p
   int32_t wave;
   u32x4 desc;
@@ -532,6 +536,18 @@ struct DirectLoader {
     p += advance;
     left -= int32_t(advance / 16);
     k_left -= TL::STEP;
+    if (TURNED && --until == 0) {
+      p -= back;
+      left += int32_t(back / 16);
+    }
+    describe();
+  }
+  // Starts at step `first` of `steps` and comes back to the others at the end.
+  __device__ __forceinline__ void turn_to(int32_t first, int32_t steps) {
+    back = steps * advance;
+    until = steps - first;
+    p += first * advance;
+    left -= int32_t(first * advance / 16);
     describe();
   }
   __device__ __forceinline__ void commit(char*) {}
@@ -641,8 +657,8 @@ struct ShortLoader {
 };
 
 enum Loading { kDirect, kAny, kShort };
-template <int LOAD, int DT, class TL, bool ALONG, int THREADS>
-using LoaderOf = std::conditional_t<LOAD == kDirect, DirectLoader<TL, ALONG, THREADS>,
+template <int LOAD, int DT, class TL, bool ALONG, int THREADS, bool TURNED>
+using LoaderOf = std::conditional_t<LOAD == kDirect, DirectLoader<TL, ALONG, THREADS, TURNED>,
                                     std::conditional_t<LOAD == kAny, AnyLoader<DT, TL, ALONG, THREADS>,
                                                        ShortLoader<DT, TL, ALONG, THREADS>>>;
 
@@ -656,6 +672,21 @@ __device__ __forceinline__ int32_t bound_at(const LinearArgs& g, int32_t e) {
   return b < 0 ? 0 : b < g.rows ? int32_t(b) : int32_t(g.rows);
 }
 
+// Sums, or the largest, of the values (none negative) of the lanes up to each
+// one. Moves within rows of 16 lanes, then rows' last lanes to the rows
+// behind: some 10 cycles each, a tenth of what a shuffle through LDS takes.
+template <class F>
+__device__ __forceinline__ int32_t scan_lanes(int32_t v, F&& join) {
+  v = join(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));  // from 1 lane before, 2, 4, 8 in the row
+  v = join(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));
+  v = join(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));
+  v = join(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));
+  v = join(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));  // lane 15 to row 1, 47 to row 3
+  v = join(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));  // lane 31 to rows 2 and 3
+  return v;
+}
+__device__ __forceinline__ int32_t larger(int32_t a, int32_t b) { return a > b ? a : b; }
+
 // 64 groups from e0 on, one a lane.
 struct GroupScan {
   int32_t begin, rows;     // of this lane's group
@@ -664,27 +695,14 @@ struct GroupScan {
 template <int T>
 __device__ __forceinline__ GroupScan scan_groups(const LinearArgs& g, int32_t e0, int32_t& bound, int32_t& tiles) {
   const int lane = int(threadIdx.x) & 63;
-  int32_t end = e0 + lane < g.groups ? bound_at(g, e0 + lane + 1) : 0;
-  if (end < bound) end = bound;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int32_t o = __shfl_up(end, d);
-    if (lane >= d && o > end) end = o;
-  }
+  const int32_t end = scan_lanes(larger(e0 + lane < g.groups ? bound_at(g, e0 + lane + 1) : 0, bound), larger);
   GroupScan s;
-  s.begin = __shfl_up(end, 1);
-  if (lane == 0) s.begin = bound;
+  s.begin = __builtin_amdgcn_update_dpp(bound, end, 0x138, 0xf, 0xf, false);  // the lane before's
   s.rows = e0 + lane < g.groups ? end - s.begin : 0;
   s.tiles = (s.rows + T - 1) / T;
-  s.until = s.tiles;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int32_t o = __shfl_up(s.until, d);
-    if (lane >= d) s.until += o;
-  }
-  s.until += tiles;
-  bound = __builtin_amdgcn_readfirstlane(__shfl(end, 63));
-  tiles = __builtin_amdgcn_readfirstlane(__shfl(s.until, 63));
+  s.until = tiles + scan_lanes(s.tiles, [](int32_t a, int32_t b) { return a + b; });
+  bound = __builtin_amdgcn_readlane(end, 63);
+  tiles = __builtin_amdgcn_readlane(s.until, 63);
   return s;
 }
 // Tiles of T rows in all groups.
@@ -719,12 +737,10 @@ __device__ __forceinline__ Group group_of_tile(const LinearArgs& g, const GroupS
 }
 // Group number e.
 __device__ __forceinline__ Group group_at(const LinearArgs& g, int32_t e) {
-  int32_t bound = bound_at(g, 0), tiles = 0;
-  for (int32_t e0 = 0;; e0 += 64) {
-    const GroupScan s = scan_groups<1>(g, e0, bound, tiles);
-    if (e >= e0 + 64) continue;
-    return Group{e, __builtin_amdgcn_readlane(s.begin, e - e0), __builtin_amdgcn_readlane(s.rows, e - e0), 0};
-  }
+  int32_t bound = 0;
+  for (int32_t f = int32_t(threadIdx.x) & 63; f <= e; f += 64) bound = larger(bound, bound_at(g, f));
+  const int32_t begin = __builtin_amdgcn_readlane(scan_lanes(bound, larger), 63);
+  return Group{e, begin, larger(bound_at(g, e + 1), begin) - begin, 0};
 }
 
 // ---------------------------------------------------------------- the losses' outputs
@@ -740,11 +756,11 @@ __device__ __forceinline__ Group group_at(const LinearArgs& g, int32_t e) {
 // row slopes: dz = slope dloss (exp(z - lse) - q), by rows through LDS, where q
 // of the few entries is taken off. bf16: in one or two terms, the second what the
 // first's rounding left, which together are off by 2^-16 of dz at most.
-template <int DT, int DIR, int TI, int TJ, int WI, int WJ>
+template <int DT, int DIR, int TI, int TJ, int WI, int WJ, int STAGES>
 __device__ __forceinline__ void head_outputs(const LinearArgs& g, f32x16 (&acc)[TI / WI / 32][TJ / WJ / 32], char* lds, int64_t i0,
                                              int64_t j0, int wi, int wj, int wave, int lane, int tile_j) {
   constexpr int FI = TI / WI / 32, FJ = TJ / WJ / 32, THREADS = WI * WJ * 64, PITCH = 32 * FJ + 4;
-  static_assert((WI * WJ * 32 * PITCH + WJ * 2 * TI) * 4 <= (TI + TJ) * 256, "the outputs' rows and statistics fit in LDS");
+  static_assert((WI * WJ * 32 * PITCH + WJ * 2 * TI) * 4 <= STAGES * (TI + TJ) * 128, "the outputs' rows and statistics fit in LDS");
   const HeadArgs& h = g.head;
   const int half = lane >> 5, in = lane & 31;
   const int width = g.J - j0 - wj < 32 * FJ ? int(g.J - j0 - wj) : 32 * FJ;  // of the wave's columns inside, or less than 0
@@ -869,10 +885,62 @@ __device__ __forceinline__ void head_outputs(const LinearArgs& g, f32x16 (&acc)[
   }
 }
 
+// ---------------------------------------------------------------- a weight gradient's outputs
+
+// A whole tile's sums to C, of type GT, by rows through LDS, 32 rows at a time.
+// Where they are added to what is there, the tile's old values are asked for up
+// to two groups of 32 rows ahead of their use.
+template <int GT, int DIR, int FI, int FJ, int PITCH>
+__device__ __forceinline__ void weight_outputs(const LinearArgs& g, f32x16 (&acc)[FI][FJ], float* mine, int64_t i, int64_t j, int lane) {
+  constexpr int LPR = 4 * FJ, RPP = 64 / LPR, PASSES = 32 / RPP;
+  const float factor = DIR == kWeightTerms ? *g.factor : 1.0f;
+  i += lane / LPR;
+  j += lane % LPR * 8;
+  constexpr int AHEAD = GT == DDP_FP32 && FI > 2 ? 1 : 2;  // more do not fit beside 128 sums a lane
+  Raw8 old[AHEAD][PASSES];
+  const auto load = [&](int a) __attribute__((always_inline)) {
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) old[a % AHEAD][p] = load_raw8<GT>(g.c, (i + 32 * a + p * RPP) * g.ldc + j, 8);
+  };
+  if (g.accumulate) {
+    load(0);
+    if (AHEAD > 1 && FI > 1) load(1);
+  }
+#pragma unroll
+  for (int a = 0; a < FI; ++a) {
+#pragma unroll
+    for (int b = 0; b < FJ; ++b)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<f32x4*>(mine + (lane & 31) * PITCH + 32 * b + 8 * q + 4 * (lane >> 5)) =
+            f32x4{acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
+    __builtin_amdgcn_wave_barrier();
+    float v[PASSES][8];
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      const float* src = mine + (p * RPP + lane / LPR) * PITCH + lane % LPR * 8;
+      const f32x4 lo = *reinterpret_cast<const f32x4*>(src), hi = *reinterpret_cast<const f32x4*>(src + 4);
+      for (int k = 0; k < 4; ++k) v[p][k] = lo[k], v[p][4 + k] = hi[k];
+      if constexpr (DIR == kWeightTerms)
+        for (int k = 0; k < 8; ++k) v[p][k] *= factor;
+      if (g.accumulate) {
+        float e[8];
+        unpack8<GT>(old[a % AHEAD][p], e);
+        for (int k = 0; k < 8; ++k) v[p][k] += e[k];
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (g.accumulate && a + AHEAD < FI) load(a + AHEAD);
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) store_all8<GT, false>(g.c, (i + 32 * a + p * RPP) * g.ldc + j, v[p]);
+  }
+}
+
 // ---------------------------------------------------------------- the product
 
-// Tile TI x TJ of C by WI x WJ waves. GROUPS: of the rows of one group.
-template <int DT, int DIR, int TI, int TJ, int WI, int WJ, int LOAD, bool GROUPS = false>
+// Tile TI x TJ of C by WI x WJ waves. GROUPS: of the rows of one group. STAGES
+// steps are in LDS or on their way there.
+template <int DT, int DIR, int TI, int TJ, int WI, int WJ, int LOAD, bool GROUPS = false, int STAGES = 2>
 __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
   constexpr int THREADS = WI * WJ * 64;
   constexpr int FI = TI / WI / 32, FJ = TJ / WJ / 32;  // 32 x 32 products per wave
@@ -884,12 +952,18 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
   constexpr int SB = 128;
   using TA = Tile<DT, a_along(DIR), TI, SB, THREADS>;
   using TB = Tile<DT, b_along(DIR), TJ, SB, THREADS>;
-  using LA = LoaderOf<LOAD, DT, TA, a_along(DIR), THREADS>;
-  using LB = LoaderOf<LOAD, DT, TB, b_along(DIR), THREADS>;
+  // Rows of a multiple of some KB: what all blocks read at a time, 128 bytes of
+  // each row of B, lies in an eighth of the memory's channels or fewer, so blocks of
+  // few rows, which read B from memory, begin at different steps. A probe that only reads
+  // so, 256 MiB in rows of 4096 bytes: 4.5 TB/s as it was, 5.7 so, 5.9 in rows of 4224.
+  constexpr bool TURNED = GROUPS && LOAD == kDirect && b_along(DIR);
+  using LA = LoaderOf<LOAD, DT, TA, a_along(DIR), THREADS, TURNED>;
+  using LB = LoaderOf<LOAD, DT, TB, b_along(DIR), THREADS, TURNED>;
   constexpr int STAGE = TA::BYTES + TB::BYTES;
   constexpr int PITCH = 32 * FJ + 4;  // floats; the outputs' way through LDS
-  static_assert(WI * WJ * 32 * PITCH * 4 <= 2 * STAGE, "the outputs' rows fit");
-  __shared__ __attribute__((aligned(1024))) char lds[2 * STAGE];
+  static_assert(WI * WJ * 32 * PITCH * 4 <= STAGES * STAGE, "the outputs' rows fit");
+  static_assert(STAGES == 2 || LOAD == kDirect, "loads through registers are one step ahead");
+  __shared__ __attribute__((aligned(1024))) char lds[STAGES * STAGE];
 
   // Blocks go to the 8 XCDs in turn: XCD x takes the tiles of eighth x, in
   // groups of 4 tile rows, so that blocks that share operands share an L2
@@ -943,6 +1017,7 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
     } else {
       e = group_of_tile<TI>(g, scan, GROUP * group + in_group % rows);
       i0 = int64_t(e.tile) * TI;
+      g.spread_from = e.index * 5;
       g.a = static_cast<const char*>(g.a) + e.begin * g.lda * TA::ES;
       g.b = static_cast<const char*>(g.b) + e.index * g.b_group * TA::ES;
       if (DIR == DDP_LINEAR_FORWARD && g.bias != nullptr) g.bias = static_cast<const char*>(g.bias) + e.index * g.J * TA::ES;
@@ -964,6 +1039,10 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
 
   const int lane = int(threadIdx.x) & 63, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
   const int wi = wave / WJ * (TI / WI), wj = wave % WJ * (TJ / WJ);
+  // A group's last tile is seldom full. A wave whose rows lie all behind the
+  // group loads its share and multiplies nothing: the other wave of its SIMD has
+  // the matrix unit to itself.
+  const bool idle = i0 + wi >= g.I;
   f32x16 acc[FI][FJ];
 #pragma unroll
   for (int a = 0; a < FI; ++a)
@@ -986,6 +1065,15 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
     LB lb;
     la.init(static_cast<const char*>(g.a) + (DIR == kWeightTerms ? term * g.term : 0), g.lda, g.I, g.K, i0, k0, k1, g.a_room);
     lb.init(g.b, g.ldb, g.J, g.K, j0, k0, k1, g.b_room);
+    if constexpr (TURNED) {
+      if (g.spread && (k1 - k0) % TA::STEP == 0) {
+        const int32_t first = int32_t(uint32_t(g.spread_from + in_group / rows) * 11u % uint32_t(steps));
+        la.turn_to(first, steps);
+        lb.turn_to(first, steps);
+      } else {
+        la.until = lb.until = 0;
+      }
+    }
     u32x4 fa[2][FI], fb[2][FJ];
     // Fragment m of quarter s: B's first, then A's.
     const auto read_one = [&](const char* stage, int s, int to, int m) {
@@ -1010,11 +1098,14 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
     };
     // Every wave is done with the stage read last, and every wave's loads of
     // the next one have landed.
-    const auto turn = [&] {
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    constexpr int P = FI * FJ, Q = SB / 32, LOADS = TA::N + TB::N;
+    const auto turn = [&](auto more_on_their_way) {
+      if constexpr (STAGES > 2 && decltype(more_on_their_way)::value)  // loads of the steps behind the next one
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((STAGES - 2) * LOADS) : "memory");
+      else
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
       __syncthreads();
     };
-    constexpr int P = FI * FJ, Q = SB / 32, LOADS = TA::N + TB::N;
     const auto load_one = [&](char* stage, int n, auto full) __attribute__((always_inline)) {
       if (n < TA::N)
         la.template load<decltype(full)::value>(stage, n);
@@ -1022,10 +1113,24 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
         lb.template load<decltype(full)::value>(stage + TA::BYTES, n - TA::N);
     };
     int until_rows = tile_j;  // steps until the next one whose rows this block adds up
-    // One step: its products, with the next step's loads under way (MORE; FULL:
-    // all of whose terms exist).
-    const auto one_step = [&](const char* stage, char* next, auto more, auto full) __attribute__((always_inline)) {
-      constexpr bool MORE = decltype(more)::value;
+    // One step: its products, with the loads of a later step into `to` under way
+    // (LOADING; FULL: all of whose terms exist), and the next step's first reads from
+    // `next` (MORE).
+    const auto one_step = [&](const char* stage, const char* next, char* to, auto more, auto loading, auto full)
+                              __attribute__((always_inline)) {
+      constexpr bool MORE = decltype(more)::value, LOADING = decltype(loading)::value;
+      if (GROUPS && !is_weight(DIR) && idle) {
+        if (LOADING) {
+#pragma unroll
+          for (int n = 0; n < LOADS; ++n) load_one(to, n, full);
+          la.end();
+          lb.end();
+          la.commit(to);
+          lb.commit(to + TA::BYTES);
+        }
+        if (MORE) turn(loading);
+        return;
+      }
       const bool sum_now = DIR == DDP_LINEAR_BACKWARD_WEIGHT && until_rows == 0;
       if (DIR == DDP_LINEAR_BACKWARD_WEIGHT) until_rows = sum_now ? g.tiles_j - 1 : until_rows - 1;
       const auto add_rows = [&](int from) {
@@ -1042,10 +1147,10 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
 #pragma unroll
           for (int r = 0; r < FI + FJ; ++r)
             if (r * P / (FI + FJ) == m) read_one(stage, s + 1, (s + 1) & 1, r);
-          if (MORE) {
+          if (LOADING) {
 #pragma unroll
             for (int n = 0; n < LOADS; ++n)
-              if (n * P / LOADS == m && s == 0) load_one(next, n, full);
+              if (n * P / LOADS == m && s == 0) load_one(to, n, full);
             if (s == 1 && m == P / 2) {
               la.end();
               lb.end();
@@ -1054,11 +1159,11 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
         });
         add_rows(s & 1);
       }
-      if (MORE) {
-        la.commit(next);
-        lb.commit(next + TA::BYTES);
-        turn();
+      if (LOADING) {
+        la.commit(to);
+        lb.commit(to + TA::BYTES);
       }
+      if (MORE) turn(loading);
       products((Q - 1) & 1, [&](int m) __attribute__((always_inline)) {
         if (MORE) {
 #pragma unroll
@@ -1071,25 +1176,43 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
     constexpr std::integral_constant<bool, true> yes{};
     constexpr std::integral_constant<bool, false> no{};
 #pragma unroll
-    for (int n = 0; n < LOADS; ++n) load_one(lds, n, no);
-    la.end();
-    lb.end();
+    for (int s = 0; s < STAGES - 1; ++s) {  // past the last step: zeros
+#pragma unroll
+      for (int n = 0; n < LOADS; ++n) load_one(lds + s * STAGE, n, no);
+      la.end();
+      lb.end();
+    }
     la.commit(lds);
     lb.commit(lds + TA::BYTES);
-    turn();
+    turn(yes);
 #pragma unroll
     for (int m = 0; m < FI + FJ; ++m) read_one(lds, 0, 0, m);
     // Two steps at a time while the next ones are whole: the stages are fixed
     // then, and a wave's instructions between its products are few. (They
     // issue one by one, some 5 cycles each, while its products wait.)
-    const int whole_steps = int((k1 - k0) / TA::STEP);
     int t = 0;
-    for (; t + 2 < whole_steps; t += 2) {
-      one_step(lds, lds + STAGE, yes, yes);
-      one_step(lds + STAGE, lds, yes, yes);
+    if constexpr (STAGES == 2) {
+      const int whole_steps = int((k1 - k0) / TA::STEP);
+      for (; t + 2 < whole_steps; t += 2) {
+        one_step(lds, lds + STAGE, lds + STAGE, yes, yes, yes);
+        one_step(lds + STAGE, lds, lds, yes, yes, yes);
+      }
+      for (; t + 1 < steps; ++t) {
+        char* const next = lds + ((t & 1) ^ 1) * STAGE;
+        one_step(lds + (t & 1) * STAGE, next, next, yes, yes, no);
+      }
+      one_step(lds + (t & 1) * STAGE, nullptr, nullptr, no, no, no);
+    } else {
+      // The last steps' turns wait for all that is on its way, the first of them
+      // longer than it has to.
+      int at = 0;  // t % STAGES
+      const auto after = [](int s) { return s + 1 == STAGES ? 0 : s + 1; };
+      for (; t + STAGES - 1 < steps; ++t, at = after(at))
+        one_step(lds + at * STAGE, lds + after(at) * STAGE, lds + (at == 0 ? STAGES - 1 : at - 1) * STAGE, yes, yes, no);
+      for (; t + 1 < steps; ++t, at = after(at)) one_step(lds + at * STAGE, lds + after(at) * STAGE, nullptr, yes, no, no);
+      one_step(lds + at * STAGE, nullptr, nullptr, no, no, no);
+      if (steps < STAGES) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // zeros past the last step may still be on their way
     }
-    for (; t + 1 < steps; ++t) one_step(lds + (t & 1) * STAGE, lds + ((t & 1) ^ 1) * STAGE, yes, no);
-    one_step(lds + (t & 1) * STAGE, nullptr, no, no);
   }
 
   if (DIR == DDP_LINEAR_BACKWARD_WEIGHT && sum_rows) {
@@ -1103,7 +1226,7 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
 
   if constexpr (is_head(DIR)) {
     if (steps > 0) __syncthreads();  // every wave is done with the operands in LDS
-    head_outputs<DT, DIR, TI, TJ, WI, WJ>(g, acc, lds, i0, j0, wi, wj, wave, lane, tile_j);
+    head_outputs<DT, DIR, TI, TJ, WI, WJ, STAGES>(g, acc, lds, i0, j0, wi, wj, wave, lane, tile_j);
     return;
   }
 
@@ -1115,6 +1238,15 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
   float* const mine = reinterpret_cast<float*>(lds) + wave * 32 * PITCH;
   constexpr int LPR = 4 * FJ;        // lanes per row
   constexpr int RPP = 64 / LPR;      // rows per pass
+  if constexpr (GROUPS && is_weight(DIR)) {
+    if (g.parts == 1 && i0 + TI <= g.I && j0 + TJ <= g.J) {
+      if (DT == DDP_BF16 && !g.grad32)
+        weight_outputs<DDP_BF16, DIR, FI, FJ, PITCH>(g, acc, mine, i0 + wi, j0 + wj, lane);
+      else
+        weight_outputs<DDP_FP32, DIR, FI, FJ, PITCH>(g, acc, mine, i0 + wi, j0 + wj, lane);
+      return;
+    }
+  }
   const int64_t i_lane = i0 + wi + lane / LPR;
   const int64_t j = j0 + wj + lane % LPR * 8;
   const int n = g.J - j >= 8 ? 8 : g.J - j > 0 ? int(g.J - j) : 0;

@@ -23,11 +23,18 @@ void launch_blocks(int64_t blocks, F&& launch) {
 // Up to so many rows a forward product goes without tiles (linear_kernels.hip).
 constexpr int kFewRows = 4;
 
+// Flat tiles are for few rows, which read the other operand from memory: 32 rows,
+// 128 columns and four steps of 128 bytes in LDS or on their way, two blocks a CU.
+// (8 rows, 64000 columns of 2048 bf16, with the loss's other launches: 66.7 us, with
+// three steps 70.9, two 72.4, in tiles of 64 75.2.)
+constexpr int kFlatRows = 32, kFlatStages = 4;
+
 // How a product is cut: the tile's side (256 needs direct loads), and in how
 // many parts the sum. Up to kFewRows rows of a forward product go without
 // tiles.
 struct Cut {
   bool few = false;
+  bool flat = false;  // 32 rows
   int tile = 128;
   int32_t parts = 1;
   int64_t part_k = 0;
@@ -62,17 +69,24 @@ Cut cut_by_model(int dir, int32_t I, int32_t J, int32_t K, int dtype, bool direc
   const auto up = [](int64_t a, int64_t b) { return int32_t((a + b - 1) / b); };
   const int32_t row = std::min(a_along(dir) ? K : I, b_along(dir) ? K : J);  // the operands' shorter rows
   const int n_shapes = row < 16 / elem_bytes(dtype) ? 1 : dtype == DDP_BF16 && direct ? 3 : 2;
+  // Few rows: the other operand's bytes are what counts, whatever the type.
+  static const Shape flat{128, 4, 1500, 1900, 1000};
+  const bool flat_rows = (groups > 0 || dir >= kRowStats) && !is_weight(dir) && row >= 16 / elem_bytes(dtype) && I <= kFlatRows * std::max(groups, 1);
   const bool sums = groups > 0 && is_weight(dir);  // the groups are of terms
   const int32_t step = 128 / elem_bytes(dtype), steps = std::max(1, up(sums ? up(K, groups) : K, step));
   const float busy = float(std::min(groups, I));   // groups that have rows
   float least = INFINITY;
-  for (int k = 0; k < n_shapes; ++k) {
-    const Shape& sh = shapes[dtype == DDP_BF16][direct][k];
-    int64_t tiles = int64_t(up(I, sh.tile)) * up(J, sh.tile);
+  for (int k = 0; k < (flat_rows ? 1 : n_shapes); ++k) {
+    const Shape& sh = flat_rows ? flat : shapes[dtype == DDP_BF16][direct][k];
+    const int32_t rows = flat_rows ? kFlatRows : sh.tile;
+    // Short sums are a matter of the outputs' bytes, in which two blocks a CU overlap better
+    // than one (64 experts of 256 rows, 2048 x 4096, added to fp32: 950 us against 1070).
+    if (sh.tile == 256 && is_weight(dir) && (groups > 0 || dir >= kRowStats) && steps <= 8) continue;
+    int64_t tiles = int64_t(up(I, rows)) * up(J, sh.tile);
     if (sums)
       tiles *= groups;
     else if (groups > 1)
-      tiles = int64_t(std::max(busy, float(I) / float(sh.tile) + 0.5f * busy)) * up(J, sh.tile);
+      tiles = int64_t(std::max(busy, float(I) / float(rows) + 0.5f * busy)) * up(J, sh.tile);
     for (int32_t want : {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 28, 32}) {
       if (want > most_parts) break;
       if (want > 1 && (want > steps / 2 || tiles * want > 4 * kCus * sh.fit)) break;
@@ -82,6 +96,7 @@ Cut cut_by_model(int dir, int32_t I, int32_t J, int32_t K, int dtype, bool direc
       if (parts > 1) t += kJoin + float(parts) * kPart + float(parts + 2) * float(I) * float(J) * (4 / kBytesPerCycle);
       if (t >= least) continue;
       least = t;
+      best.flat = flat_rows;
       best.tile = sh.tile;
       best.parts = parts;
       best.part_k = int64_t(per) * step;
@@ -125,16 +140,17 @@ bool whole_chunks(const void* p, int64_t ld, int64_t rows, int64_t contiguous, i
 }
 
 // The tiles of g's groups, in as many blocks as any bounds can ask for.
-template <int DT, int DIR, int T, int WI, int WJ, int LOAD>
+template <int DT, int DIR, int TI, int TJ, int WI, int WJ, int LOAD, int STAGES = 2>
 int launch_group_tiles(LinearArgs& g, const char* fn, hipStream_t s) {
-  const int64_t ti = div_up(g.I, T) + (is_weight(DIR) ? 0 : g.groups - 1), tj = div_up(g.J, T);
+  const int64_t ti = div_up(g.I, TI) + (is_weight(DIR) ? 0 : g.groups - 1), tj = div_up(g.J, TJ);
   const int64_t blocks = is_weight(DIR) ? round_up(ti * tj * g.parts, 8) * g.groups : round_up(ti * tj * g.parts, 8);
   if (blocks >= (int64_t(1) << 30)) return fail(DDP_EINVAL, std::string(fn) + ": too many tiles for one launch");
   g.tiles_i = int32_t(ti);
   g.tiles_j = int32_t(tj);
+  g.spread = g.I <= 2 * TI * g.groups;  // else blocks share what they read of A while they read it
   launch_blocks(blocks, [&](int64_t begin, dim3 grid) {
     g.begin = int32_t(begin);
-    hipLaunchKernelGGL((k_linear<DT, DIR, T, T, WI, WJ, LOAD, true>), grid, dim3(WI * WJ * 64), 0, s, g);
+    hipLaunchKernelGGL((k_linear<DT, DIR, TI, TJ, WI, WJ, LOAD, true, STAGES>), grid, dim3(WI * WJ * 64), 0, s, g);
   });
   DDP_HIP_TRY(hipGetLastError(), fn);
   return DDP_OK;
@@ -147,20 +163,23 @@ int launch_groups(LinearArgs& g, const Cut& c, bool direct, const char* fn, hipS
   g.parts = c.parts;
   g.part_k = c.part_k;
   if constexpr (DIR == kWeightTerms) {  // operands in the library's own room: always whole chunks
-    if (c.tile == 128) return launch_group_tiles<DT, DIR, 128, 2, 2, kDirect>(g, fn, s);
+    if (c.tile == 128) return launch_group_tiles<DT, DIR, 128, 128, 2, 2, kDirect>(g, fn, s);
     if constexpr (DT == DDP_BF16) {
-      if (c.tile == 256) return launch_group_tiles<DT, DIR, 256, 2, 4, kDirect>(g, fn, s);
+      if (c.tile == 256) return launch_group_tiles<DT, DIR, 256, 256, 2, 4, kDirect>(g, fn, s);
     }
-    return launch_group_tiles<DT, DIR, 64, 2, 2, kDirect>(g, fn, s);
+    return launch_group_tiles<DT, DIR, 64, 64, 2, 2, kDirect>(g, fn, s);
   } else {
     if ((a_along(DIR) ? g.K : g.I) < V || (b_along(DIR) ? g.K : g.J) < V)  // rows shorter than a chunk
-      return launch_group_tiles<DT, DIR, 64, 2, 2, kShort>(g, fn, s);
+      return launch_group_tiles<DT, DIR, 64, 64, 2, 2, kShort>(g, fn, s);
+    if (c.flat)
+      return direct ? launch_group_tiles<DT, DIR, kFlatRows, 128, 1, 4, kDirect, kFlatStages>(g, fn, s)
+                    : launch_group_tiles<DT, DIR, kFlatRows, 128, 1, 4, kAny>(g, fn, s);
     if constexpr (DT == DDP_BF16) {
-      if (c.tile == 256) return launch_group_tiles<DT, DIR, 256, 2, 4, kDirect>(g, fn, s);
+      if (c.tile == 256) return launch_group_tiles<DT, DIR, 256, 256, 2, 4, kDirect>(g, fn, s);
     }
     if (c.tile == 128)
-      return direct ? launch_group_tiles<DT, DIR, 128, 2, 2, kDirect>(g, fn, s) : launch_group_tiles<DT, DIR, 128, 2, 2, kAny>(g, fn, s);
-    return direct ? launch_group_tiles<DT, DIR, 64, 2, 2, kDirect>(g, fn, s) : launch_group_tiles<DT, DIR, 64, 2, 2, kAny>(g, fn, s);
+      return direct ? launch_group_tiles<DT, DIR, 128, 128, 2, 2, kDirect>(g, fn, s) : launch_group_tiles<DT, DIR, 128, 128, 2, 2, kAny>(g, fn, s);
+    return direct ? launch_group_tiles<DT, DIR, 64, 64, 2, 2, kDirect>(g, fn, s) : launch_group_tiles<DT, DIR, 64, 64, 2, 2, kAny>(g, fn, s);
   }
 }
 
