@@ -1224,6 +1224,8 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
     }
   }
 
+  if (kMany && is_weight(DIR) && g.K == 0 && g.accumulate && g.parts == 1) return;  // nothing is added
+
   if constexpr (is_head(DIR)) {
     if (steps > 0) __syncthreads();  // every wave is done with the operands in LDS
     head_outputs<DT, DIR, TI, TJ, WI, WJ, STAGES>(g, acc, lds, i0, j0, wi, wj, wave, lane, tile_j);
