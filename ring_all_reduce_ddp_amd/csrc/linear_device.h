@@ -745,6 +745,8 @@ __device__ __forceinline__ Group group_at(const LinearArgs& g, int32_t e) {
 
 // ---------------------------------------------------------------- the losses' outputs
 
+constexpr float kLog2E = 1.44269504f;
+
 // From a tile of x w^T in registers (lane l: row l & 31, columns 8 q + 4 (l >> 5)
 // + r of each 32 x 32 product), so a row's values lie in two lanes:
 //
@@ -794,40 +796,44 @@ __device__ __forceinline__ void head_outputs(const LinearArgs& g, f32x16 (&acc)[
               f32x4{acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
       __builtin_amdgcn_wave_barrier();
     };
-    // f(value) for every value, `outside` in place of those outside C.
-    const auto each = [&](float outside, auto&& f) __attribute__((always_inline)) {
-      const bool whole = width == 32 * FJ;
+    // Values outside C become `outside`.
+    const auto outside_is = [&](float outside) __attribute__((always_inline)) {
+      if (width == 32 * FJ) return;
 #pragma unroll
       for (int b = 0; b < FJ; ++b)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float v = f(acc[a][b][e]);
-          acc[a][b][e] = whole || 32 * b + 8 * (e >> 2) + 4 * half + (e & 3) < width ? v : outside;
-        }
+        for (int e = 0; e < 16; ++e)
+          if (32 * b + 8 * (e >> 2) + 4 * half + (e & 3) >= width) acc[a][b][e] = outside;
+    };
+    // exp(scale v - x), with bf16 data as 2^(u v - y): one step less, and an error
+    // of 2^-24 of the terms.
+    const float u = DT == DDP_BF16 ? h.scale * kLog2E : h.scale;
+    const auto power = [&](float v, float y) __attribute__((always_inline)) {
+      return DT == DDP_BF16 ? __builtin_amdgcn_exp2f(fmaf(v, u, -y)) : expf(fmaf(v, u, -y));
     };
     if constexpr (DIR == kRowStats) {
-      each(-INFINITY, [&](float v) { return v * h.scale; });
+      outside_is(-INFINITY);
       float most = -INFINITY, sum = 0.0f;
 #pragma unroll
       for (int b = 0; b < FJ; ++b)
 #pragma unroll
         for (int e = 0; e < 16; ++e) most = fmaxf(most, acc[a][b][e]);
       most = fmaxf(most, __shfl_xor(most, 32));
-      const float base = most == -INFINITY ? 0.0f : most;
+      const float base = most == -INFINITY ? 0.0f : most * u;
 #pragma unroll
       for (int b = 0; b < FJ; ++b)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) sum += exponential<DT>(acc[a][b][e] - base);
+        for (int e = 0; e < 16; ++e) sum += power(acc[a][b][e], base);
       sum += __shfl_xor(sum, 32);
       if (half == 0) {
-        stats[(wj / (32 * FJ) * 2 + 0) * TI + wi + 32 * a + in] = most;
+        stats[(wj / (32 * FJ) * 2 + 0) * TI + wi + 32 * a + in] = most * h.scale;
         stats[(wj / (32 * FJ) * 2 + 1) * TI + wi + 32 * a + in] = sum;
       }
       if (__any(entries > 0)) {
         to_lds();
         for (int k = half; k < entries; k += 2) {
           const int at = place_of(entry + k);
-          if (at >= 0 && at < width) h.picked[row * h.top + entry + k] = mine[in * PITCH + at];
+          if (at >= 0 && at < width) h.picked[row * h.top + entry + k] = mine[in * PITCH + at] * h.scale;
         }
         __builtin_amdgcn_wave_barrier();
       }
@@ -839,7 +845,12 @@ __device__ __forceinline__ void head_outputs(const LinearArgs& g, f32x16 (&acc)[
         // A target or entry outside the vocabulary makes the row NaN.
         if (h.targets != nullptr ? h.targets[row] >= h.vocabulary : h.own_terms[row] != h.own_terms[row]) lse = NAN;
       }
-      each(0.0f, [&](float v) { return slope * exponential<DT>(fmaf(v, h.scale, -lse)); });
+      if (DT == DDP_BF16) lse *= kLog2E;
+#pragma unroll
+      for (int b = 0; b < FJ; ++b)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[a][b][e] = slope * power(acc[a][b][e], lse);
+      outside_is(0.0f);
       to_lds();
       for (int k = 0; half == 0 && k < entries; ++k) {  // an id may come again: one lane a row, in order
         const int at = place_of(entry + k);
