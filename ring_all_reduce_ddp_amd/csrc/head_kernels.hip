@@ -244,9 +244,11 @@ __global__ __launch_bounds__(kThreads) void k_loss_join(JoinArgs g) {
   __shared__ float part[kJoinSlices][kJoinRows + 1];
   const HeadArgs& h = g.head;
   const int in = int(threadIdx.x) % kJoinRows, slice = int(threadIdx.x) / kJoinRows;
-  const int64_t number = g.bounds[1], i = int64_t(blockIdx.x) * kJoinRows + in;
+  const bool in_place = g.row_of == nullptr;  // all rows are here, also those that do not count
+  const int64_t number = in_place ? g.M : g.bounds[1], i = int64_t(blockIdx.x) * kJoinRows + in;
   if (int64_t(blockIdx.x) * kJoinRows >= number) return;
-  const bool counts = i < number;
+  const int64_t row = i >= number ? 0 : in_place ? i : g.row_of[i];
+  const bool counts = i < number && (!in_place || (h.targets != nullptr ? h.targets[row] >= 0 : h.counted[row] != 0));
   const auto joined = [&](float mine, auto&& join) {
     part[slice][in] = mine;
     __syncthreads();
@@ -283,7 +285,6 @@ __global__ __launch_bounds__(kThreads) void k_loss_join(JoinArgs g) {
   const float base = most == -INFINITY ? 0.0f : most;
   sum *= expf((mine == -INFINITY ? base : mine) - base);
   const float lse = base + logf(joined(sum, add));
-  const int64_t row = counts ? g.row_of[i] : 0;
   float loss = 0.0f;
   if (h.targets != nullptr) {
     if (counts) loss = h.targets[row] < h.vocabulary ? lse - h.picked[row] : NAN;
@@ -298,9 +299,9 @@ __global__ __launch_bounds__(kThreads) void k_loss_join(JoinArgs g) {
     loss = joined(loss, add);
     if (counts) loss = g.factor * (loss + h.own_terms[row]);
   }
-  if (!counts || slice != 0) return;
+  if (i >= number || slice != 0) return;
   g.loss[row] = loss;
-  g.lse[row] = lse;
+  g.lse[row] = counts ? lse : 0.0f;
 }
 
 // ---------------------------------------------------------------- host side
@@ -415,8 +416,10 @@ int check_top(const char* fn, const Head& h) {
 
 // The rows that count, and a teacher's entries; g: the products' arguments that
 // all have in common.
+// (not gathered where they are in_place).
 template <int DT>
-int launch_rows_that_count(const Head& h, const Scratch& w, int width, RowsArgs r, LinearArgs& g, const char* fn, hipStream_t s) {
+int launch_rows_that_count(const Head& h, const Scratch& w, int width, bool in_place, RowsArgs r, LinearArgs& g, const char* fn,
+                           hipStream_t s) {
   const int32_t tiles = int32_t(div_up(h.V, width));
   if (h.top > 0 && h.M > 0) {
     TopArgs t{h.ids, h.teacher, h.ld_ids, h.ld_teacher, h.V, h.top, width, tiles, 1.0f / h.temperature,
@@ -428,42 +431,48 @@ int launch_rows_that_count(const Head& h, const Scratch& w, int width, RowsArgs 
       hipLaunchKernelGGL((k_top<DDP_FP32>), dim3(unsigned(h.M)), dim3(64), lds, s, t);
     DDP_HIP_TRY(hipGetLastError(), fn);
   }
-  r.targets = h.targets, r.counted = w.counted;
-  r.x = h.x, r.ldx = h.ldx, r.M = h.M, r.K = h.K, r.ld_out = h.ldg();
-  r.rows = int32_t(std::min<int64_t>(kThreads, std::max<int64_t>(8, div_up(h.M, 1024))));
-  r.bounds = w.bounds, r.row_of = w.row_of, r.out = w.rows;
-  hipLaunchKernelGGL((k_rows<DT>), dim3(unsigned(std::max<int64_t>(1, div_up(h.M, r.rows)))), dim3(kThreads), 0, s, r);
-  DDP_HIP_TRY(hipGetLastError(), fn);
-  g.a = w.rows, g.lda = h.ldg(), g.a_room = int32_t(h.ldg() - h.K);
+  if (!in_place) {
+    r.targets = h.targets, r.counted = w.counted;
+    r.x = h.x, r.ldx = h.ldx, r.M = h.M, r.K = h.K, r.ld_out = h.ldg();
+    r.rows = int32_t(std::min<int64_t>(kThreads, std::max<int64_t>(8, div_up(h.M, 1024))));
+    r.bounds = w.bounds, r.row_of = w.row_of, r.out = w.rows;
+    hipLaunchKernelGGL((k_rows<DT>), dim3(unsigned(std::max<int64_t>(1, div_up(h.M, r.rows)))), dim3(kThreads), 0, s, r);
+    DDP_HIP_TRY(hipGetLastError(), fn);
+    g.a = w.rows, g.lda = h.ldg(), g.a_room = int32_t(h.ldg() - h.K);
+    g.bounds = w.bounds, g.row_of = w.row_of;
+  } else {
+    g.a = h.x, g.lda = h.ldx;
+  }
   g.ldb = h.ldw;
   g.I = h.M, g.K = h.K;
-  g.bounds = w.bounds, g.groups = 1, g.rows = h.M;
-  g.row_of = w.row_of;
+  g.groups = 1, g.rows = h.M;
   HeadArgs& a = g.head;
   a.scale = 1.0f / h.temperature;
   a.slope = h.temperature;
   a.vocabulary = h.V;
   a.targets = h.targets;
   a.top = std::max(h.top, 1), a.tiles = tiles;
-  a.ids = w.ids, a.weights = w.weights, a.starts = w.starts, a.own_terms = w.own_terms;
+  a.ids = w.ids, a.weights = w.weights, a.starts = w.starts, a.own_terms = w.own_terms, a.counted = w.counted;
   return DDP_OK;
 }
 
 template <int DT>
 int loss_forward(const Head& h, float* loss, float* lse, void* workspace, const char* fn, hipStream_t s) {
   const Scratch w = scratch_of(h, workspace);
-  const bool direct = h.w_whole();
+  // Few rows are a tile or two whether they count or not, and a launch less counts.
+  const bool in_place = h.M <= 64;
+  const bool direct = h.w_whole() && (!in_place || whole_chunks(h.x, h.ldx, h.M, h.K, DT));
   const Cut c = cut_of(kRowStats, h.M, h.V, h.K, DT, direct, 0, 1);
   LinearArgs g{};
   RowsArgs r{};
   r.loss = loss, r.lse = lse;
-  int st = launch_rows_that_count<DT>(h, w, c.tile, r, g, fn, s);
+  int st = launch_rows_that_count<DT>(h, w, c.tile, in_place, r, g, fn, s);
   if (st != DDP_OK) return st;
   g.b = h.w, g.J = h.V;
   g.head.stats = w.stats, g.head.picked = w.picked;
   st = launch_groups<DT, kRowStats>(g, c, direct, fn, s);
   if (st != DDP_OK) return st;
-  const JoinArgs j{w.bounds, w.row_of, h.M, g.tiles_j, g.head, h.temperature * h.temperature, loss, lse};
+  const JoinArgs j{g.bounds, g.row_of, h.M, g.tiles_j, g.head, h.temperature * h.temperature, loss, lse};
   hipLaunchKernelGGL(k_loss_join, dim3(unsigned(div_up(h.M, kJoinRows))), dim3(kThreads), 0, s, j);
   DDP_HIP_TRY(hipGetLastError(), fn);
   return DDP_OK;
@@ -492,7 +501,7 @@ int loss_backward(const Head& h, const float* lse, const float* dloss, void* dx,
   RowsArgs r{};
   r.dx = dx, r.lddx = lddx;
   r.dloss = dloss, r.factor = reinterpret_cast<float*>(w.bounds + 2);
-  int st = launch_rows_that_count<DT>(h, w, c.tile, r, all, fn, s);
+  int st = launch_rows_that_count<DT>(h, w, c.tile, false, r, all, fn, s);
   if (st != DDP_OK) return st;
   all.head.lse = lse, all.head.dloss = dloss;
   all.factor = r.factor;

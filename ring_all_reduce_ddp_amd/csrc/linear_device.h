@@ -66,6 +66,7 @@ struct HeadArgs {
   const float* weights;    // [row][top]
   const uint16_t* starts;  // [row][tiles + 1], the first entry of a column tile or a later one
   const float* own_terms;  // [row], NaN where an entry is not valid
+  const int32_t* counted;  // [row], 0 where a row has no entry
   float* stats;            // row statistics: [column tile][2][compact row]: maximum, sum of exp(z - maximum)
   float* picked;           // row statistics: [row][top], z of the entries
   const float* lse;        // row slopes: [row]
@@ -110,7 +111,7 @@ struct LinearArgs {
   int64_t term;            // bytes from A's first term to its second, or elements of C (row slopes)
   float* sums;             // input pieces: the sum over pieces, fp32 (NULL: one piece)
   int32_t first, last;     // input pieces: whether this is the first, the last piece
-  const int32_t* row_of;   // where the compact rows come from
+  const int32_t* row_of;   // where the compact rows come from (row statistics: NULL, bounds too: all rows, in place)
   const float* factor;     // input pieces, weight terms: the sums' factor, on the device
   HeadArgs head;
 };
@@ -772,8 +773,13 @@ __device__ __forceinline__ void head_outputs(const LinearArgs& g, f32x16 (&acc)[
 #pragma unroll
   for (int a = 0; a < FI; ++a) {
     const int64_t i = i0 + wi + 32 * a + in;
-    const bool counts = i < g.I;
-    const int64_t row = counts ? g.row_of[i] : 0;
+    bool counts = i < g.I;
+    int64_t row = counts ? i : 0;
+    if (DIR == kRowStats && g.row_of == nullptr) {
+      if (counts && h.targets == nullptr) counts = h.counted[row] != 0;
+    } else if (counts) {
+      row = g.row_of[i];
+    }
     // The row's entries in this tile; of a target, `place` is known at once.
     int entry = 0, entries = 0, place = -1;
     if (h.targets != nullptr) {
@@ -985,7 +991,7 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
   int tiles_i = g.tiles_i;
   GroupScan scan;
   if constexpr (GROUPS && one_group(DIR)) {
-    (is_weight(DIR) ? g.K : g.I) = bound_at(g, 1);
+    (is_weight(DIR) ? g.K : g.I) = DIR == kRowStats && g.bounds == nullptr ? g.rows : bound_at(g, 1);
     if (!is_weight(DIR)) tiles_i = int(g.I + TI - 1) / TI;
   } else if constexpr (GROUPS && !is_weight(DIR)) {
     tiles_i = tiles_of_groups<TI>(g, scan);
