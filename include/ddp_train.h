@@ -259,7 +259,8 @@ int ddp_experts_backward_weight(const void* dz, int64_t lddz, const void* x, int
  * rounded to bf16; those of an fp32 dw of bf16 data take it as two bf16 terms,
  * which are off by 2^-16 of it at most.
  *
- * 1 <= V < 2^31, 0 <= M <= 2^21, 1 <= K <= 2^21, M K <= 2^33, 1 <= C <= 1024, T > 0 and finite.
+ * 1 <= V < 2^31, 0 <= M <= 2^21, 1 <= K <= 2^21, M K <= 2^33, M V < 2^42,
+ * 1 <= C <= 1024, T > 0 and finite.
  *
  * ddp_cross_entropy_workspace: bytes of scratch for a direction and sizes on
  * the current device, under the conditions of ddp_linear_workspace; grad_dtype

@@ -405,6 +405,7 @@ int check_head(const char* fn, const Head& h) {
   if (h.V < 1 || h.K < 1) return fail(DDP_EINVAL, std::string(fn) + ": V and K must be at least 1");
   if (h.M > kMostRows || h.K > kMostIns || h.M * h.K > kMostRows * 4096)
     return fail(DDP_EINVAL, std::string(fn) + ": M and K may be 2^21 at most, M * K 2^33");
+  if (h.M > 0 && h.V >= (int64_t(1) << 42) / h.M) return fail(DDP_EINVAL, std::string(fn) + ": M * V must be below 2^42");
   if (h.grad_dtype != h.dtype && h.grad_dtype != DDP_FP32)
     return fail(DDP_EINVAL, std::string(fn) + ": grad_dtype must be the data's or fp32");
   return DDP_OK;
