@@ -40,6 +40,7 @@ int launch_weight(LinearArgs& g, void* db, int32_t grad_dtype, void* workspace, 
   const bool direct = whole_chunks(g.a, g.lda, g.K, g.I, DT) && whole_chunks(g.b, g.ldb, g.K, g.J, DT);
   const Cut c = weight_cut(g.K, g.groups, g.I, g.J, DT, direct);
   const int64_t N = g.groups * g.I;  // of dw, as one matrix
+  g.stream_c = streams(N * g.J, grad_dtype);
   g.partial = static_cast<float*>(workspace);
   if (db != nullptr) g.row_sums = reinterpret_cast<float*>(static_cast<char*>(workspace) + partial_bytes(c, N, g.J));
   int st = launch_groups<DT, DDP_LINEAR_BACKWARD_WEIGHT>(g, c, direct, fn, s);

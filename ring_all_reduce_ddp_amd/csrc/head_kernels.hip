@@ -537,6 +537,7 @@ int loss_backward(const Head& h, const float* lse, const float* dloss, void* dx,
       g.I = n, g.J = h.K, g.K = h.M;
       g.c = static_cast<char*>(dw) + v0 * lddw * elem_bytes(h.grad_dtype), g.ldc = lddw;
       g.grad32 = h.grad_dtype == DDP_FP32, g.accumulate = accumulate;
+      g.stream_c = streams(h.V * h.K, h.grad_dtype);
       g.partial = w.partial;
       st = launch_joined<DT, kWeightTerms>(g, cut_of(kWeightTerms, n, h.K, h.M * all.terms, DT, true), true, fn, s);
       if (st != DDP_OK) return st;

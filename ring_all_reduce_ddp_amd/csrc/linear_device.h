@@ -107,6 +107,7 @@ struct LinearArgs {
 
   // Operands with room behind their rows, which holds zeros.
   int32_t a_room, b_room;  // elements of it that belong to the last chunk
+  int32_t stream_c;        // weight gradients: C passes the caches
   int32_t terms;           // weight terms: 1 or 2
   int64_t term;            // bytes from A's first term to its second, or elements of C (row slopes)
   float* sums;             // input pieces: the sum over pieces, fp32 (NULL: one piece)
@@ -904,20 +905,26 @@ __device__ __forceinline__ void head_outputs(const LinearArgs& g, f32x16 (&acc)[
 
 // ---------------------------------------------------------------- a weight gradient's outputs
 
-// A whole tile's sums to C, of type GT, by rows through LDS, 32 rows at a time.
-// Where they are added to what is there, the tile's old values are asked for up
-// to two groups of 32 rows ahead of their use.
-template <int GT, int DIR, int FI, int FJ, int PITCH>
+// A whole tile's sums to C, of type GT, by rows through LDS, 32 rows at a time: a
+// lane has 16 bytes of C, a row's lanes 128 or 256 together. Where they are added to
+// what is there, the tile's old values are asked for up to two groups of 32 rows ahead of
+// their use. NT: both pass the caches.
+template <int GT, bool NT, int DIR, int FI, int FJ, int PITCH>
 __device__ __forceinline__ void weight_outputs(const LinearArgs& g, f32x16 (&acc)[FI][FJ], float* mine, int64_t i, int64_t j, int lane) {
-  constexpr int LPR = 4 * FJ, RPP = 64 / LPR, PASSES = 32 / RPP;
-  const float factor = DIR == kWeightTerms ? *g.factor : 1.0f;
-  i += lane / LPR;
-  j += lane % LPR * 8;
+  constexpr int W = GT == DDP_FP32 ? 4 : 8, LPR = 32 * FJ / W, RPP = 64 / LPR, PASSES = 32 / RPP;
   constexpr int AHEAD = GT == DDP_FP32 && FI > 2 ? 1 : 2;  // more do not fit beside 128 sums a lane
-  Raw8 old[AHEAD][PASSES];
+  const float factor = DIR == kWeightTerms ? *g.factor : 1.0f;
+  char* const c = static_cast<char*>(g.c) + ((i + lane / LPR) * g.ldc + j + lane % LPR * W) * (16 / W);
+  const int64_t pass = RPP * g.ldc * (16 / W);  // bytes
+  u32x4 old[AHEAD][PASSES];
   const auto load = [&](int a) __attribute__((always_inline)) {
 #pragma unroll
-    for (int p = 0; p < PASSES; ++p) old[a % AHEAD][p] = load_raw8<GT>(g.c, (i + 32 * a + p * RPP) * g.ldc + j, 8);
+    for (int p = 0; p < PASSES; ++p) {
+      if constexpr (GT == DDP_FP32)
+        old[a % AHEAD][p] = load_at<NT, u32x4_at4>(c + (a * PASSES + p) * pass, 0);
+      else
+        old[a % AHEAD][p] = load_at<NT, u32x4_at2>(c + (a * PASSES + p) * pass, 0);
+    }
   };
   if (g.accumulate) {
     load(0);
@@ -932,24 +939,38 @@ __device__ __forceinline__ void weight_outputs(const LinearArgs& g, f32x16 (&acc
         *reinterpret_cast<f32x4*>(mine + (lane & 31) * PITCH + 32 * b + 8 * q + 4 * (lane >> 5)) =
             f32x4{acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
     __builtin_amdgcn_wave_barrier();
-    float v[PASSES][8];
+    float v[PASSES][W];
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
-      const float* src = mine + (p * RPP + lane / LPR) * PITCH + lane % LPR * 8;
-      const f32x4 lo = *reinterpret_cast<const f32x4*>(src), hi = *reinterpret_cast<const f32x4*>(src + 4);
-      for (int k = 0; k < 4; ++k) v[p][k] = lo[k], v[p][4 + k] = hi[k];
+      const float* src = mine + (p * RPP + lane / LPR) * PITCH + lane % LPR * W;
+#pragma unroll
+      for (int q = 0; q < W / 4; ++q) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(src + 4 * q);
+        for (int k = 0; k < 4; ++k) v[p][4 * q + k] = x[k];
+      }
       if constexpr (DIR == kWeightTerms)
-        for (int k = 0; k < 8; ++k) v[p][k] *= factor;
+        for (int k = 0; k < W; ++k) v[p][k] *= factor;
       if (g.accumulate) {
-        float e[8];
-        unpack8<GT>(old[a % AHEAD][p], e);
-        for (int k = 0; k < 8; ++k) v[p][k] += e[k];
+        const u32x4 o = old[a % AHEAD][p];
+        if constexpr (GT == DDP_FP32) {
+          for (int k = 0; k < 4; ++k) v[p][k] += __uint_as_float(o[k]);
+        } else {
+          for (int k = 0; k < 4; ++k) v[p][2 * k] += bf16_lo(o[k]), v[p][2 * k + 1] += bf16_hi(o[k]);
+        }
       }
     }
     __builtin_amdgcn_wave_barrier();
     if (g.accumulate && a + AHEAD < FI) load(a + AHEAD);
+    if (NT) asm volatile("; streamed");  // or the compiler may join these stores with those of the other variant
 #pragma unroll
-    for (int p = 0; p < PASSES; ++p) store_all8<GT, false>(g.c, (i + 32 * a + p * RPP) * g.ldc + j, v[p]);
+    for (int p = 0; p < PASSES; ++p) {
+      char* const to = c + (a * PASSES + p) * pass;
+      if constexpr (GT == DDP_FP32)
+        store4<DDP_FP32, NT>(to, 0, v[p]);
+      else
+        store_all8<DDP_BF16, NT>(to, 0, v[p]);
+    }
+    if (NT) asm volatile("; to here");
   }
 }
 
@@ -1259,10 +1280,17 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
   constexpr int RPP = 64 / LPR;      // rows per pass
   if constexpr (GROUPS && is_weight(DIR)) {
     if (g.parts == 1 && i0 + TI <= g.I && j0 + TJ <= g.J) {
-      if (DT == DDP_BF16 && !g.grad32)
-        weight_outputs<DDP_BF16, DIR, FI, FJ, PITCH>(g, acc, mine, i0 + wi, j0 + wj, lane);
+      const auto outputs = [&](auto nt) __attribute__((always_inline)) {
+        constexpr bool NT = decltype(nt)::value;
+        if (DT == DDP_BF16 && !g.grad32)
+          weight_outputs<DDP_BF16, NT, DIR, FI, FJ, PITCH>(g, acc, mine, i0 + wi, j0 + wj, lane);
+        else
+          weight_outputs<DDP_FP32, NT, DIR, FI, FJ, PITCH>(g, acc, mine, i0 + wi, j0 + wj, lane);
+      };
+      if (g.stream_c)
+        outputs(std::integral_constant<bool, true>{});
       else
-        weight_outputs<DDP_FP32, DIR, FI, FJ, PITCH>(g, acc, mine, i0 + wi, j0 + wj, lane);
+        outputs(std::integral_constant<bool, false>{});
       return;
     }
   }

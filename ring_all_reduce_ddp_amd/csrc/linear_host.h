@@ -139,6 +139,10 @@ bool whole_chunks(const void* p, int64_t ld, int64_t rows, int64_t contiguous, i
          rows * (ld / V) < (int64_t(1) << 31);
 }
 
+// Whether a weight gradient of so many elements passes the caches: it would
+// push out what the other products read again.
+bool streams(int64_t elements, int32_t grad_dtype) { return elements * elem_bytes(grad_dtype) > kInfinityCacheBytes / 3 * 2; }
+
 // The tiles of g's groups, in as many blocks as any bounds can ask for.
 template <int DT, int DIR, int TI, int TJ, int WI, int WJ, int LOAD, int STAGES = 2>
 int launch_group_tiles(LinearArgs& g, const char* fn, hipStream_t s) {
