@@ -35,6 +35,7 @@ constexpr int kFlatRows = 32, kFlatStages = 4;
 struct Cut {
   bool few = false;
   bool flat = false;  // 32 rows
+  bool half = false;  // 128 rows, of 256 columns
   int tile = 128;
   int32_t parts = 1;
   int64_t part_k = 0;
@@ -71,14 +72,19 @@ Cut cut_by_model(int dir, int32_t I, int32_t J, int32_t K, int dtype, bool direc
   const int n_shapes = row < 16 / elem_bytes(dtype) ? 1 : dtype == DDP_BF16 && direct ? 3 : 2;
   // Few rows: the other operand's bytes are what counts, whatever the type.
   static const Shape flat{128, 4, 1500, 1900, 1000};
+  // Groups of some 100 rows leave much of a tile of 256 empty: half tiles of 128 rows and 256 columns,
+  // three steps in LDS or on their way. (4096 rows of 32 groups, 4096 x 2048: 162 us, in tiles of
+  // 256 188; 16384 rows of 64: 480 and 461.)
+  static const Shape half{256, 1, 1350, 1450, 5500};
+  const bool half_rows = groups > 1 && !is_weight(dir) && n_shapes == 3;
   const bool flat_rows = (groups > 0 || dir >= kRowStats) && !is_weight(dir) && row >= 16 / elem_bytes(dtype) && I <= kFlatRows * std::max(groups, 1);
   const bool sums = groups > 0 && is_weight(dir);  // the groups are of terms
   const int32_t step = 128 / elem_bytes(dtype), steps = std::max(1, up(sums ? up(K, groups) : K, step));
   const float busy = float(std::min(groups, I));   // groups that have rows
   float least = INFINITY;
-  for (int k = 0; k < (flat_rows ? 1 : n_shapes); ++k) {
-    const Shape& sh = flat_rows ? flat : shapes[dtype == DDP_BF16][direct][k];
-    const int32_t rows = flat_rows ? kFlatRows : sh.tile;
+  for (int k = 0; k < (flat_rows ? 1 : n_shapes + int(half_rows)); ++k) {
+    const Shape& sh = flat_rows ? flat : k == 3 ? half : shapes[dtype == DDP_BF16][direct][k];
+    const int32_t rows = flat_rows ? kFlatRows : k == 3 ? 128 : sh.tile;
     // Short sums are a matter of the outputs' bytes, in which two blocks a CU overlap better
     // than one (64 experts of 256 rows, 2048 x 4096, added to fp32: 950 us against 1070).
     if (sh.tile == 256 && is_weight(dir) && (groups > 0 || dir >= kRowStats) && steps <= 8) continue;
@@ -97,6 +103,7 @@ Cut cut_by_model(int dir, int32_t I, int32_t J, int32_t K, int dtype, bool direc
       if (t >= least) continue;
       least = t;
       best.flat = flat_rows;
+      best.half = k == 3;
       best.tile = sh.tile;
       best.parts = parts;
       best.part_k = int64_t(per) * step;
@@ -179,6 +186,9 @@ int launch_groups(LinearArgs& g, const Cut& c, bool direct, const char* fn, hipS
       return direct ? launch_group_tiles<DT, DIR, kFlatRows, 128, 1, 4, kDirect, kFlatStages>(g, fn, s)
                     : launch_group_tiles<DT, DIR, kFlatRows, 128, 1, 4, kAny>(g, fn, s);
     if constexpr (DT == DDP_BF16) {
+      if constexpr (!one_group(DIR) && !is_weight(DIR)) {
+        if (c.half) return launch_group_tiles<DT, DIR, 128, 256, 2, 4, kDirect, 3>(g, fn, s);
+      }
       if (c.tile == 256) return launch_group_tiles<DT, DIR, 256, 256, 2, 4, kDirect>(g, fn, s);
     }
     if (c.tile == 128)
