@@ -367,7 +367,7 @@ Scratch scratch_of(const Head& h, void* base) {
     p = base == nullptr ? nullptr : reinterpret_cast<std::remove_reference_t<decltype(p)>>(static_cast<char*>(base) + at);
     at += round_up(bytes, 256);
   };
-  const int64_t eb = elem_bytes(h.dtype), tiles = div_up(h.V, 64);  // of any width
+  const int64_t eb = elem_bytes(h.dtype), tiles = div_up(h.V, h.M <= kFlatRows ? 32 : 64);  // of any width
   take(s.bounds, 24);
   take(s.row_of, h.M * 4);
   take(s.rows, h.M * h.ldg() * eb);
@@ -390,7 +390,7 @@ Scratch scratch_of(const Head& h, void* base) {
     for (int64_t v0 = 0; v0 < h.V; v0 += p.columns) {
       const int64_t n = std::min(p.columns, h.V - v0);
       for (bool direct : {false, true})
-        most = std::max(most, partial_bytes(cut_of(kInputPiece, h.M, h.K, n, h.dtype, direct), h.M, h.K));
+        most = std::max(most, partial_bytes(cut_of(kInputPiece, h.M, h.K, n, h.dtype, direct, 0, 128), h.M, h.K));
       most = std::max(most, partial_bytes(cut_of(kWeightTerms, n, h.K, h.M * h.terms(), h.dtype, true), n, h.K));
     }
     take(s.partial, most);
@@ -527,7 +527,7 @@ int loss_backward(const Head& h, const float* lse, const float* dloss, void* dx,
       g.c = dx, g.ldc = lddx;
       g.sums = w.sums, g.first = v0 == 0, g.last = v0 + n == h.V;
       g.partial = w.partial;
-      st = launch_joined<DT, kInputPiece>(g, cut_of(kInputPiece, h.M, h.K, n, DT, w_whole), w_whole, fn, s);
+      st = launch_joined<DT, kInputPiece>(g, cut_of(kInputPiece, h.M, h.K, n, DT, w_whole, 0, 128), w_whole, fn, s);
       if (st != DDP_OK) return st;
     }
     if (dw != nullptr) {

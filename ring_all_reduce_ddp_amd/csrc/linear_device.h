@@ -409,7 +409,7 @@ struct Tile {
   static_assert(BYTES % (16 * THREADS) == 0, "whole chunks per thread");
 
   static __device__ __forceinline__ int swizzle(int row) {
-    if (ALONG) return (row / (256 / SB)) & (CPR - 1);
+    if (ALONG) return SB > 256 ? row & 15 : (row / (256 / (SB > 256 ? 256 : SB))) & (CPR - 1);
     if (DT != DDP_BF16) return 0;
     return CPR > 8 ? (row & 3) << 2 : (row >> 1 & 1) << 2;  // rows of 128 bytes: two fill the banks as they lie
   }
@@ -760,11 +760,11 @@ constexpr float kLog2E = 1.44269504f;
 // row slopes: dz = slope dloss (exp(z - lse) - q), by rows through LDS, where q
 // of the few entries is taken off. bf16: in one or two terms, the second what the
 // first's rounding left, which together are off by 2^-16 of dz at most.
-template <int DT, int DIR, int TI, int TJ, int WI, int WJ, int STAGES>
+template <int DT, int DIR, int TI, int TJ, int WI, int WJ, int WK, int STAGES>
 __device__ __forceinline__ void head_outputs(const LinearArgs& g, f32x16 (&acc)[TI / WI / 32][TJ / WJ / 32], char* lds, int64_t i0,
-                                             int64_t j0, int wi, int wj, int wave, int lane, int tile_j) {
-  constexpr int FI = TI / WI / 32, FJ = TJ / WJ / 32, THREADS = WI * WJ * 64, PITCH = 32 * FJ + 4;
-  static_assert((WI * WJ * 32 * PITCH + WJ * 2 * TI) * 4 <= STAGES * (TI + TJ) * 128, "the outputs' rows and statistics fit in LDS");
+                                             int64_t j0, int wi, int wj, int wave, int wk, int lane, int tile_j) {
+  constexpr int FI = TI / WI / 32, FJ = TJ / WJ / 32, THREADS = WI * WJ * WK * 64, PITCH = 32 * FJ + 4;
+  static_assert((WI * WJ * 32 * PITCH + WJ * 2 * TI) * 4 <= STAGES * (TI + TJ) * 128 * WK, "the outputs' rows and statistics fit in LDS");
   const HeadArgs& h = g.head;
   const int half = lane >> 5, in = lane & 31;
   const int width = g.J - j0 - wj < 32 * FJ ? int(g.J - j0 - wj) : 32 * FJ;  // of the wave's columns inside, or less than 0
@@ -773,6 +773,7 @@ __device__ __forceinline__ void head_outputs(const LinearArgs& g, f32x16 (&acc)[
   const int64_t column = h.j_base + j0;                                       // of the vocabulary, the tile's first
 #pragma unroll
   for (int a = 0; a < FI; ++a) {
+    if (WK > 1 && wk > 0) break;  // the sums are the first waves'
     const int64_t i = i0 + wi + 32 * a + in;
     bool counts = i < g.I;
     int64_t row = counts ? i : 0;
@@ -977,17 +978,19 @@ __device__ __forceinline__ void weight_outputs(const LinearArgs& g, f32x16 (&acc
 // ---------------------------------------------------------------- the product
 
 // Tile TI x TJ of C by WI x WJ waves. GROUPS: of the rows of one group. STAGES
-// steps are in LDS or on their way there.
-template <int DT, int DIR, int TI, int TJ, int WI, int WJ, int LOAD, bool GROUPS = false, int STAGES = 2>
-__global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
-  constexpr int THREADS = WI * WJ * 64;
+// steps are in LDS or on their way there. WK: as many waves share each part of the
+// tile and take 128 bytes of k each of a step that is as much longer.
+template <int DT, int DIR, int TI, int TJ, int WI, int WJ, int LOAD, bool GROUPS = false, int STAGES = 2, int WK = 1>
+__global__ __launch_bounds__(WI * WJ * WK * 64, 2) void k_linear(LinearArgs g) {
+  constexpr int THREADS = WI * WJ * WK * 64;
   constexpr int FI = TI / WI / 32, FJ = TJ / WJ / 32;  // 32 x 32 products per wave
   // Steps of 128 bytes of k, one on its way while one is multiplied. (Four
   // stages of 64 bytes, three of them on their way, ran 15 % slower: twice the
   // barriers. 4 waves with 128 x 128 products each read a third less from LDS
   // but have nobody to fill their waits: as fast without outputs to speak of,
   // 8192 x 8192 x 2048 input gradient through gelu_tanh 303 us against 269.)
-  constexpr int SB = 128;
+  constexpr int SB = 128 * WK;
+  static_assert(WK == 1 || (GROUPS && b_along(DIR)), "where waves share a part");
   using TA = Tile<DT, a_along(DIR), TI, SB, THREADS>;
   using TB = Tile<DT, b_along(DIR), TJ, SB, THREADS>;
   // Rows of a multiple of some KB: what all blocks read at a time, 128 bytes of
@@ -1000,6 +1003,7 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
   constexpr int STAGE = TA::BYTES + TB::BYTES;
   constexpr int PITCH = 32 * FJ + 4;  // floats; the outputs' way through LDS
   static_assert(WI * WJ * 32 * PITCH * 4 <= STAGES * STAGE, "the outputs' rows fit");
+  static_assert((WK - 1) * TI * TJ * 4 <= STAGES * STAGE, "the sums that waves hand over fit");
   static_assert(STAGES == 2 || LOAD == kDirect, "loads through registers are one step ahead");
   __shared__ __attribute__((aligned(1024))) char lds[STAGES * STAGE];
 
@@ -1075,7 +1079,8 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
   }
   const int steps = int((k1 - k0 + TA::STEP - 1) / TA::STEP);
 
-  const int lane = int(threadIdx.x) & 63, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+  const int lane = int(threadIdx.x) & 63, all_wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+  const int wave = WK > 1 ? all_wave % (WI * WJ) : all_wave, wk = WK > 1 ? all_wave / (WI * WJ) : 0;
   const int wi = wave / WJ * (TI / WI), wj = wave % WJ * (TJ / WJ);
   // A group's last tile is seldom full. A wave whose rows lie all behind the
   // group loads its share and multiplies nothing: the other wave of its SIMD has
@@ -1116,9 +1121,9 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
     // Fragment m of quarter s: B's first, then A's.
     const auto read_one = [&](const char* stage, int s, int to, int m) {
       if (m < FJ)
-        fb[to][m] = TB::fragment(stage + TA::BYTES, wj, m, s, lane);
+        fb[to][m] = TB::fragment(stage + TA::BYTES, wj, m, s + 4 * wk, lane);
       else
-        fa[to][m - FJ] = TA::fragment(stage, wi, m - FJ, s, lane);
+        fa[to][m - FJ] = TA::fragment(stage, wi, m - FJ, s + 4 * wk, lane);
     };
     // The products of the fragments in `from`, with step(m) after the m-th. The
     // order written is the schedule: left to itself, the compiler moves the
@@ -1136,7 +1141,7 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
     };
     // Every wave is done with the stage read last, and every wave's loads of
     // the next one have landed.
-    constexpr int P = FI * FJ, Q = SB / 32, LOADS = TA::N + TB::N;
+    constexpr int P = FI * FJ, Q = SB / WK / 32, LOADS = TA::N + TB::N;
     const auto turn = [&](auto more_on_their_way) {
       if constexpr (STAGES > 2 && decltype(more_on_their_way)::value)  // loads of the steps behind the next one
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((STAGES - 2) * LOADS) : "memory");
@@ -1264,9 +1269,27 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
 
   if (kMany && is_weight(DIR) && g.K == 0 && g.accumulate && g.parts == 1) return;  // nothing is added
 
+  if constexpr (WK > 1) {  // the first waves add up what the others have
+    __syncthreads();
+    f32x16* const sums = reinterpret_cast<f32x16*>(lds) + lane;
+#pragma unroll
+    for (int a = 0; a < FI; ++a)
+#pragma unroll
+      for (int b = 0; b < FJ; ++b)
+        if (wk > 0) sums[(((wk - 1) * WI * WJ + wave) * FI * FJ + a * FJ + b) * 64] = acc[a][b];
+    __syncthreads();
+    if (wk == 0) {
+      for (int o = 0; o < WK - 1; ++o)
+#pragma unroll
+        for (int a = 0; a < FI; ++a)
+#pragma unroll
+          for (int b = 0; b < FJ; ++b) acc[a][b] += sums[((o * WI * WJ + wave) * FI * FJ + a * FJ + b) * 64];
+    }
+  }
+
   if constexpr (is_head(DIR)) {
     if (steps > 0) __syncthreads();  // every wave is done with the operands in LDS
-    head_outputs<DT, DIR, TI, TJ, WI, WJ, STAGES>(g, acc, lds, i0, j0, wi, wj, wave, lane, tile_j);
+    head_outputs<DT, DIR, TI, TJ, WI, WJ, WK, STAGES>(g, acc, lds, i0, j0, wi, wj, wave, wk, lane, tile_j);
     return;
   }
 
@@ -1275,6 +1298,7 @@ __global__ __launch_bounds__(WI * WJ * 64, 2) void k_linear(LinearArgs g) {
   // back eight columns to a lane, so that loads and stores cover whole lines.
   // Each wave has its own part of LDS.
   if (steps > 0) __syncthreads();  // every wave is done with the operands there
+  if (WK > 1 && wk > 0) return;
   float* const mine = reinterpret_cast<float*>(lds) + wave * 32 * PITCH;
   constexpr int LPR = 4 * FJ;        // lanes per row
   constexpr int RPP = 64 / LPR;      // rows per pass

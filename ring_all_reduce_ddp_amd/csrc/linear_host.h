@@ -35,6 +35,7 @@ constexpr int kFlatRows = 32, kFlatStages = 4;
 struct Cut {
   bool few = false;
   bool flat = false;  // 32 rows
+  bool deep = false;  // 32 rows and columns, four waves along the sum
   bool half = false;  // 128 rows, of 256 columns
   int tile = 128;
   int32_t parts = 1;
@@ -82,8 +83,10 @@ Cut cut_by_model(int dir, int32_t I, int32_t J, int32_t K, int dtype, bool direc
   const int32_t step = 128 / elem_bytes(dtype), steps = std::max(1, up(sums ? up(K, groups) : K, step));
   const float busy = float(std::min(groups, I));   // groups that have rows
   float least = INFINITY;
-  for (int k = 0; k < (flat_rows ? 1 : n_shapes + int(half_rows)); ++k) {
-    const Shape& sh = flat_rows ? flat : k == 3 ? half : shapes[dtype == DDP_BF16][direct][k];
+  static const Shape deep{32, 2, 2600, 2600, 1500};
+  for (int k = 0; k < (flat_rows ? b_along(dir) ? 2 : 1 : n_shapes + int(half_rows)); ++k) {
+    const bool is_deep = flat_rows && k == 1;
+    const Shape& sh = is_deep ? deep : flat_rows ? flat : k == 3 ? half : shapes[dtype == DDP_BF16][direct][k];
     const int32_t rows = flat_rows ? kFlatRows : k == 3 ? 128 : sh.tile;
     // Short sums are a matter of the outputs' bytes, in which two blocks a CU overlap better
     // than one (64 experts of 256 rows, 2048 x 4096, added to fp32: 950 us against 1070).
@@ -93,16 +96,18 @@ Cut cut_by_model(int dir, int32_t I, int32_t J, int32_t K, int dtype, bool direc
       tiles *= groups;
     else if (groups > 1)
       tiles = int64_t(std::max(busy, float(I) / float(rows) + 0.5f * busy)) * up(J, sh.tile);
-    for (int32_t want : {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 28, 32}) {
+    for (int32_t want : {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 28, 32, 48, 64, 96, 128}) {
       if (want > most_parts) break;
       if (want > 1 && (want > steps / 2 || tiles * want > 4 * kCus * sh.fit)) break;
       const int32_t per = up(steps, want), parts = up(steps, per), on_cu = up(tiles * parts, kCus);
-      float t = std::max(float(up(on_cu, sh.fit)) * (kStart + float(per) * sh.alone),
-                         kStart + float(on_cu) * (float(per) * sh.step + sh.ends));
+      const int32_t rounds = is_deep ? up(per, 4) : per;
+      float t = std::max(float(up(on_cu, sh.fit)) * (kStart + float(rounds) * sh.alone),
+                         kStart + float(on_cu) * (float(rounds) * sh.step + sh.ends));
       if (parts > 1) t += kJoin + float(parts) * kPart + float(parts + 2) * float(I) * float(J) * (4 / kBytesPerCycle);
       if (t >= least) continue;
       least = t;
       best.flat = flat_rows;
+      best.deep = is_deep;
       best.half = k == 3;
       best.tile = sh.tile;
       best.parts = parts;
@@ -120,7 +125,7 @@ Cut cut_of(int dir, int64_t I, int64_t J, int64_t K, int dtype, bool direct, int
     Cut cut;
   };
   static thread_local Seen seen[64];
-  const int64_t key[4] = {I, J, K, (int64_t(groups) * 64 + most_parts) * 32 + dir * 4 + dtype * 2 + int(direct)};
+  const int64_t key[4] = {I, J, K, (int64_t(groups) * 256 + most_parts) * 32 + dir * 4 + dtype * 2 + int(direct)};
   const uint64_t h = (uint64_t(I) * 31 + uint64_t(J) * 7 + uint64_t(K)) * 8 + uint64_t(key[3]);
   Seen& s = seen[(h ^ (h >> 7)) % 64];
   if (!std::equal(key, key + 4, s.key)) {
@@ -151,7 +156,7 @@ bool whole_chunks(const void* p, int64_t ld, int64_t rows, int64_t contiguous, i
 bool streams(int64_t elements, int32_t grad_dtype) { return elements * elem_bytes(grad_dtype) > kInfinityCacheBytes / 3 * 2; }
 
 // The tiles of g's groups, in as many blocks as any bounds can ask for.
-template <int DT, int DIR, int TI, int TJ, int WI, int WJ, int LOAD, int STAGES = 2>
+template <int DT, int DIR, int TI, int TJ, int WI, int WJ, int LOAD, int STAGES = 2, int WK = 1>
 int launch_group_tiles(LinearArgs& g, const char* fn, hipStream_t s) {
   const int64_t ti = div_up(g.I, TI) + (is_weight(DIR) ? 0 : g.groups - 1), tj = div_up(g.J, TJ);
   const int64_t blocks = is_weight(DIR) ? round_up(ti * tj * g.parts, 8) * g.groups : round_up(ti * tj * g.parts, 8);
@@ -161,7 +166,7 @@ int launch_group_tiles(LinearArgs& g, const char* fn, hipStream_t s) {
   g.spread = g.I <= 2 * TI * g.groups;  // else blocks share what they read of A while they read it
   launch_blocks(blocks, [&](int64_t begin, dim3 grid) {
     g.begin = int32_t(begin);
-    hipLaunchKernelGGL((k_linear<DT, DIR, TI, TJ, WI, WJ, LOAD, true, STAGES>), grid, dim3(WI * WJ * 64), 0, s, g);
+    hipLaunchKernelGGL((k_linear<DT, DIR, TI, TJ, WI, WJ, LOAD, true, STAGES, WK>), grid, dim3(WI * WJ * WK * 64), 0, s, g);
   });
   DDP_HIP_TRY(hipGetLastError(), fn);
   return DDP_OK;
@@ -182,6 +187,11 @@ int launch_groups(LinearArgs& g, const Cut& c, bool direct, const char* fn, hipS
   } else {
     if ((a_along(DIR) ? g.K : g.I) < V || (b_along(DIR) ? g.K : g.J) < V)  // rows shorter than a chunk
       return launch_group_tiles<DT, DIR, 64, 64, 2, 2, kShort>(g, fn, s);
+    if constexpr (b_along(DIR)) {
+      if (c.deep)
+        return direct ? launch_group_tiles<DT, DIR, kFlatRows, 32, 1, 1, kDirect, 2, 4>(g, fn, s)
+                      : launch_group_tiles<DT, DIR, kFlatRows, 32, 1, 1, kAny, 2, 4>(g, fn, s);
+    }
     if (c.flat)
       return direct ? launch_group_tiles<DT, DIR, kFlatRows, 128, 1, 4, kDirect, kFlatStages>(g, fn, s)
                     : launch_group_tiles<DT, DIR, kFlatRows, 128, 1, 4, kAny>(g, fn, s);
