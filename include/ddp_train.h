@@ -205,21 +205,22 @@ int ddp_act_backward(const void* dy, int64_t lddy, const void* z, int64_t ldz, v
  * 1 <= E <= 65536, K >= 1, T, N and K below 2^31, E * N below 2^31.
  *
  * ddp_experts_workspace: bytes of scratch on the current device that a
- * direction (DDP_LINEAR_*) needs: 0 but for the weight gradient, whose
- * call takes it under the same conditions as ddp_linear_backward_weight. */
+ * direction (DDP_LINEAR_*) needs, under the conditions of
+ * ddp_linear_workspace. */
 int ddp_experts_workspace(int32_t direction, int64_t T, int64_t E, int64_t N, int64_t K, int32_t dtype, int64_t* bytes);
 
 /* y_i = act(x_i w_e^T + bias_e); z (NULL: not kept) receives the rounded
  * argument of act. bias may be NULL. */
 int ddp_experts_forward(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias, const int64_t* offsets,
                         void* y, int64_t ldy, void* z, int64_t ldz, int64_t T, int64_t E, int64_t N, int64_t K,
-                        int32_t dtype, int32_t act, void* stream);
+                        int32_t dtype, int32_t act, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* dx_i = (dz_i w_e) * act'(z_i), z[T][K] kept by the layer before (NULL: no
  * activation, `act` must be DDP_ACT_NONE). */
 int ddp_experts_backward_input(const void* dz, int64_t lddz, const void* w, int64_t ldw, const int64_t* offsets,
                                const void* z, int64_t ldz, void* dx, int64_t lddx, int64_t T, int64_t E, int64_t N,
-                               int64_t K, int32_t dtype, int32_t act, void* stream);
+                               int64_t K, int32_t dtype, int32_t act, void* workspace, int64_t workspace_bytes,
+                               void* stream);
 
 /* dw_e = sum of dz_i^T x_i, db_e = sum of dz_i over the expert's rows (db
  * NULL: not wanted), of grad_dtype (`dtype`, or fp32 gradients of bf16 data),

@@ -111,8 +111,9 @@ def _load():
         "ddp_linear_backward_weight": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i32, i32, i32,
                                                       vp, i64, vp]),
         "ddp_experts_workspace": (ctypes.c_int, [i32, i64, i64, i64, i64, i32, ctypes.POINTER(i64)]),
-        "ddp_experts_forward": (ctypes.c_int, [vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, i64, i64, i64, i64, i32, i32, vp]),
-        "ddp_experts_backward_input": (ctypes.c_int, [vp, i64, vp, i64, vp, vp, i64, vp, i64, i64, i64, i64, i64, i32, i32, vp]),
+        "ddp_experts_forward": (ctypes.c_int, [vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, i64, i64, i64, i64, i32, i32, vp, i64, vp]),
+        "ddp_experts_backward_input": (ctypes.c_int, [vp, i64, vp, i64, vp, vp, i64, vp, i64, i64, i64, i64, i64, i32, i32,
+                                                      vp, i64, vp]),
         "ddp_experts_backward_weight": (ctypes.c_int, [vp, i64, vp, i64, vp, vp, i64, vp, i64, i64, i64, i64, i32, i32, i32,
                                                        vp, i64, vp]),
         "ddp_cross_entropy_workspace": (ctypes.c_int, [i32, i64, i64, i64, i32, i32, ctypes.POINTER(i64)]),
@@ -824,7 +825,13 @@ def _experts_workspace(direction, t, e, n, k, code):
     return b.value
 
 
-def experts_forward(x, w, offsets, bias=None, act="none", keep=False, out=None, z=None, stream=None):
+def experts_workspace(direction, t, e, n, k, dtype):
+    """Bytes of scratch that an experts' call of these sizes needs (direction
+    LINEAR_FORWARD, LINEAR_BACKWARD_INPUT or LINEAR_BACKWARD_WEIGHT)."""
+    return _experts_workspace(int(direction), int(t), int(e), int(n), int(k), dtype_code(dtype))
+
+
+def experts_forward(x, w, offsets, bias=None, act="none", keep=False, out=None, z=None, workspace=None, stream=None):
     """act(x_i w_e^T + bias_e) over rows sorted by expert: expert e has the rows
     offsets[e] to offsets[e + 1] (int64, on the GPU) of x and the matrix w[e].
     With keep=True (or a matrix z to fill) the pair (y, z). Rows of no expert
@@ -841,12 +848,13 @@ def experts_forward(x, w, offsets, bias=None, act="none", keep=False, out=None, 
     wp, ldw = _expert_matrices(w, e, n, k, dt, "w")
     yp, ldy = _matrix(y, t, n, dt, "out")
     zp, ldz = _matrix(z, t, n, dt, "z")
+    ws, (nbytes, p) = _scratch(_experts_workspace(LINEAR_FORWARD, t, e, n, k, code), workspace, stream)
     _check(_get_lib().ddp_experts_forward(xp, ldx, wp, ldw, _expert_vectors(bias, e, n, dt, "bias"), _offsets(offsets, e + 1),
-                                          yp, ldy, zp, ldz, t, e, n, k, code, ACTIVATIONS[act], _stream(stream)))
+                                          yp, ldy, zp, ldz, t, e, n, k, code, ACTIVATIONS[act], p, nbytes, _stream(stream)))
     return y if z is None else (y, z)
 
 
-def experts_backward_input(dz, w, offsets, act="none", z=None, out=None, stream=None):
+def experts_backward_input(dz, w, offsets, act="none", z=None, out=None, workspace=None, stream=None):
     """(dz_i w_e) * act'(z_i) (see ddp_experts_backward_input)."""
     t, n = dz.shape
     e, k = w.shape[0], w.shape[2]
@@ -856,8 +864,10 @@ def experts_backward_input(dz, w, offsets, act="none", z=None, out=None, stream=
     wp, ldw = _expert_matrices(w, e, n, k, dt, "w")
     zp, ldz = _matrix(z, t, k, dt, "z")
     op, ldo = _matrix(dx, t, k, dt, "out")
-    _check(_get_lib().ddp_experts_backward_input(gp, ldg, wp, ldw, _offsets(offsets, e + 1), zp, ldz, op, ldo, t, e, n, k,
-                                                 dtype_code(dt), ACTIVATIONS[act], _stream(stream)))
+    code = dtype_code(dt)
+    ws, (nbytes, p) = _scratch(_experts_workspace(LINEAR_BACKWARD_INPUT, t, e, n, k, code), workspace, stream)
+    _check(_get_lib().ddp_experts_backward_input(gp, ldg, wp, ldw, _offsets(offsets, e + 1), zp, ldz, op, ldo, t, e, n, k, code,
+                                                 ACTIVATIONS[act], p, nbytes, _stream(stream)))
     return dx
 
 

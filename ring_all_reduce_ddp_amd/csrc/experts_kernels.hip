@@ -28,11 +28,22 @@ Cut weight_cut(int64_t T, int64_t E, int64_t N, int64_t K, int32_t dtype, bool d
   return cut_of(DDP_LINEAR_BACKWARD_WEIGHT, N, K, T, dtype, direct, int32_t(E));
 }
 
+// How a product of rows is cut.
+Cut rows_cut(int dir, int64_t T, int64_t E, int64_t J, int64_t K, int32_t dtype, bool direct) {
+  return cut_of(dir, T, J, K, dtype, direct, int32_t(E));
+}
+
 template <int DT, int DIR>
-int launch_rows(LinearArgs& g, const char* fn, hipStream_t s) {
+int launch_rows(LinearArgs& g, void* workspace, const char* fn, hipStream_t s) {
   const bool direct = whole_chunks(g.a, g.lda, g.I, g.K, DT) &&
                       whole_chunks(g.b, g.ldb, b_along(DIR) ? g.J : g.K, b_along(DIR) ? g.K : g.J, DT);
-  return launch_groups<DT, DIR>(g, cut_of(DIR, g.I, g.J, g.K, DT, direct, g.groups, 1), direct, fn, s);
+  g.partial = static_cast<float*>(workspace);
+  int st = launch_groups<DT, DIR>(g, rows_cut(DIR, g.I, g.groups, g.J, g.K, DT, direct), direct, fn, s);
+  if (st != DDP_OK || g.parts == 1) return st;
+  g.bias = nullptr;  // the first part's sums have it
+  hipLaunchKernelGGL((k_linear_join<DT, DIR, true>), dim3(unsigned(div_up(g.I * div_up(g.J, 8), kThreads))), dim3(kThreads), 0, s, g);
+  DDP_HIP_TRY(hipGetLastError(), fn);
+  return DDP_OK;
 }
 
 template <int DT>
@@ -70,26 +81,37 @@ extern "C" int ddp_experts_workspace(int32_t direction, int64_t T, int64_t E, in
     return fail(DDP_EINVAL, std::string(fn) + ": unknown direction");
   int st = check_experts(fn, T, E, N, K, dtype, DDP_ACT_NONE);
   if (st != DDP_OK) return st;
-  if (direction != DDP_LINEAR_BACKWARD_WEIGHT || N == 0) return DDP_OK;
+  if (N == 0) return DDP_OK;
   for (bool direct : {false, true}) {
-    const Cut c = weight_cut(T, E, N, K, dtype, direct);
-    *bytes = std::max(*bytes, partial_bytes(c, E * N, K) + bias_bytes(c, E * N, K));
+    if (direction == DDP_LINEAR_BACKWARD_WEIGHT) {
+      const Cut c = weight_cut(T, E, N, K, dtype, direct);
+      *bytes = std::max(*bytes, partial_bytes(c, E * N, K) + bias_bytes(c, E * N, K));
+    } else {
+      const int64_t J = direction == DDP_LINEAR_FORWARD ? N : K;
+      *bytes = std::max(*bytes, partial_bytes(rows_cut(direction, T, E, J, N + K - J, dtype, direct), T, J));
+    }
   }
   return DDP_OK;
 }
 
 extern "C" int ddp_experts_forward(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias,
                                    const int64_t* offsets, void* y, int64_t ldy, void* z, int64_t ldz, int64_t T, int64_t E,
-                                   int64_t N, int64_t K, int32_t dtype, int32_t act, void* stream) {
+                                   int64_t N, int64_t K, int32_t dtype, int32_t act, void* workspace,
+                                   int64_t workspace_bytes, void* stream) {
   const char* fn = "ddp_experts_forward";
   int st = check_experts(fn, T, E, N, K, dtype, act);
   if (st != DDP_OK) return st;
   if (T == 0 || N == 0) return DDP_OK;
   const int eb = elem_bytes(dtype);
+  int64_t need = 0;
+  st = ddp_experts_workspace(DDP_LINEAR_FORWARD, T, E, N, K, dtype, &need);
+  if (st == DDP_OK) st = check_workspace(fn, workspace, workspace_bytes, need);
+  if (st != DDP_OK) return st;
   const Matrix m[] = {{x, T, K, ldx, eb, "x", false, false},     {w, E * N, K, ldw, eb, "w", false, false},
                       {bias, 1, E * N, E * N, eb, "bias", false, true}, bounds_of(offsets, E),
-                      {y, T, N, ldy, eb, "y", true, false},      {z, T, N, ldz, eb, "z", true, true}};
-  st = check_matrices(fn, m, 6, -1, -1);
+                      {y, T, N, ldy, eb, "y", true, false},      {z, T, N, ldz, eb, "z", true, true},
+                      {need > 0 ? workspace : nullptr, 1, need, need, 1, "workspace", true, true}};
+  st = check_matrices(fn, m, 7, -1, -1);
   if (st != DDP_OK) return st;
   LinearArgs g{};
   g.a = x, g.lda = ldx, g.b = w, g.ldb = ldw, g.b_group = N * ldw;
@@ -97,23 +119,29 @@ extern "C" int ddp_experts_forward(const void* x, int64_t ldx, const void* w, in
   g.c = y, g.ldc = ldy, g.z = z, g.ldz = ldz, g.bias = bias;
   g.act = act;
   g.bounds = offsets, g.groups = int32_t(E), g.rows = T;
-  return dtype == DDP_BF16 ? launch_rows<DDP_BF16, DDP_LINEAR_FORWARD>(g, fn, as_stream(stream))
-                           : launch_rows<DDP_FP32, DDP_LINEAR_FORWARD>(g, fn, as_stream(stream));
+  return dtype == DDP_BF16 ? launch_rows<DDP_BF16, DDP_LINEAR_FORWARD>(g, workspace, fn, as_stream(stream))
+                           : launch_rows<DDP_FP32, DDP_LINEAR_FORWARD>(g, workspace, fn, as_stream(stream));
 }
 
 extern "C" int ddp_experts_backward_input(const void* dz, int64_t lddz, const void* w, int64_t ldw, const int64_t* offsets,
                                           const void* z, int64_t ldz, void* dx, int64_t lddx, int64_t T, int64_t E, int64_t N,
-                                          int64_t K, int32_t dtype, int32_t act, void* stream) {
+                                          int64_t K, int32_t dtype, int32_t act, void* workspace, int64_t workspace_bytes,
+                                          void* stream) {
   const char* fn = "ddp_experts_backward_input";
   int st = check_experts(fn, T, E, N, K, dtype, act);
   if (st != DDP_OK) return st;
   if (z == nullptr && act != DDP_ACT_NONE) return fail(DDP_EINVAL, std::string(fn) + ": an activation's slope needs z");
   if (T == 0) return DDP_OK;
   const int eb = elem_bytes(dtype);
+  int64_t need = 0;
+  st = ddp_experts_workspace(DDP_LINEAR_BACKWARD_INPUT, T, E, N, K, dtype, &need);
+  if (st == DDP_OK) st = check_workspace(fn, workspace, workspace_bytes, need);
+  if (st != DDP_OK) return st;
   const Matrix m[] = {{dz, T, N, lddz, eb, "dz", false, false}, {w, E * N, K, ldw, eb, "w", false, false},
                       bounds_of(offsets, E),                    {z, T, K, ldz, eb, "z", false, true},
-                      {dx, T, K, lddx, eb, "dx", true, false}};
-  st = check_matrices(fn, m, 5, -1, -1);
+                      {dx, T, K, lddx, eb, "dx", true, false},
+                      {need > 0 ? workspace : nullptr, 1, need, need, 1, "workspace", true, true}};
+  st = check_matrices(fn, m, 6, -1, -1);
   if (st != DDP_OK) return st;
   LinearArgs g{};
   g.a = dz, g.lda = lddz, g.b = w, g.ldb = ldw, g.b_group = N * ldw;
@@ -121,8 +149,8 @@ extern "C" int ddp_experts_backward_input(const void* dz, int64_t lddz, const vo
   g.c = dx, g.ldc = lddx, g.z = const_cast<void*>(z), g.ldz = ldz;
   g.act = act;
   g.bounds = offsets, g.groups = int32_t(E), g.rows = T;
-  return dtype == DDP_BF16 ? launch_rows<DDP_BF16, DDP_LINEAR_BACKWARD_INPUT>(g, fn, as_stream(stream))
-                           : launch_rows<DDP_FP32, DDP_LINEAR_BACKWARD_INPUT>(g, fn, as_stream(stream));
+  return dtype == DDP_BF16 ? launch_rows<DDP_BF16, DDP_LINEAR_BACKWARD_INPUT>(g, workspace, fn, as_stream(stream))
+                           : launch_rows<DDP_FP32, DDP_LINEAR_BACKWARD_INPUT>(g, workspace, fn, as_stream(stream));
 }
 
 extern "C" int ddp_experts_backward_weight(const void* dz, int64_t lddz, const void* x, int64_t ldx, const int64_t* offsets,

@@ -1043,6 +1043,7 @@ __global__ __launch_bounds__(WI * WJ * WK * 64, 2) void k_linear(LinearArgs g) {
   const int group = tile / (GROUP * g.tiles_j), in_group = tile % (GROUP * g.tiles_j);
   const int rows = tiles_i - GROUP * group < GROUP ? tiles_i - GROUP * group : GROUP;
   int64_t i0 = int64_t(GROUP * group + in_group % rows) * TI, j0 = int64_t(in_group / rows) * TJ;
+  int32_t first_row = 0;
   if constexpr (GROUPS && one_group(DIR)) {
     if (is_weight(DIR)) g.part_k = ((g.K + TA::STEP - 1) / TA::STEP + g.parts - 1) / g.parts * TA::STEP;
   } else if constexpr (GROUPS) {
@@ -1060,6 +1061,7 @@ __global__ __launch_bounds__(WI * WJ * WK * 64, 2) void k_linear(LinearArgs g) {
       e = group_of_tile<TI>(g, scan, GROUP * group + in_group % rows);
       i0 = int64_t(e.tile) * TI;
       g.spread_from = e.index * 5;
+      first_row = e.begin;
       g.a = static_cast<const char*>(g.a) + e.begin * g.lda * TA::ES;
       g.b = static_cast<const char*>(g.b) + e.index * g.b_group * TA::ES;
       if (DIR == DDP_LINEAR_FORWARD && g.bias != nullptr) g.bias = static_cast<const char*>(g.bias) + e.index * g.J * TA::ES;
@@ -1071,8 +1073,9 @@ __global__ __launch_bounds__(WI * WJ * WK * 64, 2) void k_linear(LinearArgs g) {
     }
   }
   constexpr bool kMany = GROUPS && !one_group(DIR);
-  const int64_t all_i = kMany && is_weight(DIR) ? g.I * g.groups : g.I;      // rows of all groups' C,
-  const int64_t first_i = kMany && is_weight(DIR) ? group_index * g.I : 0;   // and this one's first
+  // Rows of all groups' C, and this one's first.
+  const int64_t all_i = !kMany ? g.I : is_weight(DIR) ? g.I * g.groups : g.rows;
+  const int64_t first_i = !kMany ? 0 : is_weight(DIR) ? group_index * g.I : first_row;
   int64_t k0 = part * g.part_k, k1 = k0 + g.part_k < g.K ? k0 + g.part_k : g.K;
   if constexpr (GROUPS) {
     if (k0 > k1) k0 = k1;  // a part of a short group
@@ -1360,6 +1363,11 @@ __global__ __launch_bounds__(WI * WJ * WK * 64, 2) void k_linear(LinearArgs g) {
     __builtin_amdgcn_wave_barrier();
     const int64_t i = i_lane + it * ROWS;
     if (g.parts > 1) {
+      if (kMany && DIR == DDP_LINEAR_FORWARD && part == 0) {  // the join does not know a row's group
+#pragma unroll
+        for (int p = 0; p < BATCH; ++p)
+          for (int k = 0; k < 8; ++k) v[p][k] += bias[k];
+      }
 #pragma unroll
       for (int p = 0; p < BATCH; ++p)
         if (i + p * RPP < g.I && n > 0) store8<DDP_FP32>(g.partial, (part * all_i + first_i + i + p * RPP) * jp + j, 8, v[p]);
@@ -1408,11 +1416,24 @@ __global__ __launch_bounds__(WI * WJ * WK * 64, 2) void k_linear(LinearArgs g) {
 // parts, 42 MB with residual and outputs: 9 either way).
 template <int DT, int DIR, bool GROUPS = false>
 __global__ __launch_bounds__(kThreads) void k_linear_join(LinearArgs g) {
-  if constexpr (GROUPS) g.I = bound_at(g, 1);  // one group, of rows
+  int64_t first = 0, end = g.I;   // the rows that are anybody's
+  if constexpr (GROUPS && one_group(DIR)) {
+    g.I = end = bound_at(g, 1);
+  } else if constexpr (GROUPS) {
+    __shared__ int32_t most[kThreads / 64];
+    int32_t bound = 0;
+    for (int32_t e = int32_t(threadIdx.x); e <= g.groups; e += kThreads) bound = larger(bound, bound_at(g, e));
+    bound = scan_lanes(bound, larger);
+    if ((threadIdx.x & 63) == 63) most[threadIdx.x >> 6] = bound;
+    __syncthreads();
+    first = bound_at(g, 0);
+    end = larger(larger(most[0], most[1]), larger(most[2], most[3]));
+  }
   const int64_t jv = (g.J + 7) / 8;
   const int64_t at = int64_t(blockIdx.x) * kThreads + threadIdx.x;
   if (at >= g.I * jv) return;
   const int64_t i = at / jv, j = at % jv * 8;
+  if (GROUPS && (i < first || i >= end)) return;
   const int n = g.J - j >= 8 ? 8 : int(g.J - j);
   float bias[8] = {};
   if (DIR == DDP_LINEAR_FORWARD && g.bias != nullptr) load8<DT>(g.bias, j, n, bias);

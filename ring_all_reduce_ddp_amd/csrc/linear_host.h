@@ -72,7 +72,7 @@ Cut cut_by_model(int dir, int32_t I, int32_t J, int32_t K, int dtype, bool direc
   const int32_t row = std::min(a_along(dir) ? K : I, b_along(dir) ? K : J);  // the operands' shorter rows
   const int n_shapes = row < 16 / elem_bytes(dtype) ? 1 : dtype == DDP_BF16 && direct ? 3 : 2;
   // Few rows: the other operand's bytes are what counts, whatever the type.
-  static const Shape flat{128, 4, 1500, 1900, 1000};
+  const Shape flat = direct ? Shape{128, 4, 1000, 600, 1000} : Shape{128, 4, 1500, 1100, 1000};
   // Groups of some 100 rows leave much of a tile of 256 empty: half tiles of 128 rows and 256 columns,
   // three steps in LDS or on their way. (4096 rows of 32 groups, 4096 x 2048: 162 us, in tiles of
   // 256 188; 16384 rows of 64: 480 and 461.)
@@ -83,7 +83,7 @@ Cut cut_by_model(int dir, int32_t I, int32_t J, int32_t K, int dtype, bool direc
   const int32_t step = 128 / elem_bytes(dtype), steps = std::max(1, up(sums ? up(K, groups) : K, step));
   const float busy = float(std::min(groups, I));   // groups that have rows
   float least = INFINITY;
-  static const Shape deep{32, 2, 2600, 2600, 1500};
+  const Shape deep{32, 2, 2600, direct ? 1100.0f : 1400.0f, 1500};  // of four steps
   for (int k = 0; k < (flat_rows ? b_along(dir) ? 2 : 1 : n_shapes + int(half_rows)); ++k) {
     const bool is_deep = flat_rows && k == 1;
     const Shape& sh = is_deep ? deep : flat_rows ? flat : k == 3 ? half : shapes[dtype == DDP_BF16][direct][k];

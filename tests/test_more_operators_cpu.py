@@ -22,7 +22,7 @@ def args(base, change):
 
 
 EXPERTS_FORWARD = dict(x=A, ldx=16, w=A + FAR, ldw=16, bias=A + 2 * FAR, offsets=A + 3 * FAR, y=A + 4 * FAR, ldy=8, z=A + 5 * FAR, ldz=8,
-                       T=4, E=3, N=8, K=16, dtype=0, act=1, stream=None)
+                       T=4, E=3, N=8, K=16, dtype=0, act=1, workspace=A + 6 * FAR, workspace_bytes=FAR, stream=None)
 
 
 @pytest.mark.parametrize("change, match", [
@@ -39,7 +39,7 @@ def test_experts_forward(change, match):
 
 
 EXPERTS_INPUT = dict(dz=A, lddz=8, w=A + FAR, ldw=16, offsets=A + 3 * FAR, z=A + 2 * FAR, ldz=16, dx=A + 4 * FAR, lddx=16, T=4, E=3, N=8,
-                     K=16, dtype=0, act=1, stream=None)
+                     K=16, dtype=0, act=1, workspace=A + 6 * FAR, workspace_bytes=FAR, stream=None)
 
 
 @pytest.mark.parametrize("change, match", [
@@ -125,6 +125,9 @@ def test_workspaces():
     refused(lib.ddp_experts_workspace(9, 4, 3, 8, 16, 0, ctypes.byref(n)), "direction")
     refused(lib.ddp_experts_workspace(0, 4, 3, 8, 16, 0, None), "bytes is NULL")
     assert n.value == 0 and lib.ddp_experts_workspace(0, 4, 3, 8, 16, 0, ctypes.byref(n)) == rar.DDP_OK and n.value == 0
+    n.value = 7
+    refused(lib.ddp_experts_workspace(1, 4, 0, 8, 16, 0, ctypes.byref(n)), "E must")
+    assert n.value == 0
     refused(lib.ddp_cross_entropy_workspace(2, 4, 8, 16, 0, 0, ctypes.byref(n)), "direction")
     refused(lib.ddp_cross_entropy_workspace(0, 4, 8, 16, 0, 0, None), "bytes is NULL")
     refused(lib.ddp_distill_workspace(0, 4, 8, 16, 0, 0, 0, ctypes.byref(n)), "C must")
