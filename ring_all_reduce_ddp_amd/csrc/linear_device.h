@@ -521,7 +521,7 @@ struct DirectLoader {
                  uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(a >> 32))),
                  uint32_t(__builtin_amdgcn_readfirstlane(range)) << 4, 0x00020000u};
   }
-  template <bool FULL>
+  template <bool FULL, int SET = 0>
   __device__ __forceinline__ void load(const char* lds, int n) {
     const uint32_t to = uint32_t(reinterpret_cast<uintptr_t>((DDP_LDS const char*)lds));
     const uint32_t m = uint32_t(__builtin_amdgcn_readfirstlane(to + (n * (THREADS / 64) + wave) * 1024));
@@ -534,6 +534,7 @@ struct DirectLoader {
     // assembly.
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(o), "s"(desc), "s"(m) : "m0");
   }
+  template <int SET = 0>
   __device__ __forceinline__ void end() {
     p += advance;
     left -= int32_t(advance / 16);
@@ -552,6 +553,7 @@ struct DirectLoader {
     left -= int32_t(first * advance / 16);
     describe();
   }
+  template <int SET = 0>
   __device__ __forceinline__ void commit(char*) {}
 };
 
@@ -561,18 +563,20 @@ struct DirectLoader {
 // for before the next starts: twice as slow). A chunk that runs over the
 // end of its row is loaded from as far back as it fits and shifted into place
 // when it goes to LDS, zeros following; one past the sum's end is shifted out
-// whole.
-template <int DT, class TL, bool ALONG, int THREADS>
+// whole. PIPE: steps whose chunks are in registers or on their way there; with two, a
+// step's loads have two steps' time.
+template <int DT, class TL, bool ALONG, int THREADS, int PIPE>
 struct AnyLoader {
   static constexpr int kWidth = TL::CPR * TL::V;  // "across": elements of a row in the tile
   const char* p;         // the tile at the current step
   int64_t row_bytes;
   int32_t k_left;        // terms left
   int32_t width;         // "across": elements of a row that exist
-  bool shifted;          // some chunk of the step is to be shifted
   int64_t off[TL::N];    // of this lane's chunks, in bytes from p
-  int32_t shift[TL::N];  // elements to shift out
-  u32x4 x[TL::N];
+  int32_t back[TL::N];   // "across": elements that a chunk is loaded before its place
+  bool shifted[PIPE];    // some chunk of the step is to be shifted
+  int32_t shift[PIPE][TL::N];  // elements to shift out
+  u32x4 x[PIPE][TL::N];
 
   static __device__ __forceinline__ int chunk(int n) { return n * THREADS + int(threadIdx.x); }
   __device__ __forceinline__ void init(const void* base, int64_t ld, int64_t side, int64_t, int64_t s0, int64_t k0, int64_t k1, int32_t) {
@@ -584,45 +588,48 @@ struct AnyLoader {
     for (int n = 0; n < TL::N; ++n) {
       const int row = TL::row_of(chunk(n)), col = TL::col_of(chunk(n)) * TL::V;
       const int64_t r = ALONG && s0 + row >= side ? side - 1 - s0 : row;
-      const int back = !ALONG && col + TL::V > width ? col + TL::V - width : 0;
-      off[n] = r * row_bytes + (col - back) * TL::ES;  // from p, perhaps negative; never before the row
-      shift[n] = back;
+      back[n] = !ALONG && col + TL::V > width ? col + TL::V - width : 0;
+      off[n] = r * row_bytes + (col - back[n]) * TL::ES;  // from p, perhaps negative; never before the row
+#pragma unroll
+      for (int s = 0; s < PIPE; ++s) shift[s][n] = back[n];
     }
   }
-  template <bool FULL>
+  template <bool FULL, int SET = 0>
   __device__ __forceinline__ void load(const char*, int n) {
     int64_t o = off[n];
     if (!FULL && k_left < TL::STEP) {
       const int row = TL::row_of(chunk(n)), col = TL::col_of(chunk(n)) * TL::V;
       if (ALONG) {
-        shift[n] = col + TL::V > k_left ? col + TL::V - k_left : 0;
-        o -= shift[n] * TL::ES;
+        shift[SET][n] = col + TL::V > k_left ? col + TL::V - k_left : 0;
+        o -= shift[SET][n] * TL::ES;
       } else if (row >= k_left) {
         o -= (row - (k_left - 1)) * row_bytes;
-        shift[n] = TL::V;
+        shift[SET][n] = TL::V;
       }
     }
     if constexpr (DT == DDP_FP32)
-      x[n] = load_at<false, u32x4_at4>(p + o, 0);
+      x[SET][n] = load_at<false, u32x4_at4>(p + o, 0);
     else
-      x[n] = load_at<false, u32x4_at2>(p + o, 0);
+      x[SET][n] = load_at<false, u32x4_at2>(p + o, 0);
   }
+  template <int SET = 0>
   __device__ __forceinline__ void end() {
-    shifted = k_left < TL::STEP || (!ALONG && width < kWidth);
+    shifted[SET] = k_left < TL::STEP || (!ALONG && width < kWidth);
     p += ALONG ? TL::ROW : TL::STEP * row_bytes;
     k_left -= TL::STEP;
   }
+  template <int SET = 0>
   __device__ __forceinline__ void commit(char* lds) {
-    if (shifted) {
+    if (shifted[SET]) {
 #pragma unroll
       for (int n = 0; n < TL::N; ++n) {
-        const int bits = shift[n] * TL::ES * 8;
-        const unsigned __int128 v = __builtin_bit_cast(unsigned __int128, x[n]);
-        x[n] = bits < 128 ? __builtin_bit_cast(u32x4, v >> bits) : u32x4{0u, 0u, 0u, 0u};
+        const int bits = shift[SET][n] * TL::ES * 8;
+        const unsigned __int128 v = __builtin_bit_cast(unsigned __int128, x[SET][n]);
+        x[SET][n] = bits < 128 ? __builtin_bit_cast(u32x4, v >> bits) : u32x4{0u, 0u, 0u, 0u};
       }
     }
 #pragma unroll
-    for (int n = 0; n < TL::N; ++n) *reinterpret_cast<u32x4*>(lds + chunk(n) * 16) = x[n];
+    for (int n = 0; n < TL::N; ++n) *reinterpret_cast<u32x4*>(lds + chunk(n) * 16) = x[SET][n];
   }
 };
 
@@ -636,7 +643,7 @@ struct ShortLoader {
   __device__ __forceinline__ void init(const void* b, int64_t ld_, int64_t side_, int64_t, int64_t s0_, int64_t k0, int64_t k1_, int32_t) {
     base = b, ld = ld_, side = side_, s0 = s0_, k = k0, k1 = k1_;
   }
-  template <bool FULL>
+  template <bool FULL, int SET = 0>
   __device__ __forceinline__ void load(const char*, int n) {
     const int q = n * THREADS + int(threadIdx.x);
     const int row = TL::row_of(q), col = TL::col_of(q) * TL::V;
@@ -651,7 +658,9 @@ struct ShortLoader {
         x[n][j >> 1] |= uint32_t(static_cast<const uint16_t*>(base)[r * ld + e + j]) << ((j & 1) * 16);
     }
   }
+  template <int SET = 0>
   __device__ __forceinline__ void end() { k += TL::STEP; }
+  template <int SET = 0>
   __device__ __forceinline__ void commit(char* lds) {
 #pragma unroll
     for (int n = 0; n < TL::N; ++n) *reinterpret_cast<u32x4*>(lds + (n * THREADS + int(threadIdx.x)) * 16) = x[n];
@@ -659,9 +668,9 @@ struct ShortLoader {
 };
 
 enum Loading { kDirect, kAny, kShort };
-template <int LOAD, int DT, class TL, bool ALONG, int THREADS, bool TURNED>
+template <int LOAD, int DT, class TL, bool ALONG, int THREADS, bool TURNED, int PIPE>
 using LoaderOf = std::conditional_t<LOAD == kDirect, DirectLoader<TL, ALONG, THREADS, TURNED>,
-                                    std::conditional_t<LOAD == kAny, AnyLoader<DT, TL, ALONG, THREADS>,
+                                    std::conditional_t<LOAD == kAny, AnyLoader<DT, TL, ALONG, THREADS, PIPE>,
                                                        ShortLoader<DT, TL, ALONG, THREADS>>>;
 
 // ---------------------------------------------------------------- groups of rows
@@ -998,8 +1007,11 @@ __global__ __launch_bounds__(WI * WJ * WK * 64, 2) void k_linear(LinearArgs g) {
   // few rows, which read B from memory, begin at different steps. A probe that only reads
   // so, 256 MiB in rows of 4096 bytes: 4.5 TB/s as it was, 5.7 so, 5.9 in rows of 4224.
   constexpr bool TURNED = GROUPS && LOAD == kDirect && b_along(DIR);
-  using LA = LoaderOf<LOAD, DT, TA, a_along(DIR), THREADS, TURNED>;
-  using LB = LoaderOf<LOAD, DT, TB, b_along(DIR), THREADS, TURNED>;
+  // Two steps of chunks in registers where they fit beside the sums: 1 row of 19208 columns of 2045 in fp32,
+  // forward and backward, 300 us to 258.
+  constexpr int PIPE = GROUPS && LOAD == kAny && WK == 1 && (TI < 128 || b_along(DIR)) ? 2 : 1;
+  using LA = LoaderOf<LOAD, DT, TA, a_along(DIR), THREADS, TURNED, PIPE>;
+  using LB = LoaderOf<LOAD, DT, TB, b_along(DIR), THREADS, TURNED, PIPE>;
   constexpr int STAGE = TA::BYTES + TB::BYTES;
   constexpr int PITCH = 32 * FJ + 4;  // floats; the outputs' way through LDS
   static_assert(WI * WJ * 32 * PITCH * 4 <= STAGES * STAGE, "the outputs' rows fit");
@@ -1146,33 +1158,43 @@ __global__ __launch_bounds__(WI * WJ * WK * 64, 2) void k_linear(LinearArgs g) {
     // the next one have landed.
     constexpr int P = FI * FJ, Q = SB / WK / 32, LOADS = TA::N + TB::N;
     const auto turn = [&](auto more_on_their_way) {
-      if constexpr (STAGES > 2 && decltype(more_on_their_way)::value)  // loads of the steps behind the next one
+      if constexpr (PIPE > 1)  // what went to LDS had to be there
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      else if constexpr (STAGES > 2 && decltype(more_on_their_way)::value)  // loads of the steps behind the next one
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((STAGES - 2) * LOADS) : "memory");
       else
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
       __syncthreads();
     };
-    const auto load_one = [&](char* stage, int n, auto full) __attribute__((always_inline)) {
+    const auto load_one = [&](char* stage, int n, auto full, auto set) __attribute__((always_inline)) {
       if (n < TA::N)
-        la.template load<decltype(full)::value>(stage, n);
+        la.template load<decltype(full)::value, decltype(set)::value>(stage, n);
       else
-        lb.template load<decltype(full)::value>(stage + TA::BYTES, n - TA::N);
+        lb.template load<decltype(full)::value, decltype(set)::value>(stage + TA::BYTES, n - TA::N);
+    };
+    const auto end_loads = [&](auto set) __attribute__((always_inline)) {
+      la.template end<decltype(set)::value>();
+      lb.template end<decltype(set)::value>();
+    };
+    const auto commit = [&](char* stage, auto set) __attribute__((always_inline)) {
+      la.template commit<decltype(set)::value>(stage);
+      lb.template commit<decltype(set)::value>(stage + TA::BYTES);
     };
     int until_rows = tile_j;  // steps until the next one whose rows this block adds up
     // One step: its products, with the loads of a later step into `to` under way
     // (LOADING; FULL: all of whose terms exist), and the next step's first reads from
-    // `next` (MORE).
-    const auto one_step = [&](const char* stage, const char* next, char* to, auto more, auto loading, auto full)
+    // `next` (MORE). With loads of two steps in registers, those of this call go to
+    // `set`, and the other set's to LDS.
+    const auto one_step = [&](const char* stage, const char* next, char* to, auto more, auto loading, auto full, auto set)
                               __attribute__((always_inline)) {
       constexpr bool MORE = decltype(more)::value, LOADING = decltype(loading)::value;
+      constexpr std::integral_constant<int, PIPE == 2 ? 1 - decltype(set)::value : 0> ready{};
       if (GROUPS && !is_weight(DIR) && idle) {
         if (LOADING) {
 #pragma unroll
-          for (int n = 0; n < LOADS; ++n) load_one(to, n, full);
-          la.end();
-          lb.end();
-          la.commit(to);
-          lb.commit(to + TA::BYTES);
+          for (int n = 0; n < LOADS; ++n) load_one(to, n, full, set);
+          end_loads(set);
+          commit(to, ready);
         }
         if (MORE) turn(loading);
         return;
@@ -1196,19 +1218,13 @@ __global__ __launch_bounds__(WI * WJ * WK * 64, 2) void k_linear(LinearArgs g) {
           if (LOADING) {
 #pragma unroll
             for (int n = 0; n < LOADS; ++n)
-              if (n * P / LOADS == m && s == 0) load_one(to, n, full);
-            if (s == 1 && m == P / 2) {
-              la.end();
-              lb.end();
-            }
+              if (n * P / LOADS == m && s == 0) load_one(to, n, full, set);
+            if (s == 1 && m == P / 2) end_loads(set);
           }
         });
         add_rows(s & 1);
       }
-      if (LOADING) {
-        la.commit(to);
-        lb.commit(to + TA::BYTES);
-      }
+      if (LOADING) commit(to, ready);
       if (MORE) turn(loading);
       products((Q - 1) & 1, [&](int m) __attribute__((always_inline)) {
         if (MORE) {
@@ -1218,18 +1234,31 @@ __global__ __launch_bounds__(WI * WJ * WK * 64, 2) void k_linear(LinearArgs g) {
         }
       });
       add_rows((Q - 1) & 1);
+      // The sums are there before anything else looks at them. The compiler's own
+      // waits fell short where two last steps, on an even and an odd count, both end in
+      // copies of the sums: it counted the instructions that a branch jumps over.
+      if constexpr (PIPE == 2 && !MORE) {
+        asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 3" : "+v"(acc[0][0]));
+#pragma unroll
+        for (int m = 1; m < FI * FJ; ++m) asm volatile("" : "+v"(acc[m / FJ][m % FJ]));
+      }
     };
     constexpr std::integral_constant<bool, true> yes{};
     constexpr std::integral_constant<bool, false> no{};
+    constexpr std::integral_constant<int, 0> even{};
+    constexpr std::integral_constant<int, PIPE - 1> odd{};
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s) {  // past the last step: zeros
 #pragma unroll
-      for (int n = 0; n < LOADS; ++n) load_one(lds + s * STAGE, n, no);
-      la.end();
-      lb.end();
+      for (int n = 0; n < LOADS; ++n) load_one(lds + s * STAGE, n, no, even);
+      end_loads(even);
     }
-    la.commit(lds);
-    lb.commit(lds + TA::BYTES);
+    if constexpr (PIPE == 2) {
+#pragma unroll
+      for (int n = 0; n < LOADS; ++n) load_one(lds, n, no, odd);
+      end_loads(odd);
+    }
+    commit(lds, even);
     turn(yes);
 #pragma unroll
     for (int m = 0; m < FI + FJ; ++m) read_one(lds, 0, 0, m);
@@ -1237,26 +1266,43 @@ __global__ __launch_bounds__(WI * WJ * WK * 64, 2) void k_linear(LinearArgs g) {
     // then, and a wave's instructions between its products are few. (They
     // issue one by one, some 5 cycles each, while its products wait.)
     int t = 0;
-    if constexpr (STAGES == 2) {
+    if constexpr (PIPE == 2) {
+      // Loads run two steps ahead, past the last step too: they read as zeros.
+      const int whole_steps = int((k1 - k0) / TA::STEP);
+      for (; t + 3 < whole_steps; t += 2) {
+        one_step(lds, lds + STAGE, lds + STAGE, yes, yes, yes, even);
+        one_step(lds + STAGE, lds, lds, yes, yes, yes, odd);
+      }
+      for (; t + 2 < steps; t += 2) {
+        one_step(lds, lds + STAGE, lds + STAGE, yes, yes, no, even);
+        one_step(lds + STAGE, lds, lds, yes, yes, no, odd);
+      }
+      if (t + 1 < steps) {
+        one_step(lds, lds + STAGE, lds + STAGE, yes, yes, no, even);
+        one_step(lds + STAGE, nullptr, nullptr, no, no, no, odd);
+      } else {
+        one_step(lds, nullptr, nullptr, no, no, no, even);
+      }
+    } else if constexpr (STAGES == 2) {
       const int whole_steps = int((k1 - k0) / TA::STEP);
       for (; t + 2 < whole_steps; t += 2) {
-        one_step(lds, lds + STAGE, lds + STAGE, yes, yes, yes);
-        one_step(lds + STAGE, lds, lds, yes, yes, yes);
+        one_step(lds, lds + STAGE, lds + STAGE, yes, yes, yes, even);
+        one_step(lds + STAGE, lds, lds, yes, yes, yes, even);
       }
       for (; t + 1 < steps; ++t) {
         char* const next = lds + ((t & 1) ^ 1) * STAGE;
-        one_step(lds + (t & 1) * STAGE, next, next, yes, yes, no);
+        one_step(lds + (t & 1) * STAGE, next, next, yes, yes, no, even);
       }
-      one_step(lds + (t & 1) * STAGE, nullptr, nullptr, no, no, no);
+      one_step(lds + (t & 1) * STAGE, nullptr, nullptr, no, no, no, even);
     } else {
       // The last steps' turns wait for all that is on its way, the first of them
       // longer than it has to.
       int at = 0;  // t % STAGES
       const auto after = [](int s) { return s + 1 == STAGES ? 0 : s + 1; };
       for (; t + STAGES - 1 < steps; ++t, at = after(at))
-        one_step(lds + at * STAGE, lds + after(at) * STAGE, lds + (at == 0 ? STAGES - 1 : at - 1) * STAGE, yes, yes, no);
-      for (; t + 1 < steps; ++t, at = after(at)) one_step(lds + at * STAGE, lds + after(at) * STAGE, nullptr, yes, no, no);
-      one_step(lds + at * STAGE, nullptr, nullptr, no, no, no);
+        one_step(lds + at * STAGE, lds + after(at) * STAGE, lds + (at == 0 ? STAGES - 1 : at - 1) * STAGE, yes, yes, no, even);
+      for (; t + 1 < steps; ++t, at = after(at)) one_step(lds + at * STAGE, lds + after(at) * STAGE, nullptr, yes, no, no, even);
+      one_step(lds + at * STAGE, nullptr, nullptr, no, no, no, even);
       if (steps < STAGES) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // zeros past the last step may still be on their way
     }
   }
