@@ -209,6 +209,11 @@ int ddp_act_backward(const void* dy, int64_t lddy, const void* z, int64_t ldz, v
  * ddp_linear_workspace. */
 int ddp_experts_workspace(int32_t direction, int64_t T, int64_t E, int64_t N, int64_t K, int32_t dtype, int64_t* bytes);
 
+/* ddp_experts_tiling: how a direction's products are cut, like
+ * ddp_linear_tiling: tiles of *rows x *columns, sums in *parts parts. */
+int ddp_experts_tiling(int32_t direction, int64_t T, int64_t E, int64_t N, int64_t K, int32_t dtype, int32_t direct,
+                       int32_t* rows, int32_t* columns, int32_t* parts);
+
 /* y_i = act(x_i w_e^T + bias_e); z (NULL: not kept) receives the rounded
  * argument of act. bias may be NULL. */
 int ddp_experts_forward(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias, const int64_t* offsets,
@@ -260,7 +265,7 @@ int ddp_experts_backward_weight(const void* dz, int64_t lddz, const void* x, int
  * rounded to bf16; those of an fp32 dw of bf16 data take it as two bf16 terms,
  * which are off by 2^-16 of it at most.
  *
- * 1 <= V < 2^31, 0 <= M <= 2^21, 1 <= K <= 2^21, M K <= 2^33, M V < 2^42,
+ * 1 <= V < 2^31, 0 <= M <= 2^20, 1 <= K <= 2^21, M K <= 2^32, M V < 2^42,
  * 1 <= C <= 1024, T > 0 and finite.
  *
  * ddp_cross_entropy_workspace: bytes of scratch for a direction and sizes on
@@ -270,6 +275,12 @@ int ddp_experts_backward_weight(const void* dz, int64_t lddz, const void* x, int
 #define DDP_LOSS_BACKWARD 1
 int ddp_cross_entropy_workspace(int32_t direction, int64_t M, int64_t V, int64_t K, int32_t dtype, int32_t grad_dtype,
                                 int64_t* bytes);
+
+/* ddp_loss_tiling: how a product is cut, like ddp_linear_tiling: 0: z in the
+ * forward pass, 1: z of a piece in the backward pass, 2: dx, 3: dw; *piece is the
+ * number of columns of the vocabulary that a product takes at a time. */
+int ddp_loss_tiling(int32_t product, int64_t M, int64_t V, int64_t K, int32_t dtype, int32_t grad_dtype, int32_t direct,
+                    int32_t* rows, int32_t* columns, int32_t* parts, int64_t* piece);
 
 /* loss and lse of every row. */
 int ddp_cross_entropy_forward(const void* x, int64_t ldx, const void* w, int64_t ldw, const int64_t* targets, float* loss,

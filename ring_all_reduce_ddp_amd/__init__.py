@@ -111,6 +111,8 @@ def _load():
         "ddp_linear_backward_weight": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i32, i32, i32,
                                                       vp, i64, vp]),
         "ddp_experts_workspace": (ctypes.c_int, [i32, i64, i64, i64, i64, i32, ctypes.POINTER(i64)]),
+        "ddp_experts_tiling": (ctypes.c_int, [i32, i64, i64, i64, i64, i32, i32, *[ctypes.POINTER(i32)] * 3]),
+        "ddp_loss_tiling": (ctypes.c_int, [i32, i64, i64, i64, i32, i32, i32, *[ctypes.POINTER(i32)] * 3, ctypes.POINTER(i64)]),
         "ddp_experts_forward": (ctypes.c_int, [vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, i64, i64, i64, i64, i32, i32, vp, i64, vp]),
         "ddp_experts_backward_input": (ctypes.c_int, [vp, i64, vp, i64, vp, vp, i64, vp, i64, i64, i64, i64, i64, i32, i32,
                                                       vp, i64, vp]),
@@ -831,6 +833,15 @@ def experts_workspace(direction, t, e, n, k, dtype):
     return _experts_workspace(int(direction), int(t), int(e), int(n), int(k), dtype_code(dtype))
 
 
+def experts_tiling(direction, t, e, n, k, dtype, direct=True):
+    """(rows, columns, parts): the tiles that a direction's products are cut
+    into and the parts of their sums (see ddp_experts_tiling)."""
+    out = [ctypes.c_int32() for _ in range(3)]
+    _check(_get_lib().ddp_experts_tiling(int(direction), int(t), int(e), int(n), int(k), dtype_code(dtype), 1 if direct else 0,
+                                         *(ctypes.byref(o) for o in out)))
+    return tuple(o.value for o in out)
+
+
 def experts_forward(x, w, offsets, bias=None, act="none", keep=False, out=None, z=None, workspace=None, stream=None):
     """act(x_i w_e^T + bias_e) over rows sorted by expert: expert e has the rows
     offsets[e] to offsets[e + 1] (int64, on the GPU) of x and the matrix w[e].
@@ -915,6 +926,20 @@ def distill_workspace(direction, m, v, k, top, dtype, grad_dtype=None):
         raise ValueError("a row has at least one entry")
     return _loss_workspace(int(direction), int(m), int(v), int(k), int(top), code,
                            code if grad_dtype is None else dtype_code(grad_dtype))
+
+
+LOSS_Z, LOSS_Z_AGAIN, LOSS_DX, LOSS_DW = 0, 1, 2, 3
+
+
+def loss_tiling(product, m, v, k, dtype, grad_dtype=None, direct=True):
+    """(rows, columns, parts, piece): the tiles that a loss's product (LOSS_Z,
+    LOSS_Z_AGAIN, LOSS_DX or LOSS_DW) is cut into, the parts of its sums, and the
+    columns of the vocabulary that it takes at a time (see ddp_loss_tiling)."""
+    out, piece = [ctypes.c_int32() for _ in range(3)], ctypes.c_int64()
+    code = dtype_code(dtype)
+    _check(_get_lib().ddp_loss_tiling(int(product), int(m), int(v), int(k), code, code if grad_dtype is None else dtype_code(grad_dtype),
+                                      1 if direct else 0, *(ctypes.byref(o) for o in out), ctypes.byref(piece)))
+    return (*(o.value for o in out), piece.value)
 
 
 def _row_values(t, m, what, stream):

@@ -94,6 +94,25 @@ extern "C" int ddp_experts_workspace(int32_t direction, int64_t T, int64_t E, in
   return DDP_OK;
 }
 
+extern "C" int ddp_experts_tiling(int32_t direction, int64_t T, int64_t E, int64_t N, int64_t K, int32_t dtype, int32_t direct,
+                                  int32_t* rows, int32_t* columns, int32_t* parts) {
+  const char* fn = "ddp_experts_tiling";
+  if (rows == nullptr || columns == nullptr || parts == nullptr) return fail(DDP_EINVAL, std::string(fn) + ": an output is NULL");
+  *rows = *columns = *parts = 0;
+  if (direction < DDP_LINEAR_FORWARD || direction > DDP_LINEAR_BACKWARD_WEIGHT)
+    return fail(DDP_EINVAL, std::string(fn) + ": unknown direction");
+  if (direct != 0 && direct != 1) return fail(DDP_EINVAL, std::string(fn) + ": direct must be 0 or 1");
+  int st = check_experts(fn, T, E, N, K, dtype, DDP_ACT_NONE);
+  if (st != DDP_OK) return st;
+  const int64_t J = direction == DDP_LINEAR_FORWARD ? N : K;
+  const Cut c = direction == DDP_LINEAR_BACKWARD_WEIGHT ? weight_cut(T, E, N, K, dtype, direct != 0)
+                                                        : rows_cut(direction, T, E, J, N + K - J, dtype, direct != 0);
+  *rows = c.rows();
+  *columns = c.tile;
+  *parts = c.parts;
+  return DDP_OK;
+}
+
 extern "C" int ddp_experts_forward(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias,
                                    const int64_t* offsets, void* y, int64_t ldy, void* z, int64_t ldz, int64_t T, int64_t E,
                                    int64_t N, int64_t K, int32_t dtype, int32_t act, void* workspace,

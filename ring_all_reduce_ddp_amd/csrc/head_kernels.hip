@@ -21,8 +21,9 @@ namespace {
 
 constexpr int32_t kMostTop = 1024;
 // Operands of direct loads have leading dimensions up to 2^21 and fewer than
-// 2^31 chunks, and those in the scratch are always loaded so.
-constexpr int64_t kMostRows = int64_t(1) << 21, kMostIns = int64_t(1) << 21;
+// 2^31 chunks of 16 bytes, and those in the scratch are always loaded so: the
+// gathered rows, and dz, whose pieces have 4096 columns where the rows are most.
+constexpr int64_t kMostRows = int64_t(1) << 20, kMostIns = int64_t(1) << 21;
 
 // ---------------------------------------------------------------- a teacher's top logits
 
@@ -404,7 +405,7 @@ int check_head(const char* fn, const Head& h) {
   if (st != DDP_OK) return st;
   if (h.V < 1 || h.K < 1) return fail(DDP_EINVAL, std::string(fn) + ": V and K must be at least 1");
   if (h.M > kMostRows || h.K > kMostIns || h.M * h.K > kMostRows * 4096)
-    return fail(DDP_EINVAL, std::string(fn) + ": M and K may be 2^21 at most, M * K 2^33");
+    return fail(DDP_EINVAL, std::string(fn) + ": M may be 2^20 at most, K 2^21, M * K 2^32");
   if (h.M > 0 && h.V >= (int64_t(1) << 42) / h.M) return fail(DDP_EINVAL, std::string(fn) + ": M * V must be below 2^42");
   if (h.grad_dtype != h.dtype && h.grad_dtype != DDP_FP32)
     return fail(DDP_EINVAL, std::string(fn) + ": grad_dtype must be the data's or fp32");
@@ -628,6 +629,29 @@ extern "C" int ddp_cross_entropy_workspace(int32_t direction, int64_t M, int64_t
                                            int64_t* bytes) {
   return workspace_call("ddp_cross_entropy_workspace", direction,
                         head_of(M, V, K, 0, dtype, grad_dtype, direction == DDP_LOSS_BACKWARD), bytes);
+}
+
+extern "C" int ddp_loss_tiling(int32_t product, int64_t M, int64_t V, int64_t K, int32_t dtype, int32_t grad_dtype, int32_t direct,
+                               int32_t* rows, int32_t* columns, int32_t* parts, int64_t* piece) {
+  const char* fn = "ddp_loss_tiling";
+  if (rows == nullptr || columns == nullptr || parts == nullptr || piece == nullptr)
+    return fail(DDP_EINVAL, std::string(fn) + ": an output is NULL");
+  *rows = *columns = *parts = 0;
+  *piece = 0;
+  if (product < 0 || product > 3) return fail(DDP_EINVAL, std::string(fn) + ": unknown product");
+  if (direct != 0 && direct != 1) return fail(DDP_EINVAL, std::string(fn) + ": direct must be 0 or 1");
+  const Head h = head_of(M, V, K, 0, dtype, grad_dtype, product > 0);
+  int st = check_head(fn, h);
+  if (st != DDP_OK) return st;
+  const int64_t n = product == 0 ? V : std::min(pieces_of(h).columns, V);
+  const Cut c = product < 2    ? cut_of(kRowStats, M, n, K, dtype, direct != 0, 0, 1)
+                : product == 2 ? cut_of(kInputPiece, M, K, n, dtype, direct != 0, 0, 128)
+                               : cut_of(kWeightTerms, n, K, M * h.terms(), dtype, true);
+  *rows = c.rows();
+  *columns = c.tile;
+  *parts = c.parts;
+  *piece = n;
+  return DDP_OK;
 }
 
 extern "C" int ddp_cross_entropy_forward(const void* x, int64_t ldx, const void* w, int64_t ldw, const int64_t* targets, float* loss,

@@ -40,6 +40,7 @@ struct Cut {
   int tile = 128;
   int32_t parts = 1;
   int64_t part_k = 0;
+  int32_t rows() const { return flat ? 32 : half ? 128 : tile; }
 };
 
 // The cut with the least time by a rough model in cycles. Its constants were
@@ -192,9 +193,11 @@ int launch_groups(LinearArgs& g, const Cut& c, bool direct, const char* fn, hipS
         return direct ? launch_group_tiles<DT, DIR, kFlatRows, 32, 1, 1, kDirect, 2, 4>(g, fn, s)
                       : launch_group_tiles<DT, DIR, kFlatRows, 32, 1, 1, kAny, 2, 4>(g, fn, s);
     }
-    if (c.flat)
-      return direct ? launch_group_tiles<DT, DIR, kFlatRows, 128, 1, 4, kDirect, kFlatStages>(g, fn, s)
-                    : launch_group_tiles<DT, DIR, kFlatRows, 128, 1, 4, kAny>(g, fn, s);
+    if constexpr (!is_weight(DIR)) {
+      if (c.flat)
+        return direct ? launch_group_tiles<DT, DIR, kFlatRows, 128, 1, 4, kDirect, kFlatStages>(g, fn, s)
+                      : launch_group_tiles<DT, DIR, kFlatRows, 128, 1, 4, kAny>(g, fn, s);
+    }
     if constexpr (DT == DDP_BF16) {
       if constexpr (!one_group(DIR) && !is_weight(DIR)) {
         if (c.half) return launch_group_tiles<DT, DIR, 128, 256, 2, 4, kDirect, 3>(g, fn, s);

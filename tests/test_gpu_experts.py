@@ -139,6 +139,54 @@ def test_wide_tiles(n, k):
     weight_case(WIDE, 9, n, k, "bf16", "bf16", False, False, 0, 0)
 
 
+# direction, dtype, whether rows are whole chunks, (T, E, N, K), and the tiles that these give: every form of each product
+FORMS = [
+    (0, "bf16", False, (5023, 16, 520, 40), (128, 128, 1)), (0, "bf16", False, (3707, 16, 72, 2056), (128, 128, 7)),
+    (0, "bf16", False, (60, 8, 264, 2056), (32, 128, 9)), (0, "bf16", False, (300, 16, 1032, 520), (32, 128, 1)), (0, "bf16", False, (19, 2, 40, 2056), (32, 32, 0)),
+    (0, "bf16", False, (70, 2, 40, 1032), (64, 64, 0)), (0, "bf16", True, (6392, 8, 264, 40), (128, 128, 1)),
+    (0, "bf16", True, (2269, 16, 72, 2056), (128, 128, 7)), (0, "bf16", True, (900, 8, 4104, 40), (128, 256, 1)),
+    (0, "bf16", True, (3001, 16, 2056, 40), (256, 256, 1)), (0, "bf16", True, (300, 16, 40, 2056), (32, 128, 0)),
+    (0, "bf16", True, (19, 2, 40, 2056), (32, 32, 0)), (0, "bf16", True, (70, 2, 40, 2056), (64, 64, 0)),
+    (0, "fp32", False, (5023, 16, 520, 40), (128, 128, 1)), (0, "fp32", False, (4104, 2, 72, 1032), (128, 128, 7)),
+    (0, "fp32", False, (60, 8, 264, 1032), (32, 128, 9)), (0, "fp32", False, (300, 16, 1032, 520), (32, 128, 1)), (0, "fp32", True, (5023, 16, 520, 40), (128, 128, 1)),
+    (0, "fp32", True, (3707, 16, 72, 2056), (128, 128, 7)), (0, "fp32", True, (300, 16, 40, 1032), (32, 128, 0)),
+    (0, "fp32", True, (19, 2, 40, 1032), (32, 32, 0)),
+    (1, "bf16", False, (5269, 8, 8, 520), (128, 128, 1)), (1, "bf16", False, (3670, 16, 2056, 72), (128, 128, 7)),
+    (1, "bf16", False, (19, 2, 1032, 40), (32, 128, 0)), (1, "bf16", False, (70, 2, 1032, 40), (64, 64, 0)),
+    (1, "bf16", True, (6224, 16, 8, 264), (128, 128, 1)), (1, "bf16", True, (2253, 16, 2056, 72), (128, 128, 7)),
+    (1, "bf16", True, (900, 16, 8, 2056), (128, 256, 1)), (1, "bf16", True, (900, 8, 4104, 1032), (128, 256, 0)),
+    (1, "bf16", True, (2996, 16, 8, 2056), (256, 256, 1)), (1, "bf16", True, (6315, 8, 4104, 520), (256, 256, 3)),
+    (1, "bf16", True, (19, 2, 2056, 40), (32, 128, 0)), (1, "bf16", True, (70, 2, 2056, 40), (64, 64, 0)),
+    (1, "fp32", False, (5269, 8, 8, 520), (128, 128, 1)), (1, "fp32", False, (3905, 8, 1032, 72), (128, 128, 7)),
+    (1, "fp32", True, (5269, 8, 8, 520), (128, 128, 1)), (1, "fp32", True, (1625, 2, 4104, 72), (128, 128, 19)),
+    (1, "fp32", True, (19, 2, 1032, 40), (32, 128, 0)),
+    (2, "bf16", False, (80, 5, 264, 2056), (128, 128, 1)), (2, "bf16", False, (3095, 2, 2056, 72), (128, 128, 7)),
+    (2, "bf16", False, (975, 1, 8, 40), (64, 64, 8)), (2, "bf16", True, (80, 16, 1032, 72), (128, 128, 1)),
+    (2, "bf16", True, (4927, 2, 72, 1032), (128, 128, 10)), (2, "bf16", True, (4365, 8, 4104, 136), (256, 256, 1)),
+    (2, "bf16", True, (5589, 5, 4104, 136), (256, 256, 3)), (2, "bf16", True, (1412, 1, 8, 40), (64, 64, 6)),
+    (2, "fp32", False, (80, 5, 264, 2056), (128, 128, 1)), (2, "fp32", False, (1172, 2, 2056, 72), (128, 128, 7)),
+    (2, "fp32", True, (80, 5, 264, 2056), (128, 128, 1)), (2, "fp32", True, (2486, 2, 72, 2056), (128, 128, 7)),
+    (2, "fp32", True, (570, 1, 8, 40), (64, 64, 6)),
+]
+
+
+@pytest.mark.parametrize("direction, dtype, direct, size, form", FORMS, ids=str)
+def test_every_form(direction, dtype, direct, size, form):
+    """form: rows and columns of the tiles, and the parts (0: some number over 1 or 1)."""
+    t, e, n, k = size
+    got = rar.experts_tiling(direction, t, e, n, k, dtype, direct)
+    assert got[:2] == form[:2] and form[2] in (0, got[2]), got
+    cut = sorted(torch.randint(0, t + 1, (e - 1,), generator=torch.Generator().manual_seed(t)).tolist())
+    counts = [b - a for a, b in zip([0] + cut, cut + [t])]
+    layout = (8, 0) if direct else (3, 1)
+    if direction == 0:
+        forward_case(counts, 0, n, k, dtype, "silu", True, True, *layout)
+    elif direction == 1:
+        input_case(counts, 0, n, k, dtype, "gelu_tanh", *layout)
+    else:
+        weight_case(counts, 0, n, k, dtype, "fp32", True, True, *layout)
+
+
 @pytest.mark.parametrize("bounds", [[-5, 20, 7, 30, 90], [40, 30, 50, 50, 60], [60, 60, 60, 60, 60], [0, 1 << 40, 0, 3, 5],
                                     [-(1 << 60), -3, -2, -1, 0], [10, 20, 30, 40, 50]], ids=str)
 def test_bounds_that_do_not_ascend(bounds):
@@ -163,6 +211,20 @@ def test_bounds_that_do_not_ascend(bounds):
         want, _, tol = product64(out[rows].t(), x[rows])
         close(dw[i], want, tol, "fp32", f"dw of expert {i}")
     assert bool(torch.isnan(out[:b[0]]).all()) and bool(torch.isnan(out[b[-1]:]).all())
+
+
+def test_more_experts_than_one_launch_holds():
+    """65536 experts of 65 column tiles each: more than 2^22 blocks, for 12 rows."""
+    e, n, k = 65536, 65 * 128, 8
+    g = gen(8)
+    w = torch.empty(e, n, k, device="cuda", dtype=torch.bfloat16).normal_(generator=g)
+    of = torch.tensor([0, 0, 1, 77, 4095, 30000, 30000, 30000, 50000, 65534, 65535, 65535], device="cuda")
+    x = matrix(g, len(of), k, "bf16")
+    off = torch.searchsorted(of, torch.arange(e + 1, device="cuda"))
+    y = rar.experts_forward(x, w, off)
+    for i, o in enumerate(of.tolist()):
+        want, _, tol = product64(x[i:i + 1], w[o].t())
+        close(y[i:i + 1], want, tol, "bf16", f"row {i}")
 
 
 def test_no_rows():

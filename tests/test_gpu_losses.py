@@ -172,10 +172,59 @@ def test_wide_tiles(top):
             run_case(Case(m, v, k, "bf16", top=top, ignored=0.1, pad=8), grads, grads == "fp32", 8, 0)
 
 
+# product (0: z, 2: dx, 3: dw), dtype, whether w's rows are whole chunks, (M, V, K, gradients), and the tiles that these give
+FORMS = [
+    (0, "bf16", False, (200, 12976, 40, "bf16"), (128, 128, 1)), (0, "bf16", False, (9, 3000, 40, "bf16"), (32, 128, 1)),
+    (0, "bf16", False, (30, 301, 520, "fp32"), (32, 32, 1)), (0, "bf16", True, (136, 11240, 40, "fp32"), (128, 128, 1)),
+    (0, "bf16", True, (911, 8456, 40, "bf16"), (256, 256, 1)), (0, "bf16", True, (9, 3000, 40, "bf16"), (32, 128, 1)),
+    (0, "bf16", True, (30, 301, 1032, "bf16"), (32, 32, 1)), (0, "fp32", False, (200, 12976, 40, "fp32"), (128, 128, 1)),
+    (0, "fp32", False, (30, 301, 264, "fp32"), (32, 32, 1)), (0, "fp32", True, (200, 12976, 40, "fp32"), (128, 128, 1)),
+    (0, "fp32", True, (9, 3000, 40, "fp32"), (32, 128, 1)), (0, "fp32", True, (30, 301, 520, "fp32"), (32, 32, 1)),
+    (2, "bf16", False, (5443, 16, 520, "bf16"), (128, 128, 1)), (2, "bf16", False, (4145, 1984, 72, "bf16"), (128, 128, 7)),
+    (2, "bf16", True, (3589, 16, 520, "bf16"), (128, 128, 1)), (2, "bf16", True, (2825, 2120, 72, "bf16"), (128, 128, 7)),
+    (2, "bf16", True, (3841, 16, 2056, "fp32"), (256, 256, 1)), (2, "bf16", True, (5646, 4328, 136, "bf16"), (256, 256, 10)),
+    (2, "bf16", True, (20, 20000, 40, "bf16"), (32, 128, 0)), (2, "bf16", False, (20, 20000, 40, "fp32"), (32, 128, 0)),
+    (2, "fp32", False, (5443, 16, 520, "fp32"), (128, 128, 1)), (2, "fp32", False, (4422, 888, 72, "fp32"), (128, 128, 7)),
+    (2, "fp32", True, (5443, 16, 520, "fp32"), (128, 128, 1)), (2, "fp32", True, (4500, 1272, 72, "fp32"), (128, 128, 7)),
+    (3, "bf16", True, (40, 11048, 136, "bf16"), (128, 128, 1)), (3, "bf16", True, (1249, 72, 2056, "fp32"), (128, 128, 8)),
+    (3, "bf16", True, (277, 13320, 520, "fp32"), (256, 256, 1)), (3, "bf16", True, (2102, 5688, 136, "fp32"), (256, 256, 11)),
+    (3, "bf16", True, (707, 16, 40, "fp32"), (64, 64, 6)), (3, "fp32", True, (40, 9952, 264, "fp32"), (128, 128, 1)),
+    (3, "fp32", True, (1268, 4448, 72, "fp32"), (128, 128, 7)), (3, "fp32", True, (545, 16, 40, "fp32"), (64, 64, 6)),
+]
+
+
+@pytest.mark.parametrize("product, dtype, direct, size, form", FORMS, ids=str)
+def test_every_form(product, dtype, direct, size, form):
+    m, v, k, grads = size
+    got = rar.loss_tiling(product, m, v, k, dtype, grads, direct)
+    assert got[:2] == form[:2] and form[2] in (0, got[2]), got
+    layout = (8, 0) if direct else (3, 1)
+    run_case(Case(m, v, k, dtype, top=7 if m % 2 else 0, ignored=0.1, pad=layout[0], shift=layout[1]), grads, m % 3 == 0, *layout)
+
+
 @pytest.mark.parametrize("dtype, grads", [("fp32", "fp32"), ("bf16", "fp32"), ("bf16", "bf16")])
 @pytest.mark.parametrize("top", [0, 5])
 def test_pieces_of_the_vocabulary(dtype, grads, top):
     run_case(Case(40000, 9003, 24, dtype, top=top, ignored=0.05), grads, True, 0, 0)
+
+
+def test_more_columns_than_one_launch_holds():
+    """2^22 blocks of 64 columns and a few more, and 257 pieces backward: the gradients of one row of one input."""
+    v = 64 * (1 << 22) + 1000
+    w = torch.randn(v, 1, generator=gen(5), device="cuda").to(torch.bfloat16)
+    x = torch.full((1, 1), 1.5, device="cuda", dtype=torch.bfloat16)
+    t = torch.tensor([v - 3], device="cuda")
+    loss, lse = rar.cross_entropy_forward(x, w, t)
+    z = w[:, 0].double() * 1.5
+    want = torch.logsumexp(z, 0)
+    tol = (math.log(v) + 40 + v / 64 ** 2) * U * float(want)   # sums of 64 values, joined by 32 threads
+    assert abs(float(lse) - float(want)) <= tol and abs(float(loss) - float(want - z[-3])) <= tol
+    dw = torch.empty(v, 1, device="cuda")
+    dx = rar.cross_entropy_backward(x, w, t, lse, torch.ones(1, device="cuda"), dw=dw)
+    p = torch.exp(z - want)
+    p[-3] -= 1
+    close(dw[:, 0], p * 1.5, 1.5 * (p.abs() * (B * B + 2 * tol) + TINY), "fp32", "dw")
+    close(dx[0], (p * z / 1.5).sum()[None], (p * z).abs().sum()[None] * (B + 2 * tol + 300 * U), "bf16", "dx")
 
 
 @pytest.mark.parametrize("which", ["dx", "dw"])

@@ -83,7 +83,7 @@ ENTROPY_BACKWARD = dict(x=A, ldx=16, w=A + FAR, ldw=16, targets=A + 2 * FAR, lse
 
 @pytest.mark.parametrize("change, match", [
     (dict(dtype=5), "unknown dtype"), (dict(M=-1), "M, N and K"), (dict(V=0), "V and K"), (dict(K=0), "V and K"),
-    (dict(M=(1 << 21) + 1), "2^21"), (dict(K=(1 << 21) + 1), "2^21"), (dict(M=1 << 21, K=4097), "2^21"),
+    (dict(M=(1 << 20) + 1), "2^20"), (dict(K=(1 << 21) + 1), "2^21"), (dict(M=1 << 20, K=4097), "2^32"),
     (dict(M=1 << 13, V=1 << 30), "M * V"),
     (dict(x=None), "x"), (dict(w=None), "w"), (dict(targets=None), "targets"), (dict(loss=None), "loss"), (dict(lse=None), "lse"),
     (dict(targets=A + 2 * FAR + 4), "targets is not aligned"), (dict(ldx=15), "leading dimension of x"), (dict(ldw=15), "leading dimension of w"),
@@ -137,3 +137,22 @@ def test_workspaces():
     assert rar.cross_entropy_workspace(rar.LOSS_BACKWARD, 8192, 128000, 4096, "bf16", "fp32") < 3 << 28
     with pytest.raises(ValueError):
         rar.distill_workspace(rar.LOSS_FORWARD, 4, 8, 16, 0, "fp32")
+
+
+def test_tilings():
+    lib, n, piece = rar.lib, [ctypes.c_int32(7) for _ in range(3)], ctypes.c_int64(7)
+    out = [ctypes.byref(x) for x in n]
+    refused(lib.ddp_experts_tiling(3, 4, 3, 8, 16, 0, 1, *out), "direction")
+    refused(lib.ddp_experts_tiling(0, 4, 3, 8, 16, 0, 2, *out), "direct must be")
+    refused(lib.ddp_experts_tiling(0, 4, 0, 8, 16, 0, 1, *out), "E must")
+    refused(lib.ddp_experts_tiling(0, 4, 3, 8, 16, 0, 1, None, *out[1:]), "output is NULL")
+    refused(lib.ddp_loss_tiling(4, 4, 8, 16, 0, 0, 1, *out, ctypes.byref(piece)), "product")
+    refused(lib.ddp_loss_tiling(0, 4, 8, 16, 0, 0, 3, *out, ctypes.byref(piece)), "direct must be")
+    refused(lib.ddp_loss_tiling(0, 4, 0, 16, 0, 0, 1, *out, ctypes.byref(piece)), "V and K")
+    refused(lib.ddp_loss_tiling(0, 4, 8, 16, 0, 0, 1, *out, None), "output is NULL")
+    assert [x.value for x in n] == [0, 0, 0] and piece.value == 0
+    assert rar.experts_tiling(rar.LINEAR_FORWARD, 1 << 17, 8, 4096, 4096, "bf16") == (256, 256, 1)
+    assert rar.loss_tiling(rar.LOSS_Z, 8192, 128000, 4096, "bf16") == (256, 256, 1, 128000)
+    # the vocabulary in pieces of whole tiles
+    assert rar.loss_tiling(rar.LOSS_Z_AGAIN, 8192, 128000, 4096, "bf16", "fp32") == (256, 256, 1, 16128)
+    assert rar.loss_tiling(rar.LOSS_DW, 8192, 128000, 4096, "bf16", "fp32")[:3] == (256, 256, 1)
