@@ -302,6 +302,35 @@ def test_repeated_calls_streams_and_graphs_give_the_same_bits():
         assert all(torch.equal(a, b) for a, b in zip(want, (y, dx, dw, db))), shift
 
 
+@pytest.mark.parametrize("rows", [3, 700])
+def test_what_a_workspace_held_reaches_nothing(rows):
+    g = gen(8)
+    counts, n, k = [rows, 0, 1], 264, 1032
+    t, e = rows + 1 + 2, 3
+    x, w, dz = matrix(g, t, k, "bf16"), matrix(g, e * n, k, "bf16", std=1 / math.sqrt(k)).unflatten(0, (e, n)), matrix(g, t, n, "bf16")
+    x[t - 2:], dz[t - 2:] = math.nan, math.nan
+    off = offsets_of(counts)
+
+    def scratch(direction):
+        return torch.full((rar.experts_workspace(direction, t, e, n, k, DT["bf16"]),), 255, dtype=torch.uint8, device="cuda")
+
+    y, dx = (torch.full((t, m), math.nan, device="cuda", dtype=DT["bf16"]) for m in (n, k))
+    dw, db = torch.full((e, n, k), math.nan, device="cuda"), torch.full((e, n), math.nan, device="cuda")
+    rar.experts_forward(x, w, off, out=y, workspace=scratch(rar.LINEAR_FORWARD))
+    rar.experts_backward_input(dz, w, off, out=dx, workspace=scratch(rar.LINEAR_BACKWARD_INPUT))
+    rar.experts_backward_weight(dz, x, off, dw, db, workspace=scratch(rar.LINEAR_BACKWARD_WEIGHT))
+    for i, rows_of in groups(counts):
+        want, _, tol = product64(x[rows_of], w[i].t())
+        close(y[rows_of], want, tol, "bf16", f"y of expert {i}")
+        want, _, tol = product64(dz[rows_of], w[i])
+        close(dx[rows_of], want, tol, "bf16", f"dx of expert {i}")
+        want, _, tol = product64(dz[rows_of].t(), x[rows_of])
+        close(dw[i], want, tol, "fp32", f"dw of expert {i}")
+        want = dz[rows_of].double().sum(0)
+        close(db[i], want, 2 * (counts[i] + 2) * U * dz[rows_of].double().abs().sum(0), "fp32", f"db of expert {i}")
+    assert behind_untouched(y, counts) and behind_untouched(dx, counts)
+
+
 def test_arguments():
     x, w = torch.zeros(6, 8, device="cuda"), torch.zeros(2, 4, 8, device="cuda")
     off = torch.tensor([0, 3, 6], device="cuda")

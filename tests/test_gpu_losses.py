@@ -379,6 +379,26 @@ def test_repeated_calls_streams_and_graphs_give_the_same_bits(top):
         assert all(torch.equal(a, b) for a, b in zip(want, outs)), r
 
 
+@pytest.mark.parametrize("m, v", [(40, 300), (300, 9000)])
+@pytest.mark.parametrize("top", [0, 5])
+@pytest.mark.parametrize("types", [("fp32", "fp32"), ("bf16", "fp32"), ("bf16", "bf16")], ids=str)
+def test_what_a_workspace_held_reaches_nothing(types, top, m, v):
+    c = Case(m, v, 72, types[0], top=top, ignored=0.4)
+    dw = torch.full((v, 72), math.nan, device="cuda", dtype=DT[types[1]])
+
+    def scratch(direction):
+        sizes = (m, v, 72, top, DT[types[0]], DT[types[1]]) if top else (m, v, 72, DT[types[0]], DT[types[1]])
+        need = (rar.distill_workspace if top else rar.cross_entropy_workspace)(direction, *sizes)
+        return torch.full((need,), 255, dtype=torch.uint8, device="cuda")   # NaN of either type
+
+    loss, lse = c.forward(workspace=scratch(rar.LOSS_FORWARD))
+    c.formulas()
+    c.check_forward(loss, lse)
+    dx = c.backward(lse, dw=dw, workspace=scratch(rar.LOSS_BACKWARD))
+    c.check_backward(dx, dw, types[1])
+    assert bool((dx[~c.counts] == 0).all())
+
+
 def test_workspaces_and_arguments():
     c = Case(40, 300, 64, "bf16")
     need = rar.cross_entropy_workspace(rar.LOSS_FORWARD, 40, 300, 64, torch.bfloat16)
