@@ -4,6 +4,12 @@
 // One launch covers all experts. Their bounds are on the device, so nothing
 // waits for the host: the grid is what the worst bounds would need, and each
 // block finds its expert by a scan over the bounds, 64 a wave at a time.
+//
+// What bounds it: with some 100 to 300 rows an expert the weights' bytes, and the rows of
+// tiles that are not full. bf16, 16384 rows of 64 experts, 4096 x 2048: forward with
+// z kept 450 us (1.8 GB read, of 1.14 needed, and 0.26 written: 4.6 TB/s; the matrix
+// units busy 37 %), weight gradient added to fp32 870 (2.7 GB read and 2.1 written,
+// 5.6 TB/s). 16 rows of 32: 30 us, 165 MB of weights at 5.4 TB/s.
 #include "linear_host.h"
 
 namespace ddp {

@@ -12,6 +12,14 @@
 // and a sum a row. Backward makes z again, a piece of the vocabulary at a time:
 // dz of the piece, then its part of dx, kept in fp32 from piece to piece, and
 // its rows of dw.
+//
+// What bounds it: the matrix instructions of four products, five with an fp32 dw of
+// bf16 data, whose two terms are the price of dw's 2^-17. 8192 rows (2 % of
+// them not counted), 128000 columns of 4096, bf16: z and its statistics 6.5 ms
+// (1300 TFLOP/s, the matrix units busy 78 %; the library's bare product 1420), then by
+// pieces of 16128 columns dz 0.89 (1190), dx 0.93 (1140) and dw in two terms
+// 1.75 (1210): 34 ms in all. Making z again costs 7 of them; kept in bf16 it would take
+// 2 GiB. Few rows: the weights' bytes. Small sizes: seven launches of 4 to 7 us.
 #include <climits>
 
 #include "linear_host.h"
@@ -23,6 +31,7 @@ constexpr int32_t kMostTop = 1024;
 // Operands of direct loads have leading dimensions up to 2^21 and fewer than
 // 2^31 chunks of 16 bytes, and those in the scratch are always loaded so: the
 // gathered rows, and dz, whose pieces have 4096 columns where the rows are most.
+constexpr int64_t kCopyRows = 2048;  // of a forward pass; backward two products read the copy
 constexpr int64_t kMostRows = int64_t(1) << 20, kMostIns = int64_t(1) << 21;
 
 // ---------------------------------------------------------------- a teacher's top logits
@@ -224,6 +233,41 @@ __global__ __launch_bounds__(kThreads) void k_rows(RowsArgs g) {
   }
 }
 
+// ---------------------------------------------------------------- weights whose rows are not whole chunks
+
+// Rows of w, of 8 elements and more, in whole chunks of 16 bytes with zeros from K on:
+// what direct loads need. Four chunks a lane, all under way at once: a row's last chunk
+// is loaded from where it is whole, and shifted. Memory bounds it.
+constexpr int kCopied = 4;
+
+__global__ __launch_bounds__(kThreads) void k_whole_rows(const uint16_t* w, int64_t ldw, uint32_t chunks, uint32_t per_row, int32_t K,
+                                                         u32x4* out) {
+  const uint32_t first = blockIdx.x * uint32_t(kCopied * kThreads) + threadIdx.x;
+  u32x4 v[kCopied];
+  int32_t past[kCopied];  // elements of the chunk behind the row
+#pragma unroll
+  for (int u = 0; u < kCopied; ++u) {
+    const uint32_t q = first + u * kThreads < chunks ? first + u * kThreads : chunks - 1;
+    const uint32_t row = q / per_row;
+    const int32_t j = int32_t(q - row * per_row) * 8;
+    past[u] = j + 8 > K ? j + 8 - K : 0;
+    v[u] = load_at<false, u32x4_at2>(w + (int64_t(row) * ldw + j - past[u]), 0);
+  }
+#pragma unroll
+  for (int u = 0; u < kCopied; ++u) {
+    uint64_t lo = v[u].x | uint64_t(v[u].y) << 32, hi = v[u].z | uint64_t(v[u].w) << 32;
+    const int bits = 16 * past[u];
+    if (bits >= 64) {
+      lo = hi >> (bits - 64);
+      hi = 0;
+    } else if (bits > 0) {
+      lo = lo >> bits | hi << (64 - bits);
+      hi >>= bits;
+    }
+    if (first + u * kThreads < chunks) out[first + u * kThreads] = u32x4{uint32_t(lo), uint32_t(lo >> 32), uint32_t(hi), uint32_t(hi >> 32)};
+  }
+}
+
 // ---------------------------------------------------------------- the rows' losses
 
 struct JoinArgs {
@@ -329,16 +373,27 @@ struct Head {
   // fp32 gradients of bf16 data: dz in two terms.
   int32_t terms() const { return dtype == DDP_BF16 && grad_dtype == DDP_FP32 ? 2 : 1; }
   bool w_whole() const { return whole_chunks(w, ldw, V, K, dtype); }
+  // Whether the weights are copied to whole chunks, a piece at a time: of this width no
+  // rows are, and from so many rows on the copy costs less than what loads at any alignment
+  // and smaller tiles do. (32003 columns of 2047, without and with it: forward of 1030 rows
+  // 203 us and 213, 2050 366 and 324, 8000 1280 and 934; backward of 520 rows 385 and 362, 1030
+  // 629 and 538, 2050 1142 and 931, 8000 3642 and 2771. 5003 of 101: no gain before 8000 rows.
+  // How many rows count is on the device: backward of 1037, half of which do, 32003 of 1001: 206
+  // us and 200.)
+  bool copies() const { return dtype == DDP_BF16 && K % 8 != 0 && K >= 128 && M >= (backward ? kCopyRows / 2 : kCopyRows); }
 };
 
 // Columns of a piece, and pieces. A piece of dz should lie in the Infinity Cache
 // for the two products that read it, but be long enough that dx's sum over it
-// is worth the pass over dx in fp32 that each piece costs.
+// is worth the pass over dx in fp32 that each piece costs. A copy of the weights has
+// 128 MiB, or 4096 rows.
 struct Pieces {
   int64_t columns, number;
 };
 Pieces pieces_of(const Head& h) {
-  const int64_t most = std::min<int64_t>(1 << 20, std::max<int64_t>(4096, (int64_t(1) << 27) / std::max<int64_t>(h.M, 1)));
+  int64_t most = h.V;
+  if (h.backward) most = std::min<int64_t>(1 << 20, std::max<int64_t>(4096, (int64_t(1) << 27) / std::max<int64_t>(h.M, 1)));
+  if (h.copies()) most = std::min(most, std::max<int64_t>(4096, (int64_t(1) << 26) / h.ldg()));
   const int64_t columns = round_up(div_up(h.V, div_up(h.V, most)), 256);
   return {columns, div_up(h.V, columns)};
 }
@@ -353,6 +408,7 @@ struct Scratch {
   int32_t* ids;
   float* weights;
   uint16_t* starts;
+  char* whole;       // the weights' copy
   float* stats;
   float* picked;
   char* dz;
@@ -379,6 +435,7 @@ Scratch scratch_of(const Head& h, void* base) {
     take(s.weights, h.M * h.top * 4);
     take(s.starts, h.M * (tiles + 1) * 2);
   }
+  if (h.copies()) take(s.whole, pieces_of(h).columns * h.ldg() * eb);
   if (!h.backward) {
     take(s.stats, tiles * 2 * h.M * 4);
     take(s.picked, h.M * std::max(h.top, 1) * 4);
@@ -416,9 +473,8 @@ int check_top(const char* fn, const Head& h) {
   return DDP_OK;
 }
 
-// The rows that count, and a teacher's entries; g: the products' arguments that
-// all have in common.
-// (not gathered where they are in_place).
+// The rows that count (not gathered where they are in_place), and a teacher's
+// entries; g: the products' arguments that all have in common.
 template <int DT>
 int launch_rows_that_count(const Head& h, const Scratch& w, int width, bool in_place, RowsArgs r, LinearArgs& g, const char* fn,
                            hipStream_t s) {
@@ -458,23 +514,45 @@ int launch_rows_that_count(const Head& h, const Scratch& w, int width, bool in_p
   return DDP_OK;
 }
 
+// Columns v0 .. v0 + n of the vocabulary as an operand of g, copied to whole chunks or in place.
+template <int DT>
+int launch_weights(const Head& h, const Scratch& w, int64_t v0, int64_t n, LinearArgs& g, const char* fn, hipStream_t s) {
+  g.b = static_cast<const char*>(h.w) + v0 * h.ldw * elem_bytes(DT);
+  if (!h.copies()) return DDP_OK;
+  const int64_t per_row = h.ldg() / 8, chunks = n * per_row;
+  hipLaunchKernelGGL(k_whole_rows, dim3(unsigned(div_up(chunks, kCopied * kThreads))), dim3(kThreads), 0, s,
+                     static_cast<const uint16_t*>(g.b), h.ldw, uint32_t(chunks), uint32_t(per_row), int32_t(h.K), reinterpret_cast<u32x4*>(w.whole));
+  DDP_HIP_TRY(hipGetLastError(), fn);
+  g.b = w.whole, g.ldb = h.ldg(), g.b_room = int32_t(h.ldg() - h.K);
+  return DDP_OK;
+}
+
 template <int DT>
 int loss_forward(const Head& h, float* loss, float* lse, void* workspace, const char* fn, hipStream_t s) {
   const Scratch w = scratch_of(h, workspace);
   // Few rows are a tile or two whether they count or not, and a launch less counts.
   const bool in_place = h.M <= 64;
-  const bool direct = h.w_whole() && (!in_place || whole_chunks(h.x, h.ldx, h.M, h.K, DT));
-  const Cut c = cut_of(kRowStats, h.M, h.V, h.K, DT, direct, 0, 1);
-  LinearArgs g{};
+  const bool direct = h.copies() || (h.w_whole() && (!in_place || whole_chunks(h.x, h.ldx, h.M, h.K, DT)));
+  const Pieces p = pieces_of(h);
+  const Cut c = cut_of(kRowStats, h.M, std::min(p.columns, h.V), h.K, DT, direct, 0, 1);
+  LinearArgs all{};
   RowsArgs r{};
   r.loss = loss, r.lse = lse;
-  int st = launch_rows_that_count<DT>(h, w, c.tile, in_place, r, g, fn, s);
+  int st = launch_rows_that_count<DT>(h, w, c.tile, in_place, r, all, fn, s);
   if (st != DDP_OK) return st;
-  g.b = h.w, g.J = h.V;
-  g.head.stats = w.stats, g.head.picked = w.picked;
-  st = launch_groups<DT, kRowStats>(g, c, direct, fn, s);
-  if (st != DDP_OK) return st;
-  const JoinArgs j{g.bounds, g.row_of, h.M, g.tiles_j, g.head, h.temperature * h.temperature, loss, lse};
+  all.head.stats = w.stats, all.head.picked = w.picked;
+  for (int64_t v0 = 0; v0 < h.V; v0 += p.columns) {
+    LinearArgs g = all;
+    g.J = std::min(p.columns, h.V - v0);
+    st = launch_weights<DT>(h, w, v0, g.J, g, fn, s);
+    if (st != DDP_OK) return st;
+    g.head.j_base = v0;
+    g.head.stats += v0 / c.tile * 2 * h.M;
+    st = launch_groups<DT, kRowStats>(g, c, direct, fn, s);
+    if (st != DDP_OK) return st;
+  }
+  const int32_t tiles = int32_t(div_up(h.V, c.tile));
+  const JoinArgs j{all.bounds, all.row_of, h.M, tiles, all.head, h.temperature * h.temperature, loss, lse};
   hipLaunchKernelGGL(k_loss_join, dim3(unsigned(div_up(h.M, kJoinRows))), dim3(kThreads), 0, s, j);
   DDP_HIP_TRY(hipGetLastError(), fn);
   return DDP_OK;
@@ -496,7 +574,7 @@ int loss_backward(const Head& h, const float* lse, const float* dloss, void* dx,
                   int32_t accumulate, void* workspace, const char* fn, hipStream_t s) {
   const Scratch w = scratch_of(h, workspace);
   const Pieces p = pieces_of(h);
-  const bool w_whole = h.w_whole();
+  const bool w_whole = h.copies() || h.w_whole();
   const Cut c = cut_of(kRowStats, h.M, std::min(p.columns, h.V), h.K, DT, w_whole, 0, 1);  // of the products that make z
   constexpr int64_t ES = DT == DDP_BF16 ? 2 : 4;
   LinearArgs all{};
@@ -511,19 +589,20 @@ int loss_backward(const Head& h, const float* lse, const float* dloss, void* dx,
   if (h.M == 0) dx = nullptr;
   for (int64_t v0 = 0; v0 < h.V; v0 += p.columns) {
     const int64_t n = std::min(p.columns, h.V - v0);
-    const char* const weights = static_cast<const char*>(h.w) + v0 * h.ldw * ES;
+    LinearArgs piece = all;
+    st = launch_weights<DT>(h, w, v0, n, piece, fn, s);
+    if (st != DDP_OK) return st;
     // dz of the piece
-    LinearArgs g = all;
-    g.b = weights, g.J = n;
+    LinearArgs g = piece;
+    g.J = n;
     g.c = w.dz, g.ldc = w.lddz, g.term = h.M * w.lddz;
     g.head.j_base = v0;
     st = launch_groups<DT, kRowSlopes>(g, c, w_whole, fn, s);
     if (st != DDP_OK) return st;
     const int32_t room = int32_t(round_up(n, 8) - n);
     if (dx != nullptr) {
-      g = all;
+      g = piece;
       g.a = w.dz, g.lda = w.lddz, g.a_room = room;
-      g.b = weights;
       g.J = h.K, g.K = n;
       g.c = dx, g.ldc = lddx;
       g.sums = w.sums, g.first = v0 == 0, g.last = v0 + n == h.V;
@@ -643,9 +722,10 @@ extern "C" int ddp_loss_tiling(int32_t product, int64_t M, int64_t V, int64_t K,
   const Head h = head_of(M, V, K, 0, dtype, grad_dtype, product > 0);
   int st = check_head(fn, h);
   if (st != DDP_OK) return st;
-  const int64_t n = product == 0 ? V : std::min(pieces_of(h).columns, V);
-  const Cut c = product < 2    ? cut_of(kRowStats, M, n, K, dtype, direct != 0, 0, 1)
-                : product == 2 ? cut_of(kInputPiece, M, K, n, dtype, direct != 0, 0, 128)
+  const int64_t n = std::min(pieces_of(h).columns, V);
+  const bool whole = direct != 0 || h.copies();
+  const Cut c = product < 2    ? cut_of(kRowStats, M, n, K, dtype, whole, 0, 1)
+                : product == 2 ? cut_of(kInputPiece, M, K, n, dtype, whole, 0, 128)
                                : cut_of(kWeightTerms, n, K, M * h.terms(), dtype, true);
   *rows = c.rows();
   *columns = c.tile;

@@ -208,6 +208,18 @@ def test_pieces_of_the_vocabulary(dtype, grads, top):
     run_case(Case(40000, 9003, 24, dtype, top=top, ignored=0.05), grads, True, 0, 0)
 
 
+# rows enough that weights of a width that no whole chunks have are copied, in one piece and in two
+@pytest.mark.parametrize("size", [(1024, 3001, 135), (2050, 700, 1001), (2060, 5000, 16390)], ids=str)
+@pytest.mark.parametrize("layout", [(0, 0), (3, 1)], ids=["dense", "odd rows"])
+@pytest.mark.parametrize("grads, top", [("fp32", 0), ("bf16", 5)])
+def test_weights_in_whole_chunks(size, layout, grads, top):
+    m, v, k = size
+    pieces = [rar.loss_tiling(p, m, v, k, "bf16", grads, False)[3] for p in (rar.LOSS_Z, rar.LOSS_DX)]
+    assert pieces == ([2560, 2560] if k == 16390 else [v, v])
+    assert rar.loss_tiling(rar.LOSS_DX, m, v, k, "bf16", grads, False) == rar.loss_tiling(rar.LOSS_DX, m, v, k, "bf16", grads, True)
+    run_case(Case(m, v, k, "bf16", top=top, ignored=0.2, pad=layout[0], shift=layout[1]), grads, grads == "fp32", *layout)
+
+
 def test_more_columns_than_one_launch_holds():
     """2^22 blocks of 64 columns and a few more, and 257 pieces backward: the gradients of one row of one input."""
     v = 64 * (1 << 22) + 1000
