@@ -14,7 +14,7 @@
 // its rows of dw.
 //
 // What bounds it: the matrix instructions of four products, five with an fp32 dw of
-// bf16 data, whose two terms are the price of dw's 2^-17. 8192 rows (2 % of
+// bf16 data, whose two terms are the price of dw's 2^-16. 8192 rows (2 % of
 // them not counted), 128000 columns of 4096, bf16: z and its statistics 6.5 ms
 // (1300 TFLOP/s, the matrix units busy 78 %; the library's bare product 1420), then by
 // pieces of 16128 columns dz 0.89 (1190), dx 0.93 (1140) and dw in two terms
