@@ -261,9 +261,8 @@ int ddp_experts_backward_weight(const void* dz, int64_t lddz, const void* x, int
  * loss_i, so a mean's is dloss = 1 / its count. lse is as the forward call left it. dx and dw may be NULL (not
  * wanted); dw is of grad_dtype (`dtype`, or fp32 gradients of bf16 data),
  * overwritten or, with accumulate = 1, added to with one rounding, and may lie in a gradient
- * arena. Sums and statistics are fp32. The products of a bf16 gradient take dz
- * rounded to bf16; those of an fp32 dw of bf16 data take it as two bf16 terms,
- * which are off by 2^-16 of it at most.
+ * arena. Sums and statistics are fp32. With bf16 data the products take dz as two
+ * bf16 terms, which are off by 2^-16 of it at most.
  * Of many rows, bf16 weights whose K is not a multiple of 8 are copied to rows of
  * whole 16 bytes in the scratch, a piece of 128 MiB (or 4096 columns) at a time.
  *

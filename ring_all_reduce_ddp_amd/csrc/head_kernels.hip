@@ -13,8 +13,9 @@
 // dz of the piece, then its part of dx, kept in fp32 from piece to piece, and
 // its rows of dw.
 //
-// What bounds it: the matrix instructions of four products, five with an fp32 dw of
-// bf16 data, whose two terms are the price of dw's 2^-16. 8192 rows (2 % of
+// What bounds it: the matrix instructions of four products, six with bf16 data, whose
+// dz is taken in two terms of bf16: off by 2^-16, where one term's 2^-8 would be as much
+// again as the gradients' own rounding. 8192 rows (2 % of
 // them not counted), 128000 columns of 4096, bf16: z and its statistics 6.5 ms
 // (1300 TFLOP/s, the matrix units busy 78 %; the library's bare product 1420), then by
 // pieces of 16128 columns dz 0.89 (1190), dx 0.93 (1140) and dw in two terms
@@ -370,8 +371,8 @@ struct Head {
   float temperature;
 
   int64_t ldg() const { return round_up(K, 8); }   // of the gathered rows
-  // fp32 gradients of bf16 data: dz in two terms.
-  int32_t terms() const { return dtype == DDP_BF16 && grad_dtype == DDP_FP32 ? 2 : 1; }
+  // bf16 data: dz in two terms, as one would be as coarse as the gradients' own rounding.
+  int32_t terms() const { return dtype == DDP_BF16 ? 2 : 1; }
   bool w_whole() const { return whole_chunks(w, ldw, V, K, dtype); }
   // Whether the weights are copied to whole chunks, a piece at a time: of this width no
   // rows are, and from so many rows on the copy costs less than what loads at any alignment
@@ -383,16 +384,21 @@ struct Head {
   bool copies() const { return dtype == DDP_BF16 && K % 8 != 0 && K >= 128 && M >= (backward ? kCopyRows / 2 : kCopyRows); }
 };
 
-// Columns of a piece, and pieces. A piece of dz should lie in the Infinity Cache
-// for the two products that read it, but be long enough that dx's sum over it
-// is worth the pass over dx in fp32 that each piece costs. A copy of the weights has
+// Columns of a piece, and pieces. A piece of dz, 4 bytes a value, should lie in the
+// Infinity Cache for the two products that read it, but be long enough that dx's
+// sum over it is worth the pass over dx in fp32 that each piece costs: 128 MiB, or 4096
+// columns. (Backward, bf16, in pieces of 128, 256 and 512 MiB: 8192 rows, 128000 columns of
+// 4096, 35.0, 35.7 and 35.8 ms; 4096 x 64000 x 2048 4.59, 4.72 and 4.73. 32768 x 32000 x 1024, in
+// pieces of 4096 columns and 1024, 10.4 and 12.5.) With an fp32 dw of bf16 data four times that, 512 MiB,
+// which takes 3 % longer (36.0 ms and 34.9; 4.77 and 4.62). A copy of the weights has
 // 128 MiB, or 4096 rows.
 struct Pieces {
   int64_t columns, number;
 };
 Pieces pieces_of(const Head& h) {
   int64_t most = h.V;
-  if (h.backward) most = std::min<int64_t>(1 << 20, std::max<int64_t>(4096, (int64_t(1) << 27) / std::max<int64_t>(h.M, 1)));
+  const int64_t values = int64_t(1) << (h.dtype == DDP_BF16 && h.grad_dtype == DDP_FP32 ? 27 : 25);
+  if (h.backward) most = std::min<int64_t>(1 << 20, std::max<int64_t>(4096, values / std::max<int64_t>(h.M, 1)));
   if (h.copies()) most = std::min(most, std::max<int64_t>(4096, (int64_t(1) << 26) / h.ldg()));
   const int64_t columns = round_up(div_up(h.V, div_up(h.V, most)), 256);
   return {columns, div_up(h.V, columns)};
@@ -585,7 +591,7 @@ int loss_backward(const Head& h, const float* lse, const float* dloss, void* dx,
   if (st != DDP_OK) return st;
   all.head.lse = lse, all.head.dloss = dloss;
   all.factor = r.factor;
-  all.terms = dw != nullptr ? h.terms() : 1;
+  all.terms = h.terms();
   if (h.M == 0) dx = nullptr;
   for (int64_t v0 = 0; v0 < h.V; v0 += p.columns) {
     const int64_t n = std::min(p.columns, h.V - v0);
@@ -602,7 +608,7 @@ int loss_backward(const Head& h, const float* lse, const float* dloss, void* dx,
     const int32_t room = int32_t(round_up(n, 8) - n);
     if (dx != nullptr) {
       g = piece;
-      g.a = w.dz, g.lda = w.lddz, g.a_room = room;
+      g.a = w.dz, g.lda = w.lddz, g.a_room = room, g.term = h.M * w.lddz * ES;
       g.J = h.K, g.K = n;
       g.c = dx, g.ldc = lddx;
       g.sums = w.sums, g.first = v0 == 0, g.last = v0 + n == h.V;

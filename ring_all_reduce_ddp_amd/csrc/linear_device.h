@@ -9,8 +9,10 @@
 
 //   row statistics   of z = x w^T: each row's maximum and sum of exponentials (the losses of an output layer)
 //   row slopes       the loss's gradient with respect to z, from z made again
-//   input pieces     dx += dz w over a piece of dz's columns, kept in fp32 between pieces
-//   weight terms     dw (+)= (dz1 + dz2)^T x, dz in two terms of 16 bits
+//   input pieces     dx += (dz1 + dz2) w over a piece of dz's columns, kept in fp32 between pieces
+//   weight terms     dw (+)= (dz1 + dz2)^T x
+//
+// (dz in two terms of 16 bits, or in fp32 one)
 //
 // each of the rows of one group or of several (experts) whose bounds are on the device.
 //
@@ -108,7 +110,7 @@ struct LinearArgs {
   // Operands with room behind their rows, which holds zeros.
   int32_t a_room, b_room;  // elements of it that belong to the last chunk
   int32_t stream_c;        // weight gradients: C passes the caches
-  int32_t terms;           // weight terms: 1 or 2
+  int32_t terms;           // input pieces, weight terms, row slopes: of dz, 1 or 2
   int64_t term;            // bytes from A's first term to its second, or elements of C (row slopes)
   float* sums;             // input pieces: the sum over pieces, fp32 (NULL: one piece)
   int32_t first, last;     // input pieces: whether this is the first, the last piece
@@ -120,6 +122,7 @@ struct LinearArgs {
 // Products beside the linear layer's three directions.
 constexpr int kRowStats = 3, kRowSlopes = 4, kInputPiece = 5, kWeightTerms = 6;
 constexpr bool one_group(int dir) { return dir >= kRowStats; }  // of grouped products, those that have only one
+constexpr bool has_terms(int dir) { return dir == kInputPiece || dir == kWeightTerms; }
 constexpr bool is_weight(int dir) { return dir == DDP_LINEAR_BACKWARD_WEIGHT || dir == kWeightTerms; }
 constexpr bool is_head(int dir) { return dir == kRowStats || dir == kRowSlopes; }
 constexpr bool a_along(int dir) { return !is_weight(dir); }
@@ -1116,14 +1119,14 @@ __global__ __launch_bounds__(WI * WJ * WK * 64, 2) void k_linear(LinearArgs g) {
   const bool sum_rows = DIR == DDP_LINEAR_BACKWARD_WEIGHT && g.row_sums != nullptr && wave % WJ == 0;
   float row_sum[FI] = {};
 
-  const int terms = DIR == kWeightTerms ? g.terms : 1;
+  const int terms = has_terms(DIR) ? g.terms : 1;
 #pragma unroll 1
-  for (int term = 0; term < (DIR == kWeightTerms ? terms : 1); ++term) {
+  for (int term = 0; term < (has_terms(DIR) ? terms : 1); ++term) {
     if (steps <= 0) break;
-    if (DIR == kWeightTerms && term > 0) __syncthreads();  // every wave is done with the first term's operands
+    if (has_terms(DIR) && term > 0) __syncthreads();  // every wave is done with the first term's operands
     LA la;
     LB lb;
-    la.init(static_cast<const char*>(g.a) + (DIR == kWeightTerms ? term * g.term : 0), g.lda, g.I, g.K, i0, k0, k1, g.a_room);
+    la.init(static_cast<const char*>(g.a) + (has_terms(DIR) ? term * g.term : 0), g.lda, g.I, g.K, i0, k0, k1, g.a_room);
     lb.init(g.b, g.ldb, g.J, g.K, j0, k0, k1, g.b_room);
     if constexpr (TURNED) {
       if (g.spread && (k1 - k0) % TA::STEP == 0) {
