@@ -237,9 +237,8 @@ int ddp_experts_backward_weight(const void* dz, int64_t lddz, const void* x, int
 
 /* ---------------------------------------------------------------- losses of an output layer
  * z = x w^T, x[M][K] and w[V][K] as in the linear layer, V the vocabulary. Its
- * M x V values are made where they are used and not kept: neither call needs
- * room for them, and the backward pass makes them again, a piece of the
- * vocabulary at a time. p_ij = exp(z_ij - lse_i), lse_i = log sum_j exp(z_ij).
+ * M x V values are made where they are used and not kept: the backward pass makes
+ * them again, a piece of the vocabulary at a time, and has room for one piece's dz. p_ij = exp(z_ij - lse_i), lse_i = log sum_j exp(z_ij).
  *
  * Cross entropy: row i has a target t_i (int64 on the device) and
  *   loss_i = lse_i - z_it,   dz_ij = dloss_i (p_ij - [j = t_i]).
@@ -271,7 +270,13 @@ int ddp_experts_backward_weight(const void* dz, int64_t lddz, const void* x, int
  *
  * ddp_cross_entropy_workspace: bytes of scratch for a direction and sizes on
  * the current device, under the conditions of ddp_linear_workspace; grad_dtype
- * counts for the backward direction. */
+ * counts for the backward direction. Both directions gather the rows that count:
+ * M K elements. Forward adds 8 bytes a row for each 32 to 256 columns of the
+ * vocabulary. Backward adds a piece's dz, 4 bytes a value, of at most 2^25 values or
+ * 4096 columns (an fp32 dw of bf16 data: 2^27 values), beyond 32768 rows 2^27 values or
+ * 1024 columns; of more pieces than one, dx in fp32, 4 M K bytes; and up to
+ * 256 MiB of sums in parts. Distillation adds 8 bytes an entry, and 2 a row for
+ * each 32 to 256 columns. */
 #define DDP_LOSS_FORWARD 0
 #define DDP_LOSS_BACKWARD 1
 int ddp_cross_entropy_workspace(int32_t direction, int64_t M, int64_t V, int64_t K, int32_t dtype, int32_t grad_dtype,

@@ -389,19 +389,29 @@ struct Head {
 // sum over it is worth the pass over dx in fp32 that each piece costs: 128 MiB, or 4096
 // columns. (Backward, bf16, in pieces of 128, 256 and 512 MiB: 8192 rows, 128000 columns of
 // 4096, 35.0, 35.7 and 35.8 ms; 4096 x 64000 x 2048 4.59, 4.72 and 4.73. 32768 x 32000 x 1024, in
-// pieces of 4096 columns and 1024, 10.4 and 12.5.) With an fp32 dw of bf16 data four times that, 512 MiB,
-// which takes 3 % longer (36.0 ms and 34.9; 4.77 and 4.62). A copy of the weights has
+// pieces of 4096 columns and 1024, 10.4 and 12.5.) With an fp32 dw of bf16 data 512 MiB,
+// which takes 3 % longer (36.0 ms and 34.9; 4.77 and 4.62). Never more than 512 MiB, or
+// 1024 columns: beyond 32768 rows, room counts more than time (65536 x 16000 x 1024, 2048 columns and 4096:
+// 11.3 and 10.3 ms; 131072 x 8000 x 512, 1024 and 4096: 7.4 and 6.3). A copy of the weights has
 // 128 MiB, or 4096 rows.
 struct Pieces {
   int64_t columns, number;
 };
 Pieces pieces_of(const Head& h) {
   int64_t most = h.V;
-  const int64_t values = int64_t(1) << (h.dtype == DDP_BF16 && h.grad_dtype == DDP_FP32 ? 27 : 25);
-  if (h.backward) most = std::min<int64_t>(1 << 20, std::max<int64_t>(4096, values / std::max<int64_t>(h.M, 1)));
+  if (h.backward) {
+    const int64_t M = std::max<int64_t>(h.M, 1);
+    most = std::min<int64_t>(1 << 20, std::max<int64_t>(1024, (int64_t(1) << 27) / M));
+    if (h.dtype != DDP_BF16 || h.grad_dtype != DDP_FP32) most = std::min(most, std::max<int64_t>(4096, (int64_t(1) << 25) / M));
+  }
   if (h.copies()) most = std::min(most, std::max<int64_t>(4096, (int64_t(1) << 26) / h.ldg()));
   const int64_t columns = round_up(div_up(h.V, div_up(h.V, most)), 256);
   return {columns, div_up(h.V, columns)};
+}
+
+// How the products that make z are cut, with or without direct loads.
+Cut z_cut(const Head& h, bool direct) {
+  return cut_of(kRowStats, h.M, std::min(pieces_of(h).columns, h.V), h.K, h.dtype, direct || h.copies(), 0, 1);
 }
 
 // Where a call's scratch lies; with base NULL, only its size.
@@ -430,7 +440,7 @@ Scratch scratch_of(const Head& h, void* base) {
     p = base == nullptr ? nullptr : reinterpret_cast<std::remove_reference_t<decltype(p)>>(static_cast<char*>(base) + at);
     at += round_up(bytes, 256);
   };
-  const int64_t eb = elem_bytes(h.dtype), tiles = div_up(h.V, h.M <= kFlatRows ? 32 : 64);  // of any width
+  const int64_t eb = elem_bytes(h.dtype), tiles = div_up(h.V, std::min(z_cut(h, false).tile, z_cut(h, true).tile));
   take(s.bounds, 24);
   take(s.row_of, h.M * 4);
   take(s.rows, h.M * h.ldg() * eb);
@@ -540,7 +550,7 @@ int loss_forward(const Head& h, float* loss, float* lse, void* workspace, const 
   const bool in_place = h.M <= 64;
   const bool direct = h.copies() || (h.w_whole() && (!in_place || whole_chunks(h.x, h.ldx, h.M, h.K, DT)));
   const Pieces p = pieces_of(h);
-  const Cut c = cut_of(kRowStats, h.M, std::min(p.columns, h.V), h.K, DT, direct, 0, 1);
+  const Cut c = z_cut(h, direct);
   LinearArgs all{};
   RowsArgs r{};
   r.loss = loss, r.lse = lse;
@@ -581,7 +591,7 @@ int loss_backward(const Head& h, const float* lse, const float* dloss, void* dx,
   const Scratch w = scratch_of(h, workspace);
   const Pieces p = pieces_of(h);
   const bool w_whole = h.copies() || h.w_whole();
-  const Cut c = cut_of(kRowStats, h.M, std::min(p.columns, h.V), h.K, DT, w_whole, 0, 1);  // of the products that make z
+  const Cut c = z_cut(h, w_whole);
   constexpr int64_t ES = DT == DDP_BF16 ? 2 : 4;
   LinearArgs all{};
   RowsArgs r{};
@@ -730,7 +740,7 @@ extern "C" int ddp_loss_tiling(int32_t product, int64_t M, int64_t V, int64_t K,
   if (st != DDP_OK) return st;
   const int64_t n = std::min(pieces_of(h).columns, V);
   const bool whole = direct != 0 || h.copies();
-  const Cut c = product < 2    ? cut_of(kRowStats, M, n, K, dtype, whole, 0, 1)
+  const Cut c = product < 2    ? z_cut(h, whole)
                 : product == 2 ? cut_of(kInputPiece, M, K, n, dtype, whole, 0, 128)
                                : cut_of(kWeightTerms, n, K, M * h.terms(), dtype, true);
   *rows = c.rows();
