@@ -262,8 +262,8 @@ int ddp_experts_backward_weight(const void* dz, int64_t lddz, const void* x, int
  * overwritten or, with accumulate = 1, added to with one rounding, and may lie in a gradient
  * arena. Sums and statistics are fp32. With bf16 data the products take dz as two
  * bf16 terms, which are off by 2^-16 of it at most.
- * Of many rows, bf16 weights whose K is not a multiple of 8 are copied to rows of
- * whole 16 bytes in the scratch, a piece of 128 MiB (or 4096 columns) at a time.
+ * Of many rows and columns, bf16 weights whose K is not a multiple of 8 are copied to rows
+ * of whole 16 bytes in the scratch, a piece of 128 MiB (or 4096 columns) at a time.
  *
  * 1 <= V < 2^31, 0 <= M <= 2^20, 1 <= K <= 2^21, M K <= 2^32, M V < 2^42,
  * 1 <= C <= 1024, T > 0 and finite.

@@ -33,6 +33,7 @@ constexpr int32_t kMostTop = 1024;
 // 2^31 chunks of 16 bytes, and those in the scratch are always loaded so: the
 // gathered rows, and dz, whose pieces have 4096 columns where the rows are most.
 constexpr int64_t kCopyRows = 2048;  // of a forward pass; backward two products read the copy
+constexpr int64_t kCopyProducts = int64_t(12000000000);  // M V K
 constexpr int64_t kMostRows = int64_t(1) << 20, kMostIns = int64_t(1) << 21;
 
 // ---------------------------------------------------------------- a teacher's top logits
@@ -374,14 +375,20 @@ struct Head {
   // bf16 data: dz in two terms, as one would be as coarse as the gradients' own rounding.
   int32_t terms() const { return dtype == DDP_BF16 ? 2 : 1; }
   bool w_whole() const { return whole_chunks(w, ldw, V, K, dtype); }
-  // Whether the weights are copied to whole chunks, a piece at a time: of this width no
-  // rows are, and from so many rows on the copy costs less than what loads at any alignment
-  // and smaller tiles do. (32003 columns of 2047, without and with it: forward of 1030 rows
-  // 203 us and 213, 2050 366 and 324, 8000 1280 and 934; backward of 520 rows 385 and 362, 1030
-  // 629 and 538, 2050 1142 and 931, 8000 3642 and 2771. 5003 of 101: no gain before 8000 rows.
-  // How many rows count is on the device: backward of 1037, half of which do, 32003 of 1001: 206
-  // us and 200.)
-  bool copies() const { return dtype == DDP_BF16 && K % 8 != 0 && K >= 128 && M >= (backward ? kCopyRows / 2 : kCopyRows); }
+  // Whether the weights are copied to whole chunks, a piece at a time: those of a width that has none, where
+  // rows are many enough that the copy costs less than what loads at any alignment and smaller tiles do.
+  // Forward, without and with it: 32003 columns of 2047, 1030 rows 206 us and 215, 2050 370 and 327, 4100 701
+  // and 558; 5003 of 501, 2050 37 and 41, 4100 60 and 64, 8000 95 and 86; 1003 of 1001, 2050 31 and 36, 8000 50 and 49; 12003 of
+  // 135, 4100 70 and 64: so by the rows and the product's length. Backward: 32003 of 2047, 520 rows 569
+  // and 517, 1030 959 and 796, 4100 3340 and 2786; 5003 of 501, 1030 103 and 96, 4100 227 and 200; 1003 of 135,
+  // 1030 49 and 50, 2050 54 and 58, 8000 86 and 81: by the rows, as what small vocabularies lose is a few us.
+  // (Rows mean all of them: how many count is on the device. 1037 rows, of which half count, 32003 of
+  // 1001, backward: 206 and 200. Rows of a whole width that begin at odd places are not copied.)
+  bool copies() const {
+    if (dtype != DDP_BF16 || K % 8 == 0 || K < 128) return false;
+    if (backward) return M >= kCopyRows / 2;
+    return M >= kCopyRows && (M * V >= int64_t(25000000) || M * V >= kCopyProducts / K);
+  }
 };
 
 // Columns of a piece, and pieces. A piece of dz, 4 bytes a value, should lie in the
