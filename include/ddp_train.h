@@ -266,7 +266,7 @@ int ddp_experts_backward_weight(const void* dz, int64_t lddz, const void* x, int
  * of whole 16 bytes in the scratch, a piece of 128 MiB (or 4096 columns) at a time.
  *
  * 1 <= V < 2^31, 0 <= M <= 2^20, 1 <= K <= 2^21, M K <= 2^32, M V < 2^42,
- * 1 <= C <= 1024, T > 0 and finite.
+ * 1 <= C <= 1024, 2^-20 <= T <= 2^20.
  *
  * ddp_cross_entropy_workspace: bytes of scratch for a direction and sizes on
  * the current device, under the conditions of ddp_linear_workspace; grad_dtype

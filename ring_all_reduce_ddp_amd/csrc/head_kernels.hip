@@ -29,6 +29,7 @@ namespace ddp {
 namespace {
 
 constexpr int32_t kMostTop = 1024;
+constexpr float kLeastTemperature = 0x1p-20f, kMostTemperature = 0x1p20f;
 // Operands of direct loads have leading dimensions up to 2^21 and fewer than
 // 2^31 chunks of 16 bytes, and those in the scratch are always loaded so: the
 // gathered rows, and dz, whose pieces have 4096 columns where the rows are most.
@@ -801,8 +802,10 @@ int distill_head(const char* fn, Head& h, const void* x, int64_t ldx, const void
   if (st == DDP_OK) st = check_head(fn, h);
   if (st != DDP_OK) return st;
   if (!valid_dtype(teacher_dtype)) return fail(DDP_EINVAL, std::string(fn) + ": unknown teacher_dtype");
-  if (!(temperature > 0.0f) || !(1.0f / temperature > 0.0f) || !(1.0f / temperature < INFINITY))
-    return fail(DDP_EINVAL, std::string(fn) + ": temperature must be positive and finite");
+  // T^2 and logits / T have to keep clear of fp32's ends: the exponent of a power of z / T is off by 2^-24 of it,
+  // which beyond 2^31 is a factor that overflows.
+  if (!(temperature >= kLeastTemperature) || !(temperature <= kMostTemperature))
+    return fail(DDP_EINVAL, std::string(fn) + ": temperature must lie in [2^-20, 2^20]");
   return DDP_OK;
 }
 }  // namespace
