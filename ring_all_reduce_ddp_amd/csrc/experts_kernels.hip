@@ -7,9 +7,9 @@
 //
 // What bounds it: with some 100 to 300 rows an expert the weights' bytes, and the rows of
 // tiles that are not full. bf16, 16384 rows of 64 experts, 4096 x 2048: forward with
-// z kept 450 us (1.8 GB read, of 1.14 needed, and 0.26 written: 4.6 TB/s; the matrix
-// units busy 37 %), weight gradient added to fp32 870 (2.7 GB read and 2.1 written,
-// 5.6 TB/s). 16 rows of 32: 30 us, 165 MB of weights at 5.4 TB/s.
+// z kept 440 us (1.75 GB read, of 1.14 needed, and 0.27 written: 4.6 TB/s; the matrix
+// units busy 38 %), weight gradient added to fp32 870 (2.8 GB read and 2.2 written,
+// 5.7 TB/s). 16 rows of 32: 30 us, 168 MB of weights at 5.5 TB/s.
 #include "linear_host.h"
 
 namespace ddp {

@@ -14,13 +14,13 @@
 // its rows of dw.
 //
 // What bounds it: the matrix instructions of four products, six with bf16 data, whose
-// dz is taken in two terms of bf16: off by 2^-16, where one term's 2^-8 would be as much
-// again as the gradients' own rounding. 8192 rows (2 % of
-// them not counted), 128000 columns of 4096, bf16: z and its statistics 6.5 ms
-// (1300 TFLOP/s, the matrix units busy 78 %; the library's bare product 1420), then by
-// pieces of 16128 columns dz 0.89 (1190), dx 0.93 (1140) and dw in two terms
-// 1.75 (1210): 34 ms in all. Making z again costs 7 of them; kept in bf16 it would take
-// 2 GiB. Few rows: the weights' bytes. Small sizes: seven launches of 4 to 7 us.
+// dz is taken in two terms of bf16: off by 2^-16, where one term's 2^-8 left bf16 gradients
+// 1.8 to 2.2 thousandths off instead of the 1.66 of their own rounding. 8192 rows (2 % of
+// them not counted), 128000 columns of 4096, bf16: z and its statistics 6.3 ms
+// (1340 TFLOP/s, the matrix units busy 78 %; the library's bare product 1420), then by
+// pieces of 16128 columns dz 0.87 (1220), dx 1.76 (1200) and dw 1.72 (1230), both
+// in two terms: 41 ms in all. Making z again costs 7 of them; kept in bf16 it would take
+// 2 GiB. Few rows: the weights' bytes. Small sizes: seven launches of 4 to 8 us.
 #include <climits>
 
 #include "linear_host.h"
@@ -163,8 +163,10 @@ struct RowsArgs {
   __device__ __forceinline__ bool counts(int64_t i) const { return targets != nullptr ? targets[i] >= 0 : counted[i] != 0; }
 };
 
-// A block counts the rows before its own by itself: reading a flag each costs
-// less than a launch that would sum them.
+// A block counts the rows before its own by itself, and the last one finds the largest dloss: up to some
+// 10000 rows, reading a flag each costs less than a launch that would sum them. The reads grow with the square of the rows:
+// of a call with little else to do (64 columns, 8 inputs), forward, 4096 rows take 18 us, 16384 24, 65536 58, 2^18 340 and
+// 2^20 1440, the last of which read 17 GB of flags.
 template <int DT>
 __global__ __launch_bounds__(kThreads) void k_rows(RowsArgs g) {
   __shared__ int32_t waves[2][4];
@@ -398,7 +400,7 @@ struct Head {
 // columns. (Backward, bf16, in pieces of 128, 256 and 512 MiB: 8192 rows, 128000 columns of
 // 4096, 35.0, 35.7 and 35.8 ms; 4096 x 64000 x 2048 4.59, 4.72 and 4.73. 32768 x 32000 x 1024, in
 // pieces of 4096 columns and 1024, 10.4 and 12.5.) With an fp32 dw of bf16 data 512 MiB,
-// which takes 3 % longer (36.0 ms and 34.9; 4.77 and 4.62). Never more than 512 MiB, or
+// which takes 3 % longer (36.0 ms and 34.9; 4.77 and 4.62): the width that test_tilings holds. Never more than 512 MiB, or
 // 1024 columns: beyond 32768 rows, room counts more than time (65536 x 16000 x 1024, 2048 columns and 4096:
 // 11.3 and 10.3 ms; 131072 x 8000 x 512, 1024 and 4096: 7.4 and 6.3). A copy of the weights has
 // 128 MiB, or 4096 rows.

@@ -1011,7 +1011,7 @@ __global__ __launch_bounds__(WI * WJ * WK * 64, 2) void k_linear(LinearArgs g) {
   // so, 256 MiB in rows of 4096 bytes: 4.5 TB/s as it was, 5.7 so, 5.9 in rows of 4224.
   constexpr bool TURNED = GROUPS && LOAD == kDirect && b_along(DIR);
   // Two steps of chunks in registers where they fit beside the sums: 1 row of 19208 columns of 2045 in fp32,
-  // forward and backward, 300 us to 258.
+  // forward and backward, 252 us to 221.
   constexpr int PIPE = GROUPS && LOAD == kAny && WK == 1 && (TI < 128 || b_along(DIR)) ? 2 : 1;
   using LA = LoaderOf<LOAD, DT, TA, a_along(DIR), THREADS, TURNED, PIPE>;
   using LB = LoaderOf<LOAD, DT, TB, b_along(DIR), THREADS, TURNED, PIPE>;

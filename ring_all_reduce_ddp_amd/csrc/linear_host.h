@@ -25,8 +25,8 @@ constexpr int kFewRows = 4;
 
 // Flat tiles are for few rows, which read the other operand from memory: 32 rows,
 // 128 columns and four steps of 128 bytes in LDS or on their way, two blocks a CU.
-// (8 rows, 64000 columns of 2048 bf16, with the loss's other launches: 66.7 us, with
-// three steps 70.9, two 72.4, in tiles of 64 75.2.)
+// (Cross entropy of 8 rows, 64000 columns of 2048 bf16 from memory: forward 53 us, with three steps 53.5, two
+// 55, in tiles of 64 54; with the backward pass 270, 264, 269 and 306.)
 constexpr int kFlatRows = 32, kFlatStages = 4;
 
 // How a product is cut: the tile's side (256 needs direct loads), and in how
@@ -46,7 +46,12 @@ struct Cut {
 // The cut with the least time by a rough model in cycles. Its constants were
 // fitted to the times of 250 products of 5 to 8192 rows, 64 to 8192 columns
 // and terms, odd and even, on MI355X, each cut in up to 27 ways: the cut it
-// picks takes 1.9 % longer than the best of them in the mean, 31 % at worst.
+// picks takes 1.9 % longer than the best of them in the mean, 31 % at worst. Those
+// products are the linear layer's. The shapes that came with groups and losses (flat,
+// deep, half) have constants set by hand: over 400 drawn products (8 to 16384 rows in up to 128 groups, 1 to 4096
+// of losses, 64 to 4096 columns and terms), each also in every other tile, the pick takes longer than the best by
+// 6 % in the mean (experts forward; 60 % at worst), 7 (input gradient; 36), 7 to 13 (weight gradient; 88) and
+// 15 (z of losses; 149: 40 to 230 rows of some 2000 columns and terms, which deep tiles would take in half the time).
 // A tile's step (128 bytes of k) takes `step` cycles of a CU that its blocks
 // fill and `alone` of a block by itself, its outputs `ends`; parts cost a
 // launch, a round each, and their bytes. With `groups`, of I rows or K terms in all,
@@ -92,7 +97,9 @@ Cut cut_by_model(int dir, int32_t I, int32_t J, int32_t K, int dtype, bool direc
     const Shape& sh = is_deep ? deep : flat_rows ? flat : k == 3 ? half : shapes[dtype == DDP_BF16][direct][k];
     const int32_t rows = flat_rows ? kFlatRows : k == 3 ? 128 : sh.tile;
     // Short sums are a matter of the outputs' bytes, in which two blocks a CU overlap better
-    // than one (64 experts of 256 rows, 2048 x 4096, added to fp32: 950 us against 1070).
+    // than one (64 experts of 256 rows, 2048 x 4096, added to fp32: 950 us against 1070). Of 65 drawn
+    // bf16 products with so short sums the 256 tile was the better one, by 2 to 14 %, in 3, all with
+    // nothing added; in the mean it took 1.7 times as long (fp32 and bf16 outputs alike), 2 where they are added to.
     if (sh.tile == 256 && is_weight(dir) && (groups > 0 || dir >= kRowStats) && steps <= 8) continue;
     int64_t tiles = int64_t(up(I, rows)) * up(J, sh.tile);
     if (sums)
